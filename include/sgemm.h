@@ -255,6 +255,97 @@ int sgemm_f32_colmajor(int transa, int transb, int64_t m, int64_t n, int64_t k, 
                        const float *A, int64_t lda, const float *B, int64_t ldb, float beta,
                        float *C, int64_t ldc, void *stream);
 
+/* ---- Gated feed-forward block -------------------------------------------
+ *
+ * The block of a transformer layer that follows attention:
+ *
+ *     G = X Wg,  U = X Wu,  H = act(G) * U        (elementwise product)
+ *
+ * X is M x K (ldx >= max(1, K)), H, G and U M x F.  The weights are stored
+ * K x F (transw == SGEMM_OP_N, ldw >= max(1, F)) or F x K (SGEMM_OP_T,
+ * ldw >= max(1, K), the layout of a linear layer); both have the same ldw and
+ * may be halves of one allocation.  Everything is float; sums are in float as
+ * in sgemm_f32, and the activation is applied to the finished float sums. */
+typedef enum sgemm_act {
+    SGEMM_ACT_SILU = 0,      /* g / (1 + exp(-g)) */
+    SGEMM_ACT_GELU = 1,      /* g (1 + erf(g / sqrt 2)) / 2 */
+    SGEMM_ACT_GELU_TANH = 2, /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2 */
+    SGEMM_ACT_RELU = 3,      /* max(g, 0) */
+    SGEMM_ACT_SIGMOID = 4,   /* 1 / (1 + exp(-g)) */
+    SGEMM_ACT_COUNT = 5
+} sgemm_act_t;
+
+/* Forward.  G and U are written too when both are given (ldgu >= max(1, F);
+ * a training step keeps them for the backward pass) and skipped when both are
+ * NULL (ldgu is then ignored); one without the other is SGEMM_ERR_ARG.  The
+ * outputs must not overlap the inputs or one another (SGEMM_ERR_ALIAS);
+ * column ranges of one buffer that share its leading dimension and no element
+ * do not count as overlapping.  K == 0: H (and G, U) are set to zero.
+ * Uses the library workspace as sgemm_f32 does, never under graph capture. */
+int sgemm_glu_f32(int act, int transw, int64_t M, int64_t F, int64_t K,
+                  const float *X, int64_t ldx, const float *Wg, const float *Wu, int64_t ldw,
+                  float *H, int64_t ldh, float *G, float *U, int64_t ldgu, void *stream);
+
+/* Backward, from the gradient dH (M x F) and the G and U that the forward
+ * pass left:
+ *
+ *     dG = dH * U * act'(G),      dU = dH * act(G)
+ *     dX = dG Wg^T + dU Wu^T                               (M x K)
+ *     dWg = X^T dG + beta dWg,    dWu = X^T dU + beta dWu  (stored as Wg, Wu)
+ *
+ * dG and dU (M x F, lddgu) are always written: callers that do not need them
+ * pass scratch, or G and U themselves (or dH, with lddgu == lddh): each of dG
+ * and dU may be exactly one of G, U and dH with an equal leading dimension,
+ * which then no longer hold the forward values.  Any other overlap of an
+ * output with an input or another output is SGEMM_ERR_ALIAS.
+ * dX == NULL skips dX; dWg == dWu == NULL skips both (one alone is
+ * SGEMM_ERR_ARG).  beta == 0: dWg and dWu are not read; beta == 1 accumulates
+ * over micro-batches.  M == 0 leaves dW = beta dW; F == 0 gives dX = 0.
+ * act'(0) = 0 for relu.  Where dG, dU adjoin as [dG | dU] in one buffer
+ * (dU == dG + F, lddgu >= 2 F) and so do the weights, or the weight
+ * gradients, a pair of products runs as one.  Nothing is atomic: the result
+ * of a call is the same from run to run.  Wg and Wu (X) are only read, and
+ * may be NULL, when dX (dWg) is skipped. */
+int sgemm_glu_backward_f32(int act, int transw, int64_t M, int64_t F, int64_t K,
+                           const float *X, int64_t ldx, const float *Wg, const float *Wu,
+                           int64_t ldw, const float *G, const float *U, int64_t ldgu,
+                           const float *dH, int64_t lddh, float *dG, float *dU, int64_t lddgu,
+                           float *dX, int64_t lddx, float *dWg, float *dWu, int64_t lddw,
+                           float beta, void *stream);
+
+/* ---- Products with 4-bit weights ----------------------------------------
+ *
+ *     Y[m, n] = sum_g s[n, g] sum_{k in group g} X[m, k] (q[n, k] - z[n, g])
+ *
+ * Wq holds N rows of ldw BYTES (ldw >= max(1, (K + 1) / 2)): byte j of row n is
+ * q[n, 2j] in its low half and q[n, 2j + 1] in its high half, unsigned; with K
+ * odd the last high half is ignored.  Groups are runs of `group` along K, a
+ * power of two >= 32, the last one shorter when K is not a multiple of it
+ * (group >= K: one scale per row).  S is N x G of type stype, Z (may be NULL:
+ * every z is 8) N x G bytes, each 0..15, G = ceil(K / group) (lds, ldz >=
+ * max(1, G); ldz is ignored without Z).  X (M x K) and Y (M x N) are of type
+ * xtype.  Every pointer has the alignment of its element type.
+ *   The product is exact to float: q - z and the sums' terms are not rounded
+ * to the type of X, each group's sum is held in float and scaled once, and the
+ * result is rounded to xtype at the end.  A group's sum is formed before its
+ * scale is applied, so X has to leave it in float range.
+ *   Y must not overlap an input (SGEMM_ERR_ALIAS).  K == 0: Y is zero.  No
+ * workspace, no synchronisation; every call can be captured. */
+typedef enum sgemm_type { SGEMM_TYPE_F32 = 0, SGEMM_TYPE_F16 = 1, SGEMM_TYPE_BF16 = 2 } sgemm_type_t;
+
+int sgemm_q4(int xtype, int stype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
+             const uint8_t *Wq, int64_t ldw, int64_t group, const void *S, int64_t lds,
+             const uint8_t *Z, int64_t ldz, void *Y, int64_t ldy, void *stream);
+
+/* The gated feed-forward block with 4-bit weights: H = act(G) * U, where G and
+ * U (kept in float, not stored) are products of the form above with the gate
+ * weights (Wg, Sg, Zg) and the up weights (Wu, Su, Zu), both F x K and of the
+ * same strides and group.  Zg and Zu are both given or both NULL. */
+int sgemm_q4_glu(int act, int xtype, int stype, int64_t M, int64_t F, int64_t K, const void *X,
+                 int64_t ldx, const uint8_t *Wg, const uint8_t *Wu, int64_t ldw, int64_t group,
+                 const void *Sg, const void *Su, int64_t lds, const uint8_t *Zg, const uint8_t *Zu,
+                 int64_t ldz, void *H, int64_t ldh, void *stream);
+
 /* Device-to-device copy dst[i] = src[i], 0 <= i < n, with a grid-stride loop:
  * the HBM bandwidth probe of amittech.dev, "7.3 Bandwidths and peak rate -
  * exercises", exercise 2 (it moves 2 * n * 4 bytes).  dst and src are device

@@ -40,12 +40,16 @@ EXPORTS = ["sgemm_f32", "sgemm_f32_variant", "sgemm_copy_f32", "sgemm_copy_f32_l
            "sgemm_status_string", "sgemm_variant_name", "sgemm_auto_variant",
            "sgemm_last_hip_error", "sgemm_abi_version", "sgemm_probe_valu_f32",
            "sgemm_probe_mfma_f32", "sgemm_f32_ex", "sgemm_f32_colmajor", "sgemm_f32_ex_split",
-           "sgemm_split_plan", "sgemm_plan_config", "sgemm_f32_ex_split_noalloc"]
+           "sgemm_split_plan", "sgemm_plan_config", "sgemm_f32_ex_split_noalloc",
+           "sgemm_glu_f32", "sgemm_glu_backward_f32", "sgemm_q4", "sgemm_q4_glu"]
 
 MAX_SPLITS = 64
 STATIC_SCRATCH_BYTES = 64 * 1024 * 1024  # SGEMM_STATIC_SCRATCH_BYTES
 
 OP_N, OP_T = 0, 1
+
+# sgemm_act_t
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}
 
 
 class SgemmError(RuntimeError):
@@ -91,6 +95,18 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.sgemm_plan_config.argtypes = [cint, cint, i64, i64, i64, vp, i64, vp, i64, ip, ip, ip, ip,
                                       ip, ctypes.POINTER(i64)]
     lib.sgemm_plan_config.restype = cint
+    lib.sgemm_glu_f32.argtypes = [cint, cint, i64, i64, i64, vp, i64, vp, vp, i64, vp, i64, vp, vp,
+                                  i64, vp]
+    lib.sgemm_glu_f32.restype = cint
+    lib.sgemm_glu_backward_f32.argtypes = [cint, cint, i64, i64, i64, vp, i64, vp, vp, i64, vp, vp,
+                                           i64, vp, i64, vp, vp, i64, vp, i64, vp, vp, i64, f32, vp]
+    lib.sgemm_glu_backward_f32.restype = cint
+    lib.sgemm_q4.argtypes = [cint, cint, i64, i64, i64, vp, i64, vp, i64, i64, vp, i64, vp, i64,
+                             vp, i64, vp]
+    lib.sgemm_q4.restype = cint
+    lib.sgemm_q4_glu.argtypes = [cint, cint, cint, i64, i64, i64, vp, i64, vp, vp, i64, i64, vp, vp,
+                                 i64, vp, vp, i64, vp, i64, vp]
+    lib.sgemm_q4_glu.restype = cint
     lib.sgemm_copy_f32.argtypes = [vp, vp, i64, vp]
     lib.sgemm_copy_f32.restype = cint
     lib.sgemm_copy_f32_launch.argtypes = [vp, vp, i64, cint, i64, vp]
@@ -271,6 +287,206 @@ def sgemm_colmajor(A, B, out, transa=False, transb=False, alpha=1.0, beta=0.0):
     if st != 0:
         raise SgemmError(st, "sgemm_f32_colmajor")
     return out
+
+
+def _act_id(act) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"unknown activation {act!r}; one of {sorted(ACTIVATIONS)}")
+    return ACTIVATIONS[act]
+
+
+def _rows(t, name, shape=None, dtypes=None):
+    """Leading dimension of a 2-D row-major GPU tensor, checked."""
+    import torch
+    dtypes = dtypes or (torch.float32,)
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        raise TypeError(f"{name} must be a tensor of {' or '.join(str(d) for d in dtypes)}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride (row-major)")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} must have a row stride of at least its row length")
+    return max(t.stride(0), t.shape[1], 1) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _pair_ld(a, b, name, shape, dtypes=None):
+    """The leading dimension two tensors share (the C entry points take one)."""
+    la, lb = _rows(a, f"{name}[0]", shape, dtypes), _rows(b, f"{name}[1]", shape, dtypes)
+    if la != lb:
+        raise ValueError(f"{name}: the two tensors must have the same row stride ({la} and {lb})")
+    return la
+
+
+def _call(fn, where, device, others, *args):
+    """Call an entry point on the device and current stream of its tensors."""
+    import torch
+    for t in others:
+        if t is not None and t.device != device:
+            raise ValueError(f"{where}: tensors on {t.device} and {device}")
+    if device.index is not None and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):  # the default stream is the current device's
+            st = fn(*args, _stream_handle(device))
+    else:
+        st = fn(*args, _stream_handle(device))
+    if st != 0:
+        raise SgemmError(st, where)
+
+
+def _halves(rows, cols, like):
+    """Two rows x cols float32 tensors, the column halves of one buffer."""
+    import torch
+    buf = torch.empty((rows, 2 * cols), dtype=torch.float32, device=like.device)
+    return buf[:, :cols], buf[:, cols:]
+
+
+def glu(X, Wg, Wu, act="silu", transw=False, out=None, save=False):
+    """The gated feed-forward block H = act(X Wg) * (X Wu), float32, on the
+    current stream.  X is M x K; Wg and Wu are K x F, or F x K with ``transw``
+    (the layout of a linear layer), with the same row stride.  ``act``: silu,
+    gelu, gelu_tanh, relu or sigmoid.  Returns H (M x F, ``out`` when given);
+    with ``save`` true (H, G, U), with G = X Wg and U = X Wu, which
+    glu_backward takes.  ``save`` may also be the pair (G, U) to write."""
+    import torch
+    a = _act_id(act)
+    ldx = _rows(X, "X")
+    M, K = X.shape
+    F = Wg.shape[0 if transw else 1] if isinstance(Wg, torch.Tensor) and Wg.dim() == 2 else 0
+    ldw = _pair_ld(Wg, Wu, "weights", (F, K) if transw else (K, F))
+    H = torch.empty((M, F), dtype=torch.float32, device=X.device) if out is None else out
+    ldh = _rows(H, "out", (M, F))
+    G = U = None
+    ldgu = 1
+    if isinstance(save, (tuple, list)):
+        G, U = save
+    elif save:
+        G, U = _halves(M, F, X)
+    if G is not None:
+        ldgu = _pair_ld(G, U, "save", (M, F))
+    null = G is None or M == 0 or F == 0
+    _call(load().sgemm_glu_f32, "sgemm_glu_f32", X.device, (Wg, Wu, H, G, U), a, int(transw), M, F, K,
+          X.data_ptr(), ldx, Wg.data_ptr(), Wu.data_ptr(), ldw, H.data_ptr(), ldh,
+          None if null else G.data_ptr(), None if null else U.data_ptr(), ldgu)
+    return H if G is None else (H, G, U)
+
+
+def glu_backward(dH, X, Wg, Wu, G, U, act="silu", transw=False, need_dx=True, need_dw=True,
+                 dX=None, dW=None, beta=0.0, inplace=False):
+    """Gradients of glu: from dH (M x F) and the G and U of the forward pass,
+    (dX, dWg, dWu), None for those not asked for (``need_dx``, ``need_dw``).
+    ``dX`` and ``dW`` = (dWg, dWu) may be supplied; with ``beta`` the weight
+    gradients are added to beta times what dW holds.  ``inplace`` overwrites
+    G and U with dG and dU instead of allocating M x 2F floats for them."""
+    import torch
+    a = _act_id(act)
+    ldx = _rows(X, "X")
+    M, K = X.shape
+    F = Wg.shape[0 if transw else 1] if isinstance(Wg, torch.Tensor) and Wg.dim() == 2 else 0
+    wshape = (F, K) if transw else (K, F)
+    ldw = _pair_ld(Wg, Wu, "weights", wshape)
+    ldgu = _pair_ld(G, U, "G, U", (M, F))
+    lddh = _rows(dH, "dH", (M, F))
+    dG, dU = (G, U) if inplace else _halves(M, F, X)
+    lddgu = _pair_ld(dG, dU, "dG, dU", (M, F))
+    lddx = lddw = 1
+    if need_dx:
+        dX = torch.empty((M, K), dtype=torch.float32, device=X.device) if dX is None else dX
+        lddx = _rows(dX, "dX", (M, K))
+    else:
+        dX = None
+    dWg = dWu = None
+    if need_dw:
+        if dW is None:
+            if beta != 0:
+                raise ValueError("beta != 0 needs dW")
+            if transw:
+                buf = torch.empty((2 * F, K), dtype=torch.float32, device=X.device)
+                dW = buf[:F], buf[F:]
+            else:
+                dW = _halves(K, F, X)
+        dWg, dWu = dW
+        lddw = _pair_ld(dWg, dWu, "dW", wshape)
+    # Empty tensors have no address; the entry point takes null for "skip".
+    x_null, w_null = dX is None or dX.numel() == 0, dWg is None or dWg.numel() == 0
+    _call(load().sgemm_glu_backward_f32, "sgemm_glu_backward_f32", X.device,
+          (Wg, Wu, G, U, dH, dX, dWg, dWu), a, int(transw), M, F, K, X.data_ptr(), ldx,
+          Wg.data_ptr(), Wu.data_ptr(), ldw, G.data_ptr(), U.data_ptr(), ldgu, dH.data_ptr(), lddh,
+          dG.data_ptr(), dU.data_ptr(), lddgu, None if x_null else dX.data_ptr(), lddx,
+          None if w_null else dWg.data_ptr(), None if w_null else dWu.data_ptr(), lddw, beta)
+    return dX, dWg, dWu
+
+
+def _float_types():
+    import torch
+    return {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _q4_weight(w, scales, zeros, N, K, group, name):
+    """Strides of one packed weight (bytes, scales, zero points), checked."""
+    import torch
+    groups = -(-K // group)
+    ldw = _rows(w, f"{name} weights", (N, (K + 1) // 2), (torch.uint8,))
+    lds = _rows(scales, f"{name} scales", (N, groups), tuple(_float_types()))
+    ldz = _rows(zeros, f"{name} zeros", (N, groups), (torch.uint8,)) if zeros is not None else 1
+    return ldw, lds, ldz
+
+
+def _q4_group(group) -> int:
+    if group < 32 or group & (group - 1):
+        raise ValueError("group must be a power of two, 32 or more")
+    return int(group)
+
+
+def q4_matmul(X, w, scales, zeros=None, group=128, out=None):
+    """Y[m, n] = sum_k X[m, k] scales[n, k // group] (q[n, k] - zeros[n, k // group])
+    on the current stream, with 4-bit q packed two to a byte along K, low half
+    first (``w``: uint8, N x ceil(K / 2)).  X is M x K float32, float16 or
+    bfloat16, and so is Y; ``scales`` is N x ceil(K / group) of any of these
+    types, ``zeros`` uint8 of that shape (None: 8).  ``group`` is a power of
+    two, 32 or more.  Sums are kept in float32 and rounded once."""
+    import torch
+    types, group = _float_types(), _q4_group(group)
+    ldx = _rows(X, "X", None, tuple(types))
+    M, K = X.shape
+    N = w.shape[0]
+    ldw, lds, ldz = _q4_weight(w, scales, zeros, N, K, group, "q4")
+    Y = torch.empty((M, N), dtype=X.dtype, device=X.device) if out is None else out
+    ldy = _rows(Y, "out", (M, N), (X.dtype,))
+    _call(load().sgemm_q4, "sgemm_q4", X.device, (w, scales, zeros, Y), types[X.dtype],
+          types[scales.dtype], M, N, K, X.data_ptr(), ldx, w.data_ptr(), ldw, group,
+          scales.data_ptr(), lds, zeros.data_ptr() if zeros is not None else None, ldz, Y.data_ptr(),
+          ldy)
+    return Y
+
+
+def q4_glu(X, gate_w, gate_scales, up_w, up_scales, gate_zeros=None, up_zeros=None, group=128,
+           act="silu", out=None):
+    """The gated feed-forward block with 4-bit weights, H = act(G) * U, where G
+    and U are q4_matmul's products of X with the gate and the up weights (the
+    same shapes, types and row strides); G and U stay in float32."""
+    import torch
+    a, types, group = _act_id(act), _float_types(), _q4_group(group)
+    ldx = _rows(X, "X", None, tuple(types))
+    M, K = X.shape
+    F = gate_w.shape[0]
+    ld = _q4_weight(gate_w, gate_scales, gate_zeros, F, K, group, "gate")
+    if _q4_weight(up_w, up_scales, up_zeros, F, K, group, "up") != ld:
+        raise ValueError("gate and up weights must have the same row strides")
+    if gate_scales.dtype != up_scales.dtype:
+        raise TypeError("gate and up scales must have the same type")
+    H = torch.empty((M, F), dtype=X.dtype, device=X.device) if out is None else out
+    ldh = _rows(H, "out", (M, F), (X.dtype,))
+    _call(load().sgemm_q4_glu, "sgemm_q4_glu", X.device,
+          (gate_w, gate_scales, up_w, up_scales, gate_zeros, up_zeros, H), a, types[X.dtype],
+          types[gate_scales.dtype], M, F, K, X.data_ptr(), ldx, gate_w.data_ptr(), up_w.data_ptr(),
+          ld[0], group, gate_scales.data_ptr(), up_scales.data_ptr(), ld[1],
+          gate_zeros.data_ptr() if gate_zeros is not None else None,
+          up_zeros.data_ptr() if up_zeros is not None else None, ld[2], H.data_ptr(), ldh)
+    return H
 
 
 def copy_f32(dst, src):

@@ -1,0 +1,67 @@
+// Activations of the gated feed-forward block and their derivatives, in
+// float.  Written so that both tails keep their relative accuracy: the
+// logistic form for silu and tanh-gelu (0.5 (1 + tanh v) = 1 / (1 + exp(-2v)))
+// and erfc for gelu (0.5 (1 + erf(g / sqrt 2)) = 0.5 erfc(-g / sqrt 2)),
+// which do not cancel for negative g.
+#pragma once
+#include <hip/hip_runtime.h>
+
+namespace sgemm {
+
+// sgemm_act_t
+enum Act { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2, ACT_RELU = 3, ACT_SIGMOID = 4 };
+constexpr int kActCount = 5;
+
+__device__ __forceinline__ float logistic(float v) { return 1.0f / (1.0f + expf(-v)); }
+
+// 2 c (g + 0.044715 g^3), c = sqrt(2 / pi): twice the argument of tanh.
+__device__ __forceinline__ float gelu_tanh_arg2(float g) {
+    return 1.5957691216057308f * g * fmaf(0.044715f * g, g, 1.0f);
+}
+
+__device__ __forceinline__ float act_value(int act, float g) {
+    switch (act) {
+        case ACT_SILU: return g * logistic(g);
+        case ACT_GELU: return 0.5f * g * erfcf(-0.70710678118654752f * g);
+        case ACT_GELU_TANH: return g * logistic(gelu_tanh_arg2(g));
+        case ACT_RELU: return g <= 0.0f ? 0.0f : g;  // NaN stays NaN
+        default: return logistic(g);
+    }
+}
+
+// act(g) and act'(g).  relu'(0) = 0.
+__device__ __forceinline__ void act_grad(int act, float g, float* a, float* da) {
+    switch (act) {
+        case ACT_SILU: {
+            const float s = logistic(g);
+            *a = g * s;
+            *da = s * fmaf(g, 1.0f - s, 1.0f);
+            return;
+        }
+        case ACT_GELU: {
+            const float c = 0.5f * erfcf(-0.70710678118654752f * g);
+            *a = g * c;
+            *da = fmaf(g * 0.39894228040143268f, expf(-0.5f * g * g), c);
+            return;
+        }
+        case ACT_GELU_TANH: {
+            const float s = logistic(gelu_tanh_arg2(g));
+            *a = g * s;
+            // d/dg of 2 c (g + 0.044715 g^3) = 2 c (1 + 0.134145 g^2)
+            *da = s * fmaf(g * (1.0f - s), 1.5957691216057308f * fmaf(0.134145f * g, g, 1.0f), 1.0f);
+            return;
+        }
+        case ACT_RELU:
+            *a = g <= 0.0f ? 0.0f : g;
+            *da = g > 0.0f ? 1.0f : 0.0f;
+            return;
+        default: {
+            const float s = logistic(g);
+            *a = s;
+            *da = s * (1.0f - s);
+            return;
+        }
+    }
+}
+
+}  // namespace sgemm

@@ -88,6 +88,115 @@ int choose_auto(const GemmArgs& g) {
     return sgemm::k4_supports(g) ? SGEMM_K4_MFMA : SGEMM_K3_REGTILE_DB;
 }
 
+// A rows x cols row-major view of elements of `size` bytes.
+struct View {
+    const void* p;
+    int64_t rows, cols, ld, size;
+};
+
+// Whether two views share an element.  Views of one leading dimension whose
+// byte ranges cross may still be disjoint column ranges of one buffer.
+bool share(const View& a, const View& b) {
+    if (a.rows == 0 || a.cols == 0 || b.rows == 0 || b.cols == 0 || !a.p || !b.p) return false;
+    // 128-bit extents: rows * ld may pass 64 bits at the limits above.
+    typedef unsigned __int128 wide;
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+    const wide ahi = a0 + (wide(a.rows - 1) * wide(a.ld) + wide(a.cols)) * wide(a.size);
+    const wide bhi = b0 + (wide(b.rows - 1) * wide(b.ld) + wide(b.cols)) * wide(b.size);
+    if (!(a0 < bhi && b0 < ahi)) return false;
+    const int64_t pitch = a.ld * a.size;
+    if (pitch != b.ld * b.size) return true;
+    // Where b's columns start in a's row pitch: disjoint if they lie wholly
+    // in the gap after a's columns.
+    const int64_t diff = int64_t(b0 - a0), r = ((diff % pitch) + pitch) % pitch;
+    return r < a.cols * a.size || r + b.cols * b.size > pitch;
+}
+
+bool same_view(const View& a, const View& b) { return a.p == b.p && a.ld == b.ld; }
+
+// No output shares an element with an input or with another output, except
+// that each of the first n_place_out outputs may be exactly one of the first
+// n_place inputs.
+template <int NI, int NO>
+int check_alias(const View (&in)[NI], const View (&out)[NO], int n_place = 0, int n_place_out = 0) {
+    for (int o = 0; o < NO; o++) {
+        for (int i = 0; i < NI; i++) {
+            if (o < n_place_out && i < n_place && same_view(out[o], in[i])) continue;
+            if (share(out[o], in[i])) return SGEMM_ERR_ALIAS;
+        }
+        for (int o2 = 0; o2 < o; o2++)
+            if (share(out[o], out[o2])) return SGEMM_ERR_ALIAS;
+    }
+    return SGEMM_OK;
+}
+
+constexpr int64_t kDimLimit = int64_t(1) << 40;
+
+bool dims_ok(int64_t a, int64_t b, int64_t c) {
+    return a >= 0 && b >= 0 && c >= 0 && a <= kDimLimit && b <= kDimLimit && c <= kDimLimit;
+}
+
+bool ld_ok(int64_t ld, int64_t cols) { return ld >= (cols > 1 ? cols : 1) && ld <= kDimLimit; }
+
+int validate_glu(int act, int transw, int64_t M, int64_t F, int64_t K, int64_t ldx, int64_t ldw) {
+    if (act < 0 || act >= SGEMM_ACT_COUNT) return SGEMM_ERR_ARG;
+    if (transw != SGEMM_OP_N && transw != SGEMM_OP_T) return SGEMM_ERR_ARG;
+    if (!dims_ok(M, F, K)) return SGEMM_ERR_DIM;
+    if (!ld_ok(ldx, K) || !ld_ok(ldw, transw ? K : F)) return SGEMM_ERR_LD;
+    return SGEMM_OK;
+}
+
+// The common body of the 4-bit entry points; act < 0: the plain product.
+int run_q4(int act, int xtype, int stype, int64_t M, int64_t N, int64_t K, const void* X,
+           int64_t ldx, const uint8_t* const (&W)[2], int64_t ldw, int64_t group,
+           const void* const (&S)[2], int64_t lds, const uint8_t* const (&Z)[2], int64_t ldz,
+           void* Y, int64_t ldy, void* stream) {
+    const int nw = act < 0 ? 1 : 2;
+    if (xtype < 0 || xtype > SGEMM_TYPE_BF16 || stype < 0 || stype > SGEMM_TYPE_BF16) return SGEMM_ERR_ARG;
+    if (group < 32 || (group & (group - 1)) != 0) return SGEMM_ERR_ARG;
+    if (nw == 2 && (Z[0] == nullptr) != (Z[1] == nullptr)) return SGEMM_ERR_ARG;
+    if (!dims_ok(M, N, K)) return SGEMM_ERR_DIM;
+    const int64_t groups = K / group + (K % group != 0), bytes = (K + 1) / 2;
+    if (!ld_ok(ldx, K) || !ld_ok(ldw, bytes) || !ld_ok(lds, groups) || !ld_ok(ldy, N)) return SGEMM_ERR_LD;
+    if (Z[0] && !ld_ok(ldz, groups)) return SGEMM_ERR_LD;
+    if (M == 0 || N == 0) return SGEMM_OK;
+    if (Y == nullptr) return SGEMM_ERR_NULLPTR;
+    const int64_t xs = xtype == SGEMM_TYPE_F32 ? 4 : 2, ss = stype == SGEMM_TYPE_F32 ? 4 : 2;
+    if (K > 0) {
+        if (X == nullptr) return SGEMM_ERR_NULLPTR;
+        for (int i = 0; i < nw; i++)
+            if (W[i] == nullptr || S[i] == nullptr) return SGEMM_ERR_NULLPTR;
+        const View in[] = {{X, M, K, ldx, xs},         {W[0], N, bytes, ldw, 1}, {S[0], N, groups, lds, ss},
+                           {Z[0], N, groups, ldz, 1}, {W[1], N, bytes, ldw, 1}, {S[1], N, groups, lds, ss},
+                           {Z[1], N, groups, ldz, 1}};
+        const View out[] = {{Y, M, N, ldy, xs}};
+        const int a = check_alias(in, out);
+        if (a != SGEMM_OK) return a;
+    }
+    sgemm::Q4Args g{};
+    g.act = act;
+    g.xtype = xtype;
+    g.stype = stype;
+    g.shift = 0;
+    while ((int64_t(1) << g.shift) < group) g.shift++;
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.X = X;
+    g.ldx = ldx;
+    g.ldw = ldw;
+    g.lds = lds;
+    g.ldz = ldz;
+    g.Y = Y;
+    g.ldy = ldy;
+    for (int i = 0; i < 2; i++) {
+        g.W[i] = W[i];
+        g.S[i] = S[i];
+        g.Z[i] = Z[i];
+    }
+    return launch_status(sgemm::launch_q4(g, static_cast<hipStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -196,6 +305,71 @@ int sgemm_f32_colmajor(int transa, int transb, int64_t m, int64_t n, int64_t k, 
     // C = op(A) op(B) (column-major) is C^T = op(B)^T op(A)^T (row-major):
     // the operands swap places and keep their transpose flags.
     return sgemm_f32_ex(transb, transa, n, m, k, alpha, B, ldb, A, lda, beta, C, ldc, stream);
+}
+
+int sgemm_glu_f32(int act, int transw, int64_t M, int64_t F, int64_t K, const float* X,
+                  int64_t ldx, const float* Wg, const float* Wu, int64_t ldw, float* H, int64_t ldh,
+                  float* G, float* U, int64_t ldgu, void* stream) {
+    int v = validate_glu(act, transw, M, F, K, ldx, ldw);
+    if (v != SGEMM_OK) return v;
+    if ((G == nullptr) != (U == nullptr)) return SGEMM_ERR_ARG;
+    if (!ld_ok(ldh, F) || (G && !ld_ok(ldgu, F))) return SGEMM_ERR_LD;
+    if (M == 0 || F == 0) return SGEMM_OK;
+    if (H == nullptr || (K > 0 && (!X || !Wg || !Wu))) return SGEMM_ERR_NULLPTR;
+    const int64_t wr = transw ? F : K, wc = transw ? K : F;
+    const View in[] = {{X, M, K, ldx, 4}, {Wg, wr, wc, ldw, 4}, {Wu, wr, wc, ldw, 4}};
+    const View out[] = {{H, M, F, ldh, 4}, {G, M, F, ldgu, 4}, {U, M, F, ldgu, 4}};
+    if ((v = check_alias(in, out)) != SGEMM_OK) return v;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (K == 0) {
+        hipError_t e = sgemm::launch_zero(H, M, F, ldh, s);
+        if (e == hipSuccess && G) e = sgemm::launch_zero(G, M, F, ldgu, s);
+        if (e == hipSuccess && U) e = sgemm::launch_zero(U, M, F, ldgu, s);
+        return launch_status(e);
+    }
+    const sgemm::GluArgs g{act, transw == SGEMM_OP_T, M, F, K, X, ldx, Wg, Wu, ldw, H, ldh, G, U, ldgu};
+    return launch_status(sgemm::launch_glu_general(g, s));
+}
+
+int sgemm_glu_backward_f32(int act, int transw, int64_t M, int64_t F, int64_t K, const float* X,
+                           int64_t ldx, const float* Wg, const float* Wu, int64_t ldw,
+                           const float* G, const float* U, int64_t ldgu, const float* dH,
+                           int64_t lddh, float* dG, float* dU, int64_t lddgu, float* dX,
+                           int64_t lddx, float* dWg, float* dWu, int64_t lddw, float beta,
+                           void* stream) {
+    int v = validate_glu(act, transw, M, F, K, ldx, ldw);
+    if (v != SGEMM_OK) return v;
+    if ((dWg == nullptr) != (dWu == nullptr)) return SGEMM_ERR_ARG;
+    const int64_t wr = transw ? F : K, wc = transw ? K : F;
+    if (!ld_ok(ldgu, F) || !ld_ok(lddh, F) || !ld_ok(lddgu, F)) return SGEMM_ERR_LD;
+    if ((dX && !ld_ok(lddx, K)) || (dWg && !ld_ok(lddw, wc))) return SGEMM_ERR_LD;
+    const bool some = M > 0 && F > 0;
+    if (some && (!G || !U || !dH || !dG || !dU)) return SGEMM_ERR_NULLPTR;
+    if (some && K > 0 && ((dX && (!Wg || !Wu)) || (dWg && !X))) return SGEMM_ERR_NULLPTR;
+    const View in[] = {{G, M, F, ldgu, 4}, {U, M, F, ldgu, 4},   {dH, M, F, lddh, 4},
+                       {X, M, K, ldx, 4},  {Wg, wr, wc, ldw, 4}, {Wu, wr, wc, ldw, 4}};
+    const View out[] = {{dG, M, F, lddgu, 4}, {dU, M, F, lddgu, 4},    {dX, M, K, lddx, 4},
+                        {dWg, wr, wc, lddw, 4}, {dWu, wr, wc, lddw, 4}};
+    if ((v = check_alias(in, out, 3, 2)) != SGEMM_OK) return v;
+    const sgemm::GluGradArgs g{act, transw == SGEMM_OP_T, M,  F,  K,     X,  ldx,  Wg,  Wu,  ldw,  G,    U,
+                               ldgu, dH, lddh, dG, dU, lddgu, dX, lddx, dWg, dWu, lddw, beta};
+    return launch_status(sgemm::launch_glu_backward(g, static_cast<hipStream_t>(stream)));
+}
+
+int sgemm_q4(int xtype, int stype, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
+             const uint8_t* Wq, int64_t ldw, int64_t group, const void* S, int64_t lds,
+             const uint8_t* Z, int64_t ldz, void* Y, int64_t ldy, void* stream) {
+    return run_q4(-1, xtype, stype, M, N, K, X, ldx, {Wq, nullptr}, ldw, group, {S, nullptr}, lds,
+                  {Z, nullptr}, ldz, Y, ldy, stream);
+}
+
+int sgemm_q4_glu(int act, int xtype, int stype, int64_t M, int64_t F, int64_t K, const void* X,
+                 int64_t ldx, const uint8_t* Wg, const uint8_t* Wu, int64_t ldw, int64_t group,
+                 const void* Sg, const void* Su, int64_t lds, const uint8_t* Zg, const uint8_t* Zu,
+                 int64_t ldz, void* H, int64_t ldh, void* stream) {
+    if (act < 0 || act >= SGEMM_ACT_COUNT) return SGEMM_ERR_ARG;
+    return run_q4(act, xtype, stype, M, F, K, X, ldx, {Wg, Wu}, ldw, group, {Sg, Su}, lds, {Zg, Zu},
+                  ldz, H, ldh, stream);
 }
 
 int sgemm_auto_variant(int64_t M, int64_t N, int64_t K, const float* A, int64_t lda,

@@ -185,4 +185,68 @@ hipError_t launch_probe_valu(float* out, int64_t iters, float x, float y, int64_
 hipError_t launch_probe_mfma(float* out, const float* a_vals, const float* b_vals, int64_t iters,
                              int64_t blocks, hipStream_t s);
 
+// Gated feed-forward block (glu.hip): H = act(X Wg) * (X Wu), X M x K, the
+// weights K x F (F x K with transw); G = X Wg and U = X Wu are stored too
+// when G is not null.
+struct GluArgs {
+    int act;
+    bool transw;
+    int64_t M, F, K;
+    const float* X;
+    int64_t ldx;
+    const float *Wg, *Wu;
+    int64_t ldw;
+    float* H;
+    int64_t ldh;
+    float *G, *U;
+    int64_t ldgu;
+};
+// General kernel (64-bit offsets, any strides).
+hipError_t launch_glu_general(const GluArgs& g, hipStream_t s);
+// Backward pass: dG, dU (M x F), then dX (M x K) unless null, and dWg, dWu
+// (as the weights are stored; += when beta is 1, in general beta dW + ...)
+// unless null.
+struct GluGradArgs {
+    int act;
+    bool transw;
+    int64_t M, F, K;
+    const float* X;
+    int64_t ldx;
+    const float *Wg, *Wu;
+    int64_t ldw;
+    const float *G, *U;
+    int64_t ldgu;
+    const float* dH;
+    int64_t lddh;
+    float *dG, *dU;
+    int64_t lddgu;
+    float* dX;
+    int64_t lddx;
+    float *dWg, *dWu;
+    int64_t lddw;
+    float beta;
+};
+hipError_t launch_glu_backward(const GluGradArgs& g, hipStream_t s);
+
+// Products with 4-bit weights (q4.hip).  act < 0: Y = X W0^T; act >= 0: the
+// gated form Y = act(X W0^T) * (X W1^T).  W[i] packed N rows of ldw bytes,
+// S[i] N x groups scales, Z[i] N x groups zero points (null: 8), groups of
+// 2^shift along K.
+enum ElemType { T_F32 = 0, T_F16 = 1, T_BF16 = 2 };
+struct Q4Args {
+    int act, xtype, stype, shift;
+    int64_t M, N, K;
+    const void* X;
+    int64_t ldx;
+    const uint8_t* W[2];
+    int64_t ldw;
+    const void* S[2];
+    int64_t lds;
+    const uint8_t* Z[2];
+    int64_t ldz;
+    void* Y;
+    int64_t ldy;
+};
+hipError_t launch_q4(const Q4Args& g, hipStream_t s);
+
 }  // namespace sgemm

@@ -83,8 +83,12 @@ def test_every_pair_of_types(M, x, st):
 
 @pytest.mark.parametrize("M", [1, 4, 16, 48, 160])
 def test_every_float_bit_counts(M):
-    """Rows with one 24-bit value each: the product is that value times q - z,
-    exact in float (24 bits times an integer below 16, rounded once)."""
+    """Rows with one 24-bit value each: the product is that value times q - z.
+    The value is the sum of three parts of 8 bits; the first part's product
+    (12 bits) is exact, adding each of the other two rounds once, and scaling
+    by 1 and adding zeros is exact: two roundings, each at most half a unit,
+    u = 2^-24 of the value then held, which is at most |v (q - z)| (1 + u).
+    A part left out would be off by 2^-8 or 2^-16 of it."""
     gen = torch.Generator().manual_seed(M)
     N, K = 64, 192
     X = torch.zeros((M, K))
@@ -95,7 +99,7 @@ def test_every_float_bit_counts(M):
     s.fill_(1.0)
     Y = rs.q4_matmul(X.cuda(), w, s, z, group=32)
     ref = X.double() @ q4_int(w, z, K, 32).t()
-    assert torch.equal(Y.cpu(), ref.float())
+    assert_within(Y, ref, 2 * U * (1 + U) * ref.abs())
 
 
 @pytest.mark.parametrize("x", TYPES)
@@ -111,6 +115,20 @@ def test_integers_are_exact(M, x):
     Y = rs.q4_matmul(X.cuda(), w, s.float(), z, group=group)
     ref, _ = q4_64(X, w, s, z, group)
     assert torch.equal(Y.cpu(), ref.to(TYPES[x]))
+
+
+@pytest.mark.parametrize("M", [1, 20, 140])
+def test_half_precision_subnormals(M):
+    """float16 X below its normal range counts in full: integers times 2^-24,
+    its smallest step, with scales that bring the sums back."""
+    gen = torch.Generator().manual_seed(M)
+    N, K, group = 64, 256, 64
+    X = (torch.randint(-40, 41, (M, K), generator=gen).double() * 2.0 ** -24).to(torch.float16)
+    w, s, z = q4_make(gen, N, K, group, torch.float32, True)
+    s.fill_(2.0 ** 20)
+    Y = rs.q4_matmul(X.cuda(), w, s, z, group=group)
+    ref, _ = q4_64(X, w, s, z, group)
+    assert torch.equal(Y.cpu(), ref.to(torch.float16))
 
 
 @pytest.mark.parametrize("M", [1, 5, 40, 150])

@@ -9,6 +9,8 @@ from __future__ import annotations
 import ctypes
 import os
 
+import torch
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(HERE, "libsgemm.so")
 _lib = None
@@ -50,6 +52,11 @@ OP_N, OP_T = 0, 1
 
 # sgemm_act_t
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}
+
+
+# sgemm_type_t
+_F32 = torch.float32
+_FLOATS = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 
 class SgemmError(RuntimeError):
@@ -289,6 +296,16 @@ def sgemm_colmajor(A, B, out, transa=False, transb=False, alpha=1.0, beta=0.0):
     return out
 
 
+def _raw_stream(dev: int) -> int:
+    """Handle of device dev's current stream."""
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+if not hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the public way, 2 us slower
+    def _raw_stream(dev: int) -> int:  # noqa: F811
+        return torch.cuda.current_stream(dev).cuda_stream
+
+
 def _act_id(act) -> int:
     if act not in ACTIVATIONS:
         raise ValueError(f"unknown activation {act!r}; one of {sorted(ACTIVATIONS)}")
@@ -297,8 +314,20 @@ def _act_id(act) -> int:
 
 def _rows(t, name, shape=None, dtypes=None):
     """Leading dimension of a 2-D row-major GPU tensor, checked."""
-    import torch
-    dtypes = dtypes or (torch.float32,)
+    try:  # the usual case in few steps: these calls take microseconds
+        (rows, cols), (ld, step) = t.shape, t.stride()
+        if (t.is_cuda and (t.dtype in dtypes if dtypes else t.dtype == _F32)
+                and (shape is None or (rows, cols) == shape) and (step == 1 or cols == 1)):
+            if rows > 1 and ld >= cols > 0:
+                return ld
+            if rows == 1 and cols > 0:
+                return cols
+    except (AttributeError, ValueError):
+        pass
+    return _rows_checked(t, name, shape, dtypes or (_F32,))
+
+
+def _rows_checked(t, name, shape, dtypes):
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
         raise TypeError(f"{name} must be a tensor of {' or '.join(str(d) for d in dtypes)}")
     if t.device.type != "cuda":
@@ -322,24 +351,24 @@ def _pair_ld(a, b, name, shape, dtypes=None):
     return la
 
 
-def _call(fn, where, device, others, *args):
-    """Call an entry point on the device and current stream of its tensors."""
-    import torch
+def _call(fn, where, X, others, *args):
+    """Call an entry point on the device of its tensors and that device's
+    current stream."""
+    dev = X.get_device()
     for t in others:
-        if t is not None and t.device != device:
-            raise ValueError(f"{where}: tensors on {t.device} and {device}")
-    if device.index is not None and device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):  # the default stream is the current device's
-            st = fn(*args, _stream_handle(device))
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{where}: tensors on {t.device} and {X.device}")
+    if dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):  # the default stream is the current device's
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
     else:
-        st = fn(*args, _stream_handle(device))
+        st = fn(*args, _raw_stream(dev))
     if st != 0:
         raise SgemmError(st, where)
 
 
 def _halves(rows, cols, like):
     """Two rows x cols float32 tensors, the column halves of one buffer."""
-    import torch
     buf = torch.empty((rows, 2 * cols), dtype=torch.float32, device=like.device)
     return buf[:, :cols], buf[:, cols:]
 
@@ -351,14 +380,15 @@ def glu(X, Wg, Wu, act="silu", transw=False, out=None, save=False):
     gelu, gelu_tanh, relu or sigmoid.  Returns H (M x F, ``out`` when given);
     with ``save`` true (H, G, U), with G = X Wg and U = X Wu, which
     glu_backward takes.  ``save`` may also be the pair (G, U) to write."""
-    import torch
     a = _act_id(act)
     ldx = _rows(X, "X")
     M, K = X.shape
     F = Wg.shape[0 if transw else 1] if isinstance(Wg, torch.Tensor) and Wg.dim() == 2 else 0
     ldw = _pair_ld(Wg, Wu, "weights", (F, K) if transw else (K, F))
-    H = torch.empty((M, F), dtype=torch.float32, device=X.device) if out is None else out
-    ldh = _rows(H, "out", (M, F))
+    if out is None:
+        H, ldh = torch.empty((M, F), dtype=torch.float32, device=X.device), max(F, 1)
+    else:
+        H, ldh = out, _rows(out, "out", (M, F))
     G = U = None
     ldgu = 1
     if isinstance(save, (tuple, list)):
@@ -368,7 +398,7 @@ def glu(X, Wg, Wu, act="silu", transw=False, out=None, save=False):
     if G is not None:
         ldgu = _pair_ld(G, U, "save", (M, F))
     null = G is None or M == 0 or F == 0
-    _call(load().sgemm_glu_f32, "sgemm_glu_f32", X.device, (Wg, Wu, H, G, U), a, int(transw), M, F, K,
+    _call(load().sgemm_glu_f32, "sgemm_glu_f32", X, (Wg, Wu, H, G, U), a, int(transw), M, F, K,
           X.data_ptr(), ldx, Wg.data_ptr(), Wu.data_ptr(), ldw, H.data_ptr(), ldh,
           None if null else G.data_ptr(), None if null else U.data_ptr(), ldgu)
     return H if G is None else (H, G, U)
@@ -381,7 +411,6 @@ def glu_backward(dH, X, Wg, Wu, G, U, act="silu", transw=False, need_dx=True, ne
     ``dX`` and ``dW`` = (dWg, dWu) may be supplied; with ``beta`` the weight
     gradients are added to beta times what dW holds.  ``inplace`` overwrites
     G and U with dG and dU instead of allocating M x 2F floats for them."""
-    import torch
     a = _act_id(act)
     ldx = _rows(X, "X")
     M, K = X.shape
@@ -412,7 +441,7 @@ def glu_backward(dH, X, Wg, Wu, G, U, act="silu", transw=False, need_dx=True, ne
         lddw = _pair_ld(dWg, dWu, "dW", wshape)
     # Empty tensors have no address; the entry point takes null for "skip".
     x_null, w_null = dX is None or dX.numel() == 0, dWg is None or dWg.numel() == 0
-    _call(load().sgemm_glu_backward_f32, "sgemm_glu_backward_f32", X.device,
+    _call(load().sgemm_glu_backward_f32, "sgemm_glu_backward_f32", X,
           (Wg, Wu, G, U, dH, dX, dWg, dWu), a, int(transw), M, F, K, X.data_ptr(), ldx,
           Wg.data_ptr(), Wu.data_ptr(), ldw, G.data_ptr(), U.data_ptr(), ldgu, dH.data_ptr(), lddh,
           dG.data_ptr(), dU.data_ptr(), lddgu, None if x_null else dX.data_ptr(), lddx,
@@ -420,17 +449,11 @@ def glu_backward(dH, X, Wg, Wu, G, U, act="silu", transw=False, need_dx=True, ne
     return dX, dWg, dWu
 
 
-def _float_types():
-    import torch
-    return {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
-
-
 def _q4_weight(w, scales, zeros, N, K, group, name):
     """Strides of one packed weight (bytes, scales, zero points), checked."""
-    import torch
     groups = -(-K // group)
     ldw = _rows(w, f"{name} weights", (N, (K + 1) // 2), (torch.uint8,))
-    lds = _rows(scales, f"{name} scales", (N, groups), tuple(_float_types()))
+    lds = _rows(scales, f"{name} scales", (N, groups), _FLOATS)
     ldz = _rows(zeros, f"{name} zeros", (N, groups), (torch.uint8,)) if zeros is not None else 1
     return ldw, lds, ldz
 
@@ -448,16 +471,17 @@ def q4_matmul(X, w, scales, zeros=None, group=128, out=None):
     bfloat16, and so is Y; ``scales`` is N x ceil(K / group) of any of these
     types, ``zeros`` uint8 of that shape (None: 8).  ``group`` is a power of
     two, 32 or more.  Sums are kept in float32 and rounded once."""
-    import torch
-    types, group = _float_types(), _q4_group(group)
-    ldx = _rows(X, "X", None, tuple(types))
+    group = _q4_group(group)
+    ldx = _rows(X, "X", None, _FLOATS)
     M, K = X.shape
     N = w.shape[0]
     ldw, lds, ldz = _q4_weight(w, scales, zeros, N, K, group, "q4")
-    Y = torch.empty((M, N), dtype=X.dtype, device=X.device) if out is None else out
-    ldy = _rows(Y, "out", (M, N), (X.dtype,))
-    _call(load().sgemm_q4, "sgemm_q4", X.device, (w, scales, zeros, Y), types[X.dtype],
-          types[scales.dtype], M, N, K, X.data_ptr(), ldx, w.data_ptr(), ldw, group,
+    if out is None:
+        Y, ldy = torch.empty((M, N), dtype=X.dtype, device=X.device), max(N, 1)
+    else:
+        Y, ldy = out, _rows(out, "out", (M, N), (X.dtype,))
+    _call(load().sgemm_q4, "sgemm_q4", X, (w, scales, zeros, Y), _FLOATS[X.dtype],
+          _FLOATS[scales.dtype], M, N, K, X.data_ptr(), ldx, w.data_ptr(), ldw, group,
           scales.data_ptr(), lds, zeros.data_ptr() if zeros is not None else None, ldz, Y.data_ptr(),
           ldy)
     return Y
@@ -468,9 +492,8 @@ def q4_glu(X, gate_w, gate_scales, up_w, up_scales, gate_zeros=None, up_zeros=No
     """The gated feed-forward block with 4-bit weights, H = act(G) * U, where G
     and U are q4_matmul's products of X with the gate and the up weights (the
     same shapes, types and row strides); G and U stay in float32."""
-    import torch
-    a, types, group = _act_id(act), _float_types(), _q4_group(group)
-    ldx = _rows(X, "X", None, tuple(types))
+    a, group = _act_id(act), _q4_group(group)
+    ldx = _rows(X, "X", None, _FLOATS)
     M, K = X.shape
     F = gate_w.shape[0]
     ld = _q4_weight(gate_w, gate_scales, gate_zeros, F, K, group, "gate")
@@ -478,11 +501,13 @@ def q4_glu(X, gate_w, gate_scales, up_w, up_scales, gate_zeros=None, up_zeros=No
         raise ValueError("gate and up weights must have the same row strides")
     if gate_scales.dtype != up_scales.dtype:
         raise TypeError("gate and up scales must have the same type")
-    H = torch.empty((M, F), dtype=X.dtype, device=X.device) if out is None else out
-    ldh = _rows(H, "out", (M, F), (X.dtype,))
-    _call(load().sgemm_q4_glu, "sgemm_q4_glu", X.device,
-          (gate_w, gate_scales, up_w, up_scales, gate_zeros, up_zeros, H), a, types[X.dtype],
-          types[gate_scales.dtype], M, F, K, X.data_ptr(), ldx, gate_w.data_ptr(), up_w.data_ptr(),
+    if out is None:
+        H, ldh = torch.empty((M, F), dtype=X.dtype, device=X.device), max(F, 1)
+    else:
+        H, ldh = out, _rows(out, "out", (M, F), (X.dtype,))
+    _call(load().sgemm_q4_glu, "sgemm_q4_glu", X,
+          (gate_w, gate_scales, up_w, up_scales, gate_zeros, up_zeros, H), a, _FLOATS[X.dtype],
+          _FLOATS[gate_scales.dtype], M, F, K, X.data_ptr(), ldx, gate_w.data_ptr(), up_w.data_ptr(),
           ld[0], group, gate_scales.data_ptr(), up_scales.data_ptr(), ld[1],
           gate_zeros.data_ptr() if gate_zeros is not None else None,
           up_zeros.data_ptr() if up_zeros is not None else None, ld[2], H.data_ptr(), ldh)

@@ -27,15 +27,22 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kUnit = 128;      // K per step of a wave: 4 lane groups of 32 weights
-constexpr int kRowsMax = 16;    // rows of X of one q4_rows workgroup
+constexpr int kRowsMax = 8;     // rows of X of one q4_rows workgroup
 
 // bfloat16 parts of X for the matrix cores: 3 for float, 1 for 16-bit types.
 template <int XT> constexpr int parts() { return XT == T_F32 ? 3 : 1; }
 
-__device__ __forceinline__ float to_float(int type, const void* p, int64_t i) {
-    if (type == T_F32) return static_cast<const float*>(p)[i];
-    if (type == T_F16) return float(static_cast<const _Float16*>(p)[i]);
-    return __uint_as_float(uint32_t(static_cast<const uint16_t*>(p)[i]) << 16);
+// An element as its bits, and these as a float.
+__device__ __forceinline__ uint32_t load_raw(int type, const void* p, int64_t i) {
+    if (type == T_F32) return static_cast<const uint32_t*>(p)[i];
+    return static_cast<const uint16_t*>(p)[i];
+}
+__device__ __forceinline__ float raw_to_float(int type, uint32_t v) {
+    const float half = float(__builtin_bit_cast(_Float16, uint16_t(v)));
+    return type == T_F32 ? __uint_as_float(v) : type == T_BF16 ? __uint_as_float(v << 16) : half;
+}
+__device__ __forceinline__ float load_float(int type, const void* p, int64_t i) {
+    return raw_to_float(type, load_raw(type, p, i));
 }
 
 template <int XT>
@@ -52,12 +59,21 @@ __device__ __forceinline__ u32x4 load16(const void* p) {
     return v;
 }
 
-// The 16 packed bytes at byte `off` of a row of `bytes`: zero past its end.
-__device__ __forceinline__ u32x4 load_w(const uint8_t* row, int64_t off, int64_t bytes) {
-    if (off + 16 <= bytes) return load16(row + off);
-    u32x4 v = {0, 0, 0, 0};
-    for (int i = 0; i < 16; i++)
-        if (off + i < bytes) v[i / 4] |= uint32_t(row[off + i]) << (8 * (i % 4));
+// The 16 packed bytes at byte `off` of a row of `bytes` that ends inside
+// them (or before them): bytes past the end repeat the last one; X is zero
+// there.
+__device__ __forceinline__ u32x4 load_w_tail(const uint8_t* row, int off, int bytes) {
+    u32x4 v;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        uint32_t w = 0;
+#pragma unroll 1
+        for (int i = 0; i < 4; i++) {
+            const int at = off + 4 * j + i;
+            w |= uint32_t(row[at < bytes ? at : bytes - 1]) << (8 * i);
+        }
+        v[j] = w;
+    }
     return v;
 }
 
@@ -66,6 +82,14 @@ template <int XT>
 __device__ __forceinline__ uint32_t zero_const(int z) {
     if constexpr (XT == T_F16) return uint32_t(z);
     else return 0x80808080u - uint32_t(z) * 0x01010101u;
+}
+
+// (v & mask) | bits in one operation: the constants in registers, as the
+// instruction takes no literal.
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) {
+    uint32_t r;
+    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(v), "s"(mask), "v"(bits));
+    return r;
 }
 
 // The eight weights q - z of one packed word as the matrix instruction's
@@ -85,8 +109,8 @@ __device__ __forceinline__ u32x4 dequant(uint32_t w, uint32_t zc) {
 #pragma unroll
         for (int h = 0; h < 2; h++) {
             const uint32_t v = w >> (8 * h);
-            const f16x2 a = __builtin_bit_cast(f16x2, (v & 0x000F000Fu) | 0x64006400u);
-            const f16x2 b = __builtin_bit_cast(f16x2, (v & 0x00F000F0u) | 0x64006400u);
+            const f16x2 a = __builtin_bit_cast(f16x2, and_or(v, 0x000F000Fu, 0x64006400u));
+            const f16x2 b = __builtin_bit_cast(f16x2, and_or(v, 0x00F000F0u, 0x64006400u));
             r[2 * h] = __builtin_bit_cast(uint32_t, a + off);
             r[2 * h + 1] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(b, six, off16));
         }
@@ -127,6 +151,52 @@ __device__ __forceinline__ void split3(float x, float (&p)[3]) {
     p[2] = r - p[1];
 }
 
+// Eight consecutive elements of row m of X from column k, zero past K, as
+// loaded, and as the matrix instruction's operand: the three parts of a
+// float, or the elements.
+template <int XT> struct RawX { u32x4 v[XT == T_F32 ? 2 : 1]; };
+
+template <int XT>
+__device__ __forceinline__ void load_x(const Q4Args& g, int64_t m, int k, RawX<XT>& raw) {
+    if constexpr (XT == T_F32) {
+        const uint32_t* xp = static_cast<const uint32_t*>(g.X) + m * g.ldx + k;
+        if (k + 8 <= g.K) {
+            raw.v[0] = load16(xp);
+            raw.v[1] = load16(xp + 4);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; e++) raw.v[e / 4][e % 4] = k + e < g.K ? xp[e] : 0u;
+        }
+    } else {
+        const uint16_t* xp = static_cast<const uint16_t*>(g.X) + m * g.ldx + k;
+        if (k + 8 <= g.K) {
+            raw.v[0] = load16(xp);
+        } else {
+            raw.v[0] = u32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (k + i < g.K) raw.v[0][i / 2] |= uint32_t(xp[i]) << (16 * (i % 2));
+        }
+    }
+}
+
+template <int XT>
+__device__ __forceinline__ void operand_x(const RawX<XT>& raw, u32x4 (&out)[parts<XT>()]) {
+    if constexpr (XT == T_F32) {
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            float a[3], b[3];
+            split3(__uint_as_float(raw.v[e / 2][2 * (e % 2)]), a);
+            split3(__uint_as_float(raw.v[e / 2][2 * (e % 2) + 1]), b);
+#pragma unroll
+            for (int p = 0; p < 3; p++)
+                out[p][e] = __builtin_amdgcn_perm(__float_as_uint(b[p]), __float_as_uint(a[p]), 0x07060302u);
+        }
+    } else {
+        out[0] = order_x<XT>(raw.v[0]);
+    }
+}
+
 template <int XT>
 __device__ __forceinline__ v4f mfma16(u32x4 x, u32x4 w, v4f c) {
     if constexpr (XT == T_F16)
@@ -151,197 +221,274 @@ __device__ __forceinline__ void transpose_groups(u32x4& v) {
 }
 }  // namespace
 
-// Up to 16 rows of X.  A workgroup owns 16 columns n of Y for rows m0 ..
-// m0 + 15; its waves deal the K units out among themselves and add their sums
+// Up to 8 rows of X.  A workgroup owns 16 columns n of Y for rows m0 ..
+// m0 + 7; its waves deal the K units out among themselves and add their sums
 // through LDS in wave order.  The weights are the B operand of the 16 x 16 x 32
 // instruction (lane: column n = lane % 16, eight k of step j from lane group
-// lane / 16) and go from memory to registers in 16-byte loads, one pass; X is
-// the A operand, rows past M repeating the last one.  16-bit X comes straight
-// from memory (each wave reads only its own K range); float X is split once
-// per workgroup into LDS, chunk by chunk.
+// lane / 16) and go from memory to registers in 16-byte loads, one pass, PF
+// units ahead.  X is the A operand, rows past M repeating the last one.  X,
+// the scales (as floats) and the zero points (as dequant's constants) are
+// staged in LDS chunk by chunk: a wave's X loads would otherwise take four
+// times the load instructions of its weights, float X would be split by every
+// wave, and loads as small as a scale's would hold up the weights' behind
+// them, since loads complete in order.
 // GS: steps of 32 that share a scale (4 for groups of 128 or more).
-template <int XT, int GS, int NWT>
-__global__ void __launch_bounds__(1024)
-q4_rows(Q4Args g, int64_t units, int64_t units_chunk, int64_t tiles_m, int64_t tiles) {
+struct ScaleZero {
+    float s;
+    uint32_t z;
+};
+
+template <int XT, int GS, int NWT, int PF>
+__global__ void __launch_bounds__(512, 4)
+q4_rows(Q4Args g, int chunk, int64_t tiles_m, int64_t tiles) {
+    // 32-bit offsets within a tile: the host sends larger strides elsewhere.
     constexpr int P = parts<XT>(), NS = 4 / GS;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nw = blockDim.x >> 6;
     const int r = lane & 15, lg = lane >> 4;
-    const int64_t bytes = (g.K + 1) / 2, groups = (g.K + (int64_t(1) << g.shift) - 1) >> g.shift;
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int64_t n0 = tile / tiles_m * 16, m0 = tile % tiles_m * kRowsMax;
-    const int rows = int(g.M - m0 < kRowsMax ? g.M - m0 : kRowsMax);
-    const int64_t n = n0 + r < g.N ? n0 + r : g.N - 1;
-    const int mr = r < rows ? r : rows - 1;
+    const int K = int(g.K), bytes = (K + 1) / 2, last = (K - 1) >> g.shift;
+    // All units, and those wholly inside a row.
+    const int units = (K + kUnit - 1) / kUnit, full = bytes / (kUnit / 2);
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int64_t n0 = tile / tiles_m * 16, m0 = tile % tiles_m * kRowsMax;
+        const int rows = int(g.M - m0 < kRowsMax ? g.M - m0 : kRowsMax);
+        const int cols = int(g.N - n0 < 16 ? g.N - n0 : 16);
+        const int mr = r < rows ? r : rows - 1;
+        const uint32_t woff = uint32_t(r < cols ? r : cols - 1) * uint32_t(g.ldw) + uint32_t(lg) * 16u;
 
-    struct Unit {
-        u32x4 w[NWT];
-        float s[NWT][NS];
-        uint32_t z[NWT][NS];
-    };
-    auto load_unit = [&](Unit& u, int64_t idx) {
+        u32x4 ring[PF][NWT];
+        auto load_unit = [&](u32x4 (&w)[NWT], int idx) {
 #pragma unroll
-        for (int t = 0; t < NWT; t++) {
-            u.w[t] = load_w(g.W[t] + n * g.ldw, idx * (kUnit / 2) + lg * 16, bytes);
+            for (int t = 0; t < NWT; t++) w[t] = load16(g.W[t] + n0 * g.ldw + idx * (kUnit / 2) + woff);
+        };
+        v4f acc[NWT];
 #pragma unroll
-            for (int q = 0; q < NS; q++) {
-                int64_t gi = (idx * kUnit + q * (kUnit / NS)) >> g.shift;
-                gi = gi < groups ? gi : groups - 1;
-                u.s[t][q] = to_float(g.stype, g.S[t], n * g.lds + gi);
-                u.z[t][q] = g.Z[t] ? g.Z[t][n * g.ldz + gi] : 8;
-            }
-        }
-    };
-    v4f acc[NWT];
+        for (int t = 0; t < NWT; t++) acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        // LDS of a chunk: a run per lane group and row of X, of units x 4 steps
+        // x P parts of 16 bytes and 16 more (runs an odd number of 16 bytes
+        // apart fall on different banks), then per unit NWT x NS x 16 scales
+        // and zeros.
+        const int run = chunk * (4 * P * 16) + 16;
+        ScaleZero* const sz = reinterpret_cast<ScaleZero*>(smem + 4 * rows * run);
+        const char* const xlane = smem + (lg * rows + mr) * run;
+        const ScaleZero* const szlane = sz + r;
+        auto do_unit = [&](u32x4 (&w)[NWT], int local) {
+            const char* xs = xlane + local * (4 * P * 16);
+            const ScaleZero* su = szlane + local * (NWT * NS * 16);
 #pragma unroll
-    for (int t = 0; t < NWT; t++) acc[t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    // xs: this unit's staged X (float only).
-    auto do_unit = [&](Unit& u, int64_t idx, const char* xs) {
+            for (int t = 0; t < NWT; t++) transpose_groups(w[t]);
+            v4f d[NWT];
+            ScaleZero c[NWT];
 #pragma unroll
-        for (int t = 0; t < NWT; t++) transpose_groups(u.w[t]);
-        v4f d[NWT];
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            u32x4 x[P];
-            if constexpr (P == 3) {
+            for (int j = 0; j < 4; j++) {
+                u32x4 x[P];
 #pragma unroll
                 for (int p = 0; p < P; p++)
-                    x[p] = *reinterpret_cast<const u32x4*>(xs + (((j * P + p) * 4 + lg) * rows + mr) * 16);
-            } else {
-                const int64_t k = idx * kUnit + j * 32 + lg * 8;
-                const uint16_t* xp = static_cast<const uint16_t*>(g.X) + (m0 + mr) * g.ldx + k;
-                u32x4 v = {0, 0, 0, 0};
-                if (k + 8 <= g.K) {
-                    v = load16(xp);
-                } else {
-                    for (int i = 0; i < 8; i++)
-                        if (k + i < g.K) v[i / 2] |= uint32_t(xp[i]) << (16 * (i % 2));
-                }
-                x[0] = order_x<XT>(v);
-            }
+                    x[p] = *reinterpret_cast<const u32x4*>(xs + (j * P + p) * 16);
 #pragma unroll
-            for (int t = 0; t < NWT; t++) {
-                const u32x4 w = dequant<XT>(u.w[t][j], zero_const<XT>(u.z[t][j / GS]));
-                // Largest part first.  The instruction rounds to nearest when
-                // what it adds is smaller than the accumulator, and truncates
-                // the accumulator downwards when that is the smaller one
-                // (measured: with the smallest part first, products of one
-                // float and one weight came out up to a unit too low).
+                for (int t = 0; t < NWT; t++) {
+                    if (j % GS == 0) c[t] = su[(t * NS + j / GS) * 16];
+                    const u32x4 q = dequant<XT>(w[t][j], c[t].z);
+                    // Largest part first.  The instruction rounds to nearest
+                    // when what it adds is smaller than the accumulator, and
+                    // truncates the accumulator downwards when that is the
+                    // smaller one (measured: with the smallest part first,
+                    // products of one float and one weight came out up to a
+                    // unit too low).
 #pragma unroll
-                for (int p = 0; p < P; p++)
-                    d[t] = mfma16<XT>(x[p], w, p == 0 && j % GS == 0 ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : d[t]);
-                if (j % GS == GS - 1) {
+                    for (int p = 0; p < P; p++)
+                        d[t] = mfma16<XT>(x[p], q, p == 0 && j % GS == 0 ? v4f{0.0f, 0.0f, 0.0f, 0.0f} : d[t]);
+                    if (j % GS == GS - 1) {
 #pragma unroll
-                    for (int e = 0; e < 4; e++) acc[t][e] = fmaf(u.s[t][j / GS], d[t][e], acc[t][e]);
+                        for (int e = 0; e < 4; e++) acc[t][e] = fmaf(c[t].s, d[t][e], acc[t][e]);
+                    }
                 }
             }
-        }
-    };
+        };
 
-    if constexpr (P == 3) {
-        // Chunks of units_chunk units: split X into LDS, then each wave its
-        // own units of the chunk.
-        const size_t unit_bytes = size_t(4) * P * 4 * rows * 16;
-        for (int64_t c0 = 0; c0 < units; c0 += units_chunk) {
-            const int cn = int(units - c0 < units_chunk ? units - c0 : units_chunk);
-            Unit u;
-            if (wave < cn) load_unit(u, c0 + wave);
+        // The wave's units in order: of each chunk, the wave-th of nw runs (64
+        // bytes of a row per unit, so a wave reads whole stretches of its rows:
+        // 33 MB in 7.5 us, against 9.7 with the units dealt out one by one).
+        int next_c = 0, next_i = -1;
+        auto load_next = [&](u32x4 (&w)[NWT]) {
+            for (; next_c < full; next_c += chunk, next_i = -1) {
+                const int cf = full - next_c < chunk ? full - next_c : chunk, per = (cf + nw - 1) / nw;
+                if (next_i < 0) next_i = wave * per;
+                const int i1 = (wave + 1) * per < cf ? (wave + 1) * per : cf;
+                if (next_i < i1) {
+                    load_unit(w, next_c + next_i++);
+                    return;
+                }
+            }
+        };
+        // Staging of a chunk, BX pieces of 8 elements of X and BS scales a lane
+        // at a time.  The first chunk's first loads go out before the first
+        // weights': loads complete in order, so the staging then waits for
+        // them alone while the weights are on their way.
+        constexpr int BX = 2, BS = 2;
+        const int nt = blockDim.x, tid = threadIdx.x;
+        for (int c0 = 0; c0 < units; c0 += chunk) {
+            const int cn = units - c0 < chunk ? units - c0 : chunk;
+            // Pieces of X: (row xm, piece kk) by consecutive lanes along K;
+            // scales: 16 rows by nt / 16 groups of a matrix a trip.
+            const int nk = cn * 16, nq = cn * NS, row = tid % 16;
+            const int64_t n = n0 + (row < cols ? row : cols - 1);
+            int xm = 0, xk = 0, st = 0, sq = 0;
             if (c0 > 0) __syncthreads();
-            // One 8-element piece of a row per lane and trip: 16 of them per
-            // unit and row.
-            const int pieces = cn * 16 * rows;
-            for (int i = threadIdx.x; i < pieces; i += blockDim.x) {
-                const int kk = i % (cn * 16), m = i / (cn * 16);
-                const int64_t k = (c0 * 16 + kk) * 8;
-                const float* xp = static_cast<const float*>(g.X) + (m0 + m) * g.ldx + k;
-                float x[8];
-                if (k + 8 <= g.K) {
-                    *reinterpret_cast<u32x4*>(x) = load16(xp);
-                    *reinterpret_cast<u32x4*>(x + 4) = load16(xp + 4);
-                } else {
-                    for (int e = 0; e < 8; e++) x[e] = k + e < g.K ? xp[e] : 0.0f;
+            while (xm < rows || st < NWT) {
+                RawX<XT> x[BX];
+                uint32_t s[BS], z[BS];
+                const int xm0 = xm, xk0 = xk, st0 = st, sq0 = sq;
+#pragma unroll
+                for (int b = 0; b < BX; b++) {
+                    if (xm < rows && xk + tid < nk) load_x<XT>(g, m0 + xm, (c0 * 16 + xk + tid) * 8, x[b]);
+                    xk += nt;
+                    if (xk >= nk) xk = 0, xm++;
                 }
-                u32x4 out[3];
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    float a[3], b[3];
-                    split3(x[2 * e], a);
-                    split3(x[2 * e + 1], b);
-#pragma unroll
-                    for (int p = 0; p < 3; p++)
-                        out[p][e] = __builtin_amdgcn_perm(__float_as_uint(b[p]), __float_as_uint(a[p]), 0x07060302u);
+                for (int b = 0; b < BS; b++) {
+                    const int q = sq + tid / 16;
+                    if (st < NWT && q < nq) {
+                        int gi = ((c0 + q / NS) * kUnit + q % NS * (kUnit / NS)) >> g.shift;
+                        gi = gi < last ? gi : last;
+                        const void* sp = st ? g.S[NWT - 1] : g.S[0];
+                        const uint8_t* zp = st ? g.Z[NWT - 1] : g.Z[0];
+                        s[b] = load_raw(g.stype, sp, n * g.lds + gi);
+                        z[b] = zp ? zp[n * g.ldz + gi] : 8;
+                    }
+                    sq += nt / 16;
+                    if (sq >= nq) sq = 0, st++;
                 }
-                char* dst = smem + (kk / 16) * unit_bytes;
-                const int j = kk % 16 / 4, l = kk % 4;
+                if (c0 == 0 && xm0 == 0 && xk0 == 0) {
 #pragma unroll
-                for (int p = 0; p < 3; p++)
-                    *reinterpret_cast<u32x4*>(dst + (((j * 3 + p) * 4 + l) * rows + m) * 16) = out[p];
+                    for (int p = 0; p < PF; p++) load_next(ring[p]);
+                }
+                xm = xm0, xk = xk0, st = st0, sq = sq0;
+#pragma unroll
+                for (int b = 0; b < BX; b++) {
+                    const int kk = xk + tid;
+                    if (xm < rows && kk < nk) {
+                        u32x4 out[P];
+                        operand_x<XT>(x[b], out);
+                        char* dst = smem + (kk % 4 * rows + xm) * run + kk / 4 * (P * 16);
+#pragma unroll
+                        for (int p = 0; p < P; p++) *reinterpret_cast<u32x4*>(dst + p * 16) = out[p];
+                    }
+                    xk += nt;
+                    if (xk >= nk) xk = 0, xm++;
+                }
+#pragma unroll
+                for (int b = 0; b < BS; b++) {
+                    const int q = sq + tid / 16;
+                    if (st < NWT && q < nq) {
+                        ScaleZero v;
+                        v.s = raw_to_float(g.stype, s[b]);
+                        v.z = zero_const<XT>(z[b]);
+                        sz[(q / NS * NWT + st) * (NS * 16) + q % NS * 16 + row] = v;
+                    }
+                    sq += nt / 16;
+                    if (sq >= nq) sq = 0, st++;
+                }
             }
             __syncthreads();
-            for (int i = wave; i < cn; i += nw) {
-                Unit v;
-                if (i + nw < cn) load_unit(v, c0 + i + nw);
-                do_unit(u, c0 + i, smem + i * unit_bytes);
-                u = v;
+            const int cf = full - c0 < cn ? full - c0 : cn, per = (cf + nw - 1) / nw;
+            const int i0 = wave * per, i1 = i0 + per < cf ? i0 + per : cf;
+            for (int i = i0; i < i1; i += PF)
+#pragma unroll
+                for (int p = 0; p < PF; p++)
+                    if (i + p < i1) {
+                        do_unit(ring[p], i + p);
+                        load_next(ring[p]);
+                    }
+            // The unit that rows end in goes to the last wave.
+            if (cf < cn && wave == nw - 1) {
+                u32x4 w[NWT];
+#pragma unroll
+                for (int t = 0; t < NWT; t++)
+                    w[t] = load_w_tail(g.W[t] + (n0 + (r < cols ? r : cols - 1)) * g.ldw,
+                                       full * (kUnit / 2) + lg * 16, bytes);
+                do_unit(w, full - c0);
             }
         }
-    } else {
-        Unit u;
-        if (wave < units) load_unit(u, wave);
-        for (int64_t i = wave; i < units; i += nw) {
-            Unit v;
-            if (i + nw < units) load_unit(v, i + nw);
-            do_unit(u, i, nullptr);
-            u = v;
-        }
-    }
 
-    // Accumulator register e of lane (lg, r) is row 4 lg + e, column r.
-    if constexpr (P == 3) __syncthreads();
-    float* red = reinterpret_cast<float*>(smem);
+        // Accumulator register e of lane (lg, r) is row 4 lg + e, column r.
+        __syncthreads();
+        float* red = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int t = 0; t < NWT; t++)
+        for (int t = 0; t < NWT; t++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) red[(wave * NWT + t) * 256 + (4 * lg + e) * 16 + r] = acc[t][e];
-    __syncthreads();
-    for (int o = threadIdx.x; o < rows * 16; o += blockDim.x) {
-        float sum[NWT];
+            for (int e = 0; e < 4; e++) red[(wave * NWT + t) * 256 + (4 * lg + e) * 16 + r] = acc[t][e];
+        __syncthreads();
+        for (int o = threadIdx.x; o < rows * 16; o += blockDim.x) {
+            float sum[NWT];
 #pragma unroll
-        for (int t = 0; t < NWT; t++) {
-            sum[t] = red[t * 256 + o];
-            for (int w = 1; w < nw; w++) sum[t] += red[(w * NWT + t) * 256 + o];
+            for (int t = 0; t < NWT; t++) {
+                sum[t] = red[t * 256 + o];
+                for (int w = 1; w < nw; w++) sum[t] += red[(w * NWT + t) * 256 + o];
+            }
+            const int64_t m = m0 + o / 16, nn = n0 + o % 16;
+            if (nn < g.N)
+                store_as<XT>(g.Y, m * g.ldy + nn, NWT == 2 ? act_value(g.act, sum[0]) * sum[NWT - 1] : sum[0]);
         }
-        const int64_t m = m0 + o / 16, nn = n0 + o % 16;
-        if (nn < g.N)
-            store_as<XT>(g.Y, m * g.ldy + nn, NWT == 2 ? act_value(g.act, sum[0]) * sum[NWT - 1] : sum[0]);
+        if (tile + gridDim.x < tiles) __syncthreads();
     }
-    if (tile + gridDim.x < tiles) __syncthreads();
-  }
 }
 
 template <int XT, int GS, int NWT>
 static hipError_t launch_rows(const Q4Args& g, hipStream_t s) {
-    const int64_t units = ceil_div(g.K, kUnit);
-    const int nw = 8;
-    const int rows = int(g.M < kRowsMax ? g.M : kRowsMax);
-    // Float X: as many units a chunk as keep the split parts within 48 KiB,
-    // in whole rounds of the waves where that allows.
-    const int unit_bytes = 4 * 3 * 4 * rows * 16;
-    int64_t chunk = units;
+    constexpr int nw = 8, PF = 2;
+    const int64_t units = ceil_div(g.K, kUnit), rows = g.M < kRowsMax ? g.M : kRowsMax;
+    const int64_t unit_bytes = 4 * parts<XT>() * 4 * rows * 16 + NWT * (4 / GS) * 16 * int64_t(sizeof(ScaleZero));
+    // X and the scales are staged whole, or in chunks of whole rounds of the
+    // waves, PF units each, that leave room for two workgroups in a CU's LDS
+    // (float X of more than 6 rows: one).
+    constexpr int64_t kLds = 80 * 1024, round = nw * PF;
+    const int64_t fixed = 64 * rows;
+    int64_t chunk = (kLds - fixed) / unit_bytes / round * round;
+    if (chunk < round) chunk = round;
+    if (chunk > units) chunk = units;
     size_t lds = size_t(nw) * NWT * 1024;
-    if (XT == T_F32) {
-        chunk = 49152 / unit_bytes;
-        if (chunk < nw) chunk = nw;
-        chunk = chunk / nw * nw;
-        if (chunk > units) chunk = units;
-        const size_t x = size_t(chunk) * unit_bytes;
-        if (x > lds) lds = x;
-    }
+    if (size_t(chunk * unit_bytes + fixed) > lds) lds = size_t(chunk * unit_bytes + fixed);
     const int64_t tm = ceil_div(g.M, kRowsMax), tiles = ceil_div(g.N, 16) * tm;
-    hipLaunchKernelGGL((q4_rows<XT, GS, NWT>), dim3(grid_for(tiles)), dim3(64 * nw), lds, s, g, units,
-                       chunk, tm, tiles);
+    const dim3 grid(grid_for(tiles)), block(64 * nw);
+    hipLaunchKernelGGL((q4_rows<XT, GS, NWT, PF>), grid, block, lds, s, g, int(chunk), tm, tiles);
     return hipGetLastError();
+}
+
+// Any strides and sizes (64-bit offsets): one output per wave, a group at a
+// time, its K dealt to the lanes.  The fallback for operands whose rows are
+// too long for the 32-bit offsets of the kernels above.
+__global__ void __launch_bounds__(64)
+q4_general(Q4Args g, int64_t tiles) {
+    const int64_t group = int64_t(1) << g.shift, groups = (g.K + group - 1) >> g.shift;
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int64_t m = t / g.N, n = t % g.N;
+        float out[2] = {0.0f, 0.0f};
+        for (int w = 0; w < (g.act >= 0 ? 2 : 1); w++) {
+            float sum = 0.0f;
+            for (int64_t q = 0; q < groups; q++) {
+                const int64_t k0 = q << g.shift, k1 = k0 + group < g.K ? k0 + group : g.K;
+                const int z = g.Z[w] ? g.Z[w][n * g.ldz + q] : 8;
+                float part = 0.0f;
+                for (int64_t k = k0 + threadIdx.x; k < k1; k += 64) {
+                    const int b = g.W[w][n * g.ldw + k / 2];
+                    const int v = (k & 1 ? b >> 4 : b & 15) - z;
+                    part = fmaf(load_float(g.xtype, g.X, m * g.ldx + k), float(v), part);
+                }
+                sum = fmaf(load_float(g.stype, g.S[w], n * g.lds + q), part, sum);
+            }
+            for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+            out[w] = sum;
+        }
+        const float y = g.act >= 0 ? act_value(g.act, out[0]) * out[1] : out[0];
+        const int64_t at = m * g.ldy + n;
+        if (threadIdx.x == 0) {
+            if (g.xtype == T_F32) store_as<T_F32>(g.Y, at, y);
+            else if (g.xtype == T_F16) store_as<T_F16>(g.Y, at, y);
+            else store_as<T_BF16>(g.Y, at, y);
+        }
+    }
 }
 
 template <int XT, int NWT>
@@ -360,7 +507,19 @@ static hipError_t launch_nwt(const Q4Args& g, hipStream_t s) {
     }
 }
 
+// Whether a tile's 32-bit offsets reach every operand.
+static bool offsets_fit(const Q4Args& g) {
+    const int64_t lim = int64_t(1) << 31;
+    return g.K < lim - kUnit && 16 * g.ldw < lim && 16 * 4 * g.lds < lim && 16 * g.ldz < lim &&
+           (g.K >> g.shift) < lim - 1;
+}
+
 hipError_t launch_q4(const Q4Args& g, hipStream_t s) {
+    if (g.K == 0 || !offsets_fit(g)) {
+        const int64_t tiles = g.M * g.N;
+        hipLaunchKernelGGL(q4_general, dim3(grid_for(tiles)), dim3(64), 0, s, g, tiles);
+        return hipGetLastError();
+    }
     return g.act >= 0 ? launch_nwt<2>(g, s) : launch_nwt<1>(g, s);
 }
 

@@ -24,6 +24,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kUnit = 128;      // K per step of a wave: 4 lane groups of 32 weights
@@ -205,6 +206,29 @@ __device__ __forceinline__ v4f mfma16(u32x4 x, u32x4 w, v4f c) {
     else
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x),
                                                        __builtin_bit_cast(bf16x8, w), c, 0, 0, 0);
+}
+
+template <int XT>
+__device__ __forceinline__ v16f mfma32(u32x4 x, u32x4 w, v16f c) {
+    if constexpr (XT == T_F16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, x),
+                                                      __builtin_bit_cast(f16x8, w), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x),
+                                                       __builtin_bit_cast(bf16x8, w), c, 0, 0, 0);
+}
+
+// Half h of the wave (lanes 32 h ..) holds words 8 h .. 8 h + 7 of its row's
+// 16; after this, step j's word (2 j in half 0, 2 j + 1 in half 1: 16 weights)
+// is v[j & 1][j / 2 % 2 + 2 * (j / 4)].
+__device__ __forceinline__ void transpose_halves(u32x4 (&v)[2]) {
+    const u32x4 a = v[0], b = v[1];
+    auto p0 = __builtin_amdgcn_permlane32_swap(a[0], a[1], false, false);  // steps 0, 4
+    auto p1 = __builtin_amdgcn_permlane32_swap(a[2], a[3], false, false);  // steps 1, 5
+    auto p2 = __builtin_amdgcn_permlane32_swap(b[0], b[1], false, false);  // steps 2, 6
+    auto p3 = __builtin_amdgcn_permlane32_swap(b[2], b[3], false, false);  // steps 3, 7
+    v[0] = u32x4{p0[0], p2[0], p0[1], p2[1]};
+    v[1] = u32x4{p1[0], p3[0], p1[1], p3[1]};
 }
 
 // Lane group l (lanes 16 l ..) holds words 4 l .. 4 l + 3 of its row's 16; after
@@ -456,6 +480,221 @@ static hipError_t launch_rows(const Q4Args& g, hipStream_t s) {
     return hipGetLastError();
 }
 
+// More rows of X: tiles on the 32 x 32 x 16 instruction.  A workgroup is WK
+// groups of WN waves over one tile of BM = 32 TM rows and BN = 32 WN columns;
+// K group kg takes units kg, kg + WK, ... of 128 k, and the groups' sums are
+// added through LDS in group order.  Within a group every wave owns 32 columns
+// (of each weight matrix) and all BM rows: its weights go from memory to its
+// registers and are converted there, once in the workgroup, while X, which
+// all waves of the group read, is staged in LDS in slabs of 64 k as the
+// instruction takes it (float X split on the way), two slabs in turn with one
+// barrier each.
+// LDS of a slab: TM x 4 steps x P parts of 1 KiB (lane L's 16 bytes at 16 L:
+// row L % 32, eight k of half L / 32), 64 bytes apart so that the pieces a
+// wave writes at once (8 pieces of 8 rows) spread over the banks.
+template <int XT, int GS, int NWT, int TM, int WN, int WK>
+__global__ void __launch_bounds__(64 * WN * WK)
+q4_tile(Q4Args g, int tiles_m, int tiles_n) {
+    constexpr int P = parts<XT>(), NS = 4 / GS, BM = 32 * TM, BN = 32 * WN;
+    constexpr int FRAG = 1024 + 64, SLAB = TM * 4 * P * FRAG;
+    constexpr int RED = WK > 1 ? (WK - 1) * WN * NWT * TM * 4096 : 0;
+    constexpr int LDS = 2 * WK * SLAB > RED ? 2 * WK * SLAB : RED;
+    constexpr int PIECES = BM * 8 / (64 * WN);  // of 8 elements, per lane and slab
+    static_assert(PIECES * 64 * WN == BM * 8, "whole pieces");
+    __shared__ __attribute__((aligned(16))) char smem[LDS];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kg = wave / WN, wn = wave % WN, gtid = threadIdx.x - kg * (64 * WN);
+    const int r = lane & 31, half = lane >> 5;
+    const int K = int(g.K), bytes = (K + 1) / 2, last = (K - 1) >> g.shift;
+    const int units = (K + kUnit - 1) / kUnit, full = bytes / (kUnit / 2);
+    const int iters = (units + WK - 1) / WK;
+
+    // Each XCD a contiguous range of tiles, rows of tiles fastest: the tiles
+    // it runs at a time share their weights in its L2.
+    const int tiles = tiles_m * tiles_n;
+    for (int t0 = blockIdx.x; t0 < tiles; t0 += gridDim.x) {
+        int lin = t0;
+        if (int(gridDim.x) == tiles) {
+            const int q = tiles / 8, rem = tiles % 8, x = t0 % 8;
+            lin = x * q + (x < rem ? x : rem) + t0 / 8;
+        }
+        const int64_t m0 = int64_t(lin % tiles_m) * BM, n0 = int64_t(lin / tiles_m) * BN + wn * 32;
+        const int64_t n = n0 + r < g.N ? n0 + r : g.N - 1;
+        const uint8_t* wrow[NWT];
+#pragma unroll
+        for (int t = 0; t < NWT; t++) wrow[t] = g.W[t] + n * g.ldw;
+
+        struct Unit {
+            u32x4 w[NWT][2];
+            uint32_t s[NWT][NS], z[NWT][NS];
+        };
+        auto load_unit = [&](Unit& u, int idx) {
+#pragma unroll
+            for (int t = 0; t < NWT; t++) {
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const int off = idx * (kUnit / 2) + half * 32 + h * 16;
+                    u.w[t][h] = idx < full ? load16(wrow[t] + off) : load_w_tail(wrow[t], off, bytes);
+                }
+#pragma unroll
+                for (int q = 0; q < NS; q++) {
+                    int gi = (idx * kUnit + q * (kUnit / NS)) >> g.shift;
+                    gi = gi < last ? gi : last;
+                    u.s[t][q] = load_raw(g.stype, g.S[t], n * g.lds + gi);
+                    u.z[t][q] = g.Z[t] ? g.Z[t][n * g.ldz + gi] : 8;
+                }
+            }
+        };
+        RawX<XT> xr[PIECES];
+        auto load_slab = [&](int slab) {  // slab of this group's X, into registers
+#pragma unroll
+            for (int p = 0; p < PIECES; p++) {
+                const int i = gtid + p * (64 * WN);
+                const int64_t m = m0 + i / 8 < g.M ? m0 + i / 8 : g.M - 1;
+                load_x<XT>(g, m, slab * 64 + i % 8 * 8, xr[p]);
+            }
+        };
+        auto store_slab = [&](int buf) {
+            char* base = smem + (buf * WK + kg) * SLAB;
+#pragma unroll
+            for (int p = 0; p < PIECES; p++) {
+                const int i = gtid + p * (64 * WN), m = i / 8, kk = i % 8;
+                u32x4 out[P];
+                operand_x<XT>(xr[p], out);
+#pragma unroll
+                for (int q = 0; q < P; q++)
+                    *reinterpret_cast<u32x4*>(base + ((m / 32 * 4 + kk / 2) * P + q) * FRAG + (kk % 2 * 32 + m % 32) * 16) = out[q];
+            }
+        };
+
+        v16f acc[NWT][TM], d[NWT][TM];
+#pragma unroll
+        for (int t = 0; t < NWT; t++)
+#pragma unroll
+            for (int b = 0; b < TM; b++) acc[t][b] = v16f{};
+        // The four steps of one slab; h: which half of its unit it is.
+        auto do_slab = [&](Unit& u, int buf, auto hc) {
+            constexpr int h = decltype(hc)::value;
+            const char* base = smem + (buf * WK + kg) * SLAB + lane * 16;
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                constexpr int PER = 2 * GS;  // steps of 16 that share a scale
+                const int step = h * 4 + j;
+                u32x4 q[NWT];
+#pragma unroll
+                for (int t = 0; t < NWT; t++)
+                    q[t] = dequant<XT>(u.w[t][step & 1][(step & 3) / 2 + (step >> 2) * 2], zero_const<XT>(u.z[t][step / PER]));
+#pragma unroll
+                for (int b = 0; b < TM; b++)
+#pragma unroll
+                    for (int p = 0; p < P; p++) {
+                        const u32x4 x = *reinterpret_cast<const u32x4*>(base + ((b * 4 + j) * P + p) * FRAG);
+#pragma unroll
+                        for (int t = 0; t < NWT; t++)
+                            d[t][b] = mfma32<XT>(x, q[t], p == 0 && step % PER == 0 ? v16f{} : d[t][b]);
+                    }
+                if (step % PER == PER - 1) {
+#pragma unroll
+                    for (int t = 0; t < NWT; t++) {
+                        const float s = raw_to_float(g.stype, u.s[t][step / PER]);
+#pragma unroll
+                        for (int b = 0; b < TM; b++)
+#pragma unroll
+                            for (int e = 0; e < 16; e++) acc[t][b][e] = fmaf(s, d[t][b][e], acc[t][b][e]);
+                    }
+                }
+            }
+        };
+
+        Unit u;
+        if (kg < units) {
+            load_slab(2 * kg);
+            load_unit(u, kg);
+            store_slab(0);
+        }
+        __syncthreads();
+        for (int i = 0; i < iters; i++) {
+            const int idx = i * WK + kg, nxt = idx + WK;
+            const bool on = idx < units, more = nxt < units;
+            Unit v;
+            if (on) {
+                load_slab(2 * idx + 1);
+                if (more) load_unit(v, nxt);
+#pragma unroll
+                for (int t = 0; t < NWT; t++) transpose_halves(u.w[t]);
+                do_slab(u, 0, std::integral_constant<int, 0>{});
+                store_slab(1);
+            }
+            __syncthreads();
+            if (on) {
+                if (more) load_slab(2 * nxt);
+                do_slab(u, 1, std::integral_constant<int, 1>{});
+                if (more) store_slab(0);
+                u = v;
+            }
+            __syncthreads();
+        }
+
+        if constexpr (WK > 1) {
+            float* red = reinterpret_cast<float*>(smem);
+            constexpr int PER_WAVE = NWT * TM * 1024;
+            if (kg > 0) {
+                float* o = red + ((kg - 1) * WN + wn) * PER_WAVE + lane;
+#pragma unroll
+                for (int t = 0; t < NWT; t++)
+#pragma unroll
+                    for (int b = 0; b < TM; b++)
+#pragma unroll
+                        for (int e = 0; e < 16; e++) o[((t * TM + b) * 16 + e) * 64] = acc[t][b][e];
+            }
+            __syncthreads();
+            if (kg == 0) {
+#pragma unroll 1
+                for (int k = 0; k < WK - 1; k++) {
+                    const float* o = red + (k * WN + wn) * PER_WAVE + lane;
+#pragma unroll
+                    for (int t = 0; t < NWT; t++)
+#pragma unroll
+                        for (int b = 0; b < TM; b++)
+#pragma unroll
+                            for (int e = 0; e < 16; e++) acc[t][b][e] += o[((t * TM + b) * 16 + e) * 64];
+                }
+            }
+        }
+        // Accumulator register e of a lane is row 8 (e / 4) + 4 half + e % 4 of
+        // its block, column r.
+        if (kg == 0 && n0 + r < g.N) {
+#pragma unroll
+            for (int b = 0; b < TM; b++)
+#pragma unroll
+                for (int e = 0; e < 16; e++) {
+                    const int64_t m = m0 + b * 32 + 8 * (e / 4) + 4 * half + e % 4;
+                    if (m < g.M)
+                        store_as<XT>(g.Y, m * g.ldy + n0 + r,
+                                     NWT == 2 ? act_value(g.act, acc[0][b][e]) * acc[NWT - 1][b][e] : acc[0][b][e]);
+                }
+        }
+        if (t0 + int(gridDim.x) < tiles) __syncthreads();
+    }
+}
+
+template <int XT, int GS, int NWT, int TM, int WN, int WK>
+static hipError_t launch_tile(const Q4Args& g, hipStream_t s) {
+    const int64_t tm = ceil_div(g.M, 32 * TM), tn = ceil_div(g.N, 32 * WN);
+    hipLaunchKernelGGL((q4_tile<XT, GS, NWT, TM, WN, WK>), dim3(grid_for(tm * tn)), dim3(64 * WN * WK), 0,
+                       s, g, int(tm), int(tn));
+    return hipGetLastError();
+}
+
+template <int XT, int GS, int NWT>
+static hipError_t launch_tiles(const Q4Args& g, hipStream_t s) {
+    constexpr bool f = XT == T_F32;
+    const int64_t big = ceil_div(g.M, NWT == 2 ? 64 : 128) * ceil_div(g.N, 256);
+    if (big >= 200) return launch_tile<XT, GS, NWT, NWT == 2 ? 2 : 4, 8, 1>(g, s);
+    if (ceil_div(g.M, 64) * ceil_div(g.N, 64) >= 200 && NWT == 1) return launch_tile<XT, GS, NWT, 2, 2, f ? 2 : 4>(g, s);
+    return launch_tile<XT, GS, NWT, 1, 1, f ? 4 : 8>(g, s);
+}
+
 // Any strides and sizes (64-bit offsets): one output per wave, a group at a
 // time, its K dealt to the lanes.  The fallback for operands whose rows are
 // too long for the 32-bit offsets of the kernels above.
@@ -491,11 +730,16 @@ q4_general(Q4Args g, int64_t tiles) {
     }
 }
 
+template <int XT, int GS, int NWT>
+static hipError_t launch_gs(const Q4Args& g, hipStream_t s) {
+    return g.M <= kRowsMax ? launch_rows<XT, GS, NWT>(g, s) : launch_tiles<XT, GS, NWT>(g, s);
+}
+
 template <int XT, int NWT>
 static hipError_t launch_xt(const Q4Args& g, hipStream_t s) {
-    if (g.shift >= 7) return launch_rows<XT, 4, NWT>(g, s);
-    if (g.shift == 6) return launch_rows<XT, 2, NWT>(g, s);
-    return launch_rows<XT, 1, NWT>(g, s);
+    if (g.shift >= 7) return launch_gs<XT, 4, NWT>(g, s);
+    if (g.shift == 6) return launch_gs<XT, 2, NWT>(g, s);
+    return launch_gs<XT, 1, NWT>(g, s);
 }
 
 template <int NWT>

@@ -328,7 +328,7 @@ int sgemm_glu_f32(int act, int transw, int64_t M, int64_t F, int64_t K, const fl
         return launch_status(e);
     }
     const sgemm::GluArgs g{act, transw == SGEMM_OP_T, M, F, K, X, ldx, Wg, Wu, ldw, H, ldh, G, U, ldgu};
-    return launch_status(sgemm::launch_glu_general(g, s));
+    return launch_status(sgemm::launch_glu(g, s));
 }
 
 int sgemm_glu_backward_f32(int act, int transw, int64_t M, int64_t F, int64_t K, const float* X,

@@ -141,13 +141,18 @@ template <class T, class F> struct pick<false, T, F> { using type = F; };
 // MF16: the wave's 32 x 32 blocks are each computed as four 16 x 16
 // accumulators of v_mfma_f32_16x16x4_f32 (four independent chains in place
 // of one).
+// GLU: two B operands of the same layout (gate and up weights).  The tile's
+// columns are BH = BN / 2 columns of the first and the same BH columns of the
+// second, each staged as an image of its own, and the wave's blocks are NB / 2
+// of the first and NB / 2 of the second at the same columns, so a lane holds
+// both sums of each of its outputs.
 template <int WAVES_M_, int WAVES_N_, int TM_, int TN_, int BK_, bool VEC_, bool A_KMAJOR_ = true,
-          bool B_KMAJOR_ = false, int NSTAGE_ = 2, bool MF16_ = false>
+          bool B_KMAJOR_ = false, int NSTAGE_ = 2, bool MF16_ = false, bool GLU_ = false>
 struct Cfg {
     static constexpr int WAVES_M = WAVES_M_, WAVES_N = WAVES_N_, TM = TM_, TN = TN_, BK = BK_;
     static constexpr bool VEC = VEC_, A_KMAJOR = A_KMAJOR_, B_KMAJOR = B_KMAJOR_;
     static constexpr int NSTAGE = NSTAGE_;
-    static constexpr bool MF16 = MF16_;
+    static constexpr bool MF16 = MF16_, GLU = GLU_;
     // Accumulator block edge, blocks per wave along M and N, k-slots of one
     // instruction (lane groups), and accumulator registers per lane.
     static constexpr int BLK = MF16 ? 16 : 32;
@@ -157,19 +162,22 @@ struct Cfg {
     static constexpr int NWAVES = WAVES_M * WAVES_N;
     static constexpr int THREADS = 64 * NWAVES;
     static constexpr int BM = WAVES_M * TM * 32, BN = WAVES_N * TN * 32;
-    static constexpr bool B_INTERLEAVE = !B_KMAJOR && (MF16 ? (NB == 2 || NB == 4) : TN == 4);
+    static constexpr int NBH = GLU ? NB / 2 : NB, BH = GLU ? BN / 2 : BN;
+    static constexpr bool B_INTERLEAVE = !B_KMAJOR && !GLU && (MF16 ? (NB == 2 || NB == 4) : TN == 4);
     using LA = typename pick<A_KMAJOR, KMajor<BM, BK, VEC>, KRows<BM, BK, VEC>>::type;
-    using LB = typename pick<B_KMAJOR, KMajor<BN, BK, VEC>,
-                             KRows<BN, BK, VEC, MF16 && B_INTERLEAVE && NB == 2>>::type;
+    using LB = typename pick<B_KMAJOR, KMajor<BH, BK, VEC>,
+                             KRows<BH, BK, VEC, MF16 && B_INTERLEAVE && NB == 2>>::type;
     static constexpr int A_BASE = 0, B_BASE = LA::STAGE;
-    static constexpr int STAGE = LA::STAGE + LB::STAGE;
+    static constexpr int B_IMAGES = GLU ? 2 : 1;
+    static constexpr int STAGE = LA::STAGE + B_IMAGES * LB::STAGE;
     static constexpr int LDS_BYTES = NSTAGE * STAGE;
     static constexpr int A_INSTR_PER_WAVE = LA::INSTR / NWAVES;
-    static constexpr int B_INSTR_PER_WAVE = LB::INSTR / NWAVES;
+    static constexpr int B_INSTR_PER_WAVE = B_IMAGES * LB::INSTR / NWAVES;
     static constexpr int KH = BK / KSLOTS;  // MFMA steps per slab
     static_assert(BK == 16 || BK == 32, "slab depth");
+    static_assert(!GLU || NB % 2 == 0, "whole blocks of each B operand");
     static_assert(NSTAGE >= 2 && NSTAGE <= 4, "stages");
-    static_assert(LA::INSTR % NWAVES == 0 && LB::INSTR % NWAVES == 0, "loads split evenly over waves");
+    static_assert(LA::INSTR % NWAVES == 0 && B_IMAGES * LB::INSTR % NWAVES == 0, "loads split evenly over waves");
     static_assert(LDS_BYTES <= 160 * 1024, "LDS per workgroup");
 
     // Slab column that k-slot s stands for at MFMA step t.
@@ -178,6 +186,7 @@ struct Cfg {
     // j = L % BLK).
     __host__ __device__ static constexpr int a_row(int wm, int mb, int j) { return wm * TM * 32 + mb * BLK + j; }
     __host__ __device__ static constexpr int b_col(int wn, int nb, int j) {
+        if constexpr (GLU) return (nb / NBH) * BH + wn * TN * 16 + (nb % NBH) * BLK + j;
         return B_INTERLEAVE ? wn * TN * 32 + NB * j + nb : wn * TN * 32 + nb * BLK + j;
     }
     // Row within its block of accumulator register r of a lane in k-slot
@@ -191,8 +200,9 @@ struct Cfg {
         else return A_BASE + LA::elem(k, m);
     }
     __host__ __device__ static constexpr int b_elem(int k, int n) {
-        if constexpr (B_KMAJOR) return B_BASE + LB::elem(n, k);
-        else return B_BASE + LB::elem(k, n);
+        const int base = B_BASE + (GLU ? n / BH * LB::STAGE : 0), c = GLU ? n % BH : n;
+        if constexpr (B_KMAJOR) return base + LB::elem(c, k);
+        else return base + LB::elem(k, c);
     }
 };
 

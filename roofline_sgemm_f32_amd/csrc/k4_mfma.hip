@@ -38,6 +38,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "activation.h"
 #include "k4_layout.h"
 #include "kernels.h"
 
@@ -85,6 +86,53 @@ __device__ __forceinline__ void wait_vm_batches(int n) {
     wait_vm<0>();
 }
 
+// The gated form's (CF::GLU) second B operand and outputs: C holds H =
+// act(A B) * (A B2), and G = A B, U = A B2 are stored too unless G is null.
+struct GluTail {
+    const float* B2;
+    float *G, *U;
+    int64_t ldgu;
+    int act;
+};
+struct NoTail {};
+
+// The B operand that load instruction u of a slab reads.
+template <class CF, class Tail>
+__device__ __forceinline__ const float* second_b(const float* B, const Tail& tail, int u) {
+    if constexpr (CF::GLU) return u < CF::LB::INSTR ? B : tail.B2;
+    else return B;
+}
+
+// Store n (1, 2 or 4) neighbouring outputs of the gated form from their two
+// sums; vec: every output row suits accesses of n floats.
+template <int NV>
+__device__ __forceinline__ void store_glu(const GluTail& tail, float* H, int64_t ldh, int row, int col, int N,
+                                          const float (&g)[NV], const float (&u)[NV], bool vec) {
+    float h[NV];
+#pragma unroll
+    for (int e = 0; e < NV; e++) h[e] = act_value(tail.act, g[e]) * u[e];
+    float* hp = H + (int64_t)row * ldh + col;
+    float* gp = tail.G ? tail.G + (int64_t)row * tail.ldgu + col : nullptr;
+    float* up = tail.G ? tail.U + (int64_t)row * tail.ldgu + col : nullptr;
+    if constexpr (NV > 1) {
+        typedef float vt __attribute__((ext_vector_type(NV)));
+        if (vec && col + NV <= N) {
+            vt a, b, c;
+#pragma unroll
+            for (int e = 0; e < NV; e++) a[e] = h[e], b[e] = g[e], c[e] = u[e];
+            *(vt*)hp = a;
+            if (gp) *(vt*)gp = b, *(vt*)up = c;
+            return;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < NV; e++)
+        if (col + e < N) {
+            hp[e] = h[e];
+            if (gp) gp[e] = g[e], up[e] = u[e];
+        }
+}
+
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const float* base) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(base), (short)0, (int)OOB,
                                              RSRC_WORD3);
@@ -117,7 +165,7 @@ template <class CF, int OCC, int GM = GROUP_M, bool XCD_REMAP = true, bool SPLIT
 __global__ void __launch_bounds__(CF::THREADS * WK) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
 k4_mfma(int M, int N, int K, const float* __restrict__ A, int lda, const float* __restrict__ B,
         int ldb, float* __restrict__ C, int64_t ldc, float alpha, float beta, int tiles_m,
-        int tiles_n, int tiles, int kchunk) {
+        int tiles_n, int tiles, int kchunk, typename std::conditional<CF::GLU, GluTail, NoTail>::type tail) {
     // 32-bit sizes: the host routes shapes whose sizes, leading dimensions
     // or slab offsets do not fit (k4_supports) to the 64-bit kernel.
     // MB x NB accumulator blocks per wave (32 x 32, or 16 x 16 with MF16).
@@ -134,6 +182,7 @@ k4_mfma(int M, int N, int K, const float* __restrict__ A, int lda, const float* 
     // workgroups per CU, and their LDS must fit the CU's 160 KiB.
     static_assert((OCC * 4 / (CF::NWAVES * WK)) * LDS_TOTAL <= 160 * 1024,
                   "occupancy target exceeds the CU's LDS");
+    static_assert(!CF::GLU || !SPLITK, "the gated form has no split mode");
     if constexpr (SPLITK) {
         const int z = blockIdx.y, k0 = z * kchunk;
         K = K - k0 < kchunk ? K - k0 : kchunk;
@@ -163,7 +212,7 @@ k4_mfma(int M, int N, int K, const float* __restrict__ A, int lda, const float* 
         const int first_m = (lin / per_group) * GM;
         const int gsz = (tiles_m - first_m) < GM ? (tiles_m - first_m) : GM;
         const int row0 = (first_m + (lin % per_group) % gsz) * CF::BM;
-        const int col0 = ((lin % per_group) / gsz) * CF::BN;
+        const int col0 = ((lin % per_group) / gsz) * CF::BH;
 
         // Loads of one slab.  CHECK: elements outside the matrix get the
         // offset the buffer's range check turns into zero.  A tile wholly
@@ -201,29 +250,35 @@ k4_mfma(int M, int N, int K, const float* __restrict__ A, int lda, const float* 
                                       !CHECK || (k0 + k < K && row0 + c < M) ? off : OOB);
                 }
             }
+            // Gated form: a wave's load instructions past the first image's
+            // are for the second B operand.
             if constexpr (CF::B_KMAJOR) {  // B stored N x K
-                const __amdgpu_buffer_rsrc_t rb = make_rsrc(B + (int64_t)col0 * ldb + k0);
+                const int64_t at = (int64_t)col0 * ldb + k0;
 #pragma unroll
                 for (int q = 0; q < CF::B_INSTR_PER_WAVE; q++) {
-                    const int u = wave * CF::B_INSTR_PER_WAVE + q;
+                    const int uu = wave * CF::B_INSTR_PER_WAVE + q;
+                    const int u = CF::GLU ? uu % LB::INSTR : uu;
+                    const __amdgpu_buffer_rsrc_t rb = make_rsrc(second_b<CF>(B, tail, uu) + at);
                     const int r = LB::load_row(u, lane), k = LB::load_k(u, lane);
                     const unsigned off = (unsigned)(r * ldb + k) * 4u;
-                    load_lds<CF::VEC>(rb, base + CF::B_BASE + LB::load_lds(u),
+                    load_lds<CF::VEC>(rb, base + CF::B_BASE + (uu - u) / LB::INSTR * LB::STAGE + LB::load_lds(u),
                                       !CHECK || (col0 + r < N && k0 + k < K) ? off : OOB);
                 }
             } else {  // B stored K x N
-                const __amdgpu_buffer_rsrc_t rb = make_rsrc(B + (int64_t)k0 * ldb + col0);
+                const int64_t at = (int64_t)k0 * ldb + col0;
 #pragma unroll
                 for (int q = 0; q < CF::B_INSTR_PER_WAVE; q++) {
-                    const int u = wave * CF::B_INSTR_PER_WAVE + q;
+                    const int uu = wave * CF::B_INSTR_PER_WAVE + q;
+                    const int u = CF::GLU ? uu % LB::INSTR : uu;
+                    const __amdgpu_buffer_rsrc_t rb = make_rsrc(second_b<CF>(B, tail, uu) + at);
                     const int k = LB::load_k(u, lane), c = LB::load_col(u, lane);
                     const unsigned off = (unsigned)(k * ldb + c) * 4u;
-                    load_lds<CF::VEC>(rb, base + CF::B_BASE + LB::load_lds(u),
+                    load_lds<CF::VEC>(rb, base + CF::B_BASE + (uu - u) / LB::INSTR * LB::STAGE + LB::load_lds(u),
                                       !CHECK || (k0 + k < K && col0 + c < N) ? off : OOB);
                 }
             }
         };
-        const bool tile_inside = row0 + CF::BM <= M && col0 + CF::BN <= N;
+        const bool tile_inside = row0 + CF::BM <= M && col0 + CF::BH <= N;
 
         Acc acc[MB][NB];
 #pragma unroll
@@ -433,6 +488,20 @@ k4_mfma(int M, int N, int K, const float* __restrict__ A, int lda, const float* 
         for (; s < iters; s++) slab_step(s, std::true_type{}, std::false_type{});
 
         const bool read_c = beta != 0.0f;
+        if constexpr (CF::GLU && WK == 1) {
+#pragma unroll
+            for (int mb = 0; mb < MB; mb++)
+#pragma unroll
+                for (int nb = 0; nb < CF::NBH; nb++)
+#pragma unroll
+                    for (int r = 0; r < NREG; r++) {
+                        const int row = row0 + CF::a_row(wm, mb, 0) + CF::acc_row(ls, r);
+                        const int col = col0 + CF::b_col(wn, nb, li);
+                        const float gv[1] = {acc[mb][nb][r]}, uv[1] = {acc[mb][nb + CF::NBH][r]};
+                        if (row < M) store_glu<1>(tail, C, ldc, row, col, N, gv, uv, false);
+                    }
+            continue;
+        }
         if constexpr (WK > 1) {
             // Every stage is free after the loop's last barrier (with NOSYNC,
             // after the one below).  Each K group
@@ -460,6 +529,28 @@ k4_mfma(int M, int N, int K, const float* __restrict__ A, int lda, const float* 
                         red[(kg * CF::BM + row) * RLD + col] = acc[mb][nb][r];
                     }
             __syncthreads();
+            if constexpr (CF::GLU) {
+                // Two neighbouring outputs a lane: four sums over the groups.
+                constexpr int PAIRS = CF::BM * CF::BH / (2 * CF::THREADS * WK);
+                static_assert(PAIRS * 2 * CF::THREADS * WK == CF::BM * CF::BH, "whole pairs per lane");
+                const bool vec_h = ((reinterpret_cast<uintptr_t>(C) | reinterpret_cast<uintptr_t>(tail.G) |
+                                     reinterpret_cast<uintptr_t>(tail.U)) & 7) == 0 &&
+                                   (ldc & 1) == 0 && (!tail.G || (tail.ldgu & 1) == 0);
+#pragma unroll
+                for (int q = 0; q < PAIRS; q++) {
+                    const int o = (tid + q * CF::THREADS * WK) * 2, row = o / CF::BH, col = o % CF::BH;
+                    v2f sg = *(const v2f*)(red + row * RLD + col), su = *(const v2f*)(red + row * RLD + CF::BH + col);
+#pragma unroll
+                    for (int g = 1; g < WK; g++) {
+                        sg += *(const v2f*)(red + (g * CF::BM + row) * RLD + col);
+                        su += *(const v2f*)(red + (g * CF::BM + row) * RLD + CF::BH + col);
+                    }
+                    const float gv[2] = {sg[0], sg[1]}, uv[2] = {su[0], su[1]};
+                    if (row0 + row < M) store_glu<2>(tail, C, ldc, row0 + row, col0 + col, N, gv, uv, vec_h);
+                }
+                if (t + (int)gridDim.x < tiles) __syncthreads();
+                continue;
+            }
             v4f sum[PER_LANE / 4];
 #pragma unroll
             for (int q = 0; q < PER_LANE / 4; q++) {
@@ -576,7 +667,7 @@ hipError_t launch_k4_cfg(const GemmArgs& g, hipStream_t s) {
     hipLaunchKernelGGL((k4_mfma<CF, OCC, GROUP_M, true, SPLIT, false, WK, PRIO, UNCHK, PIPE, NOSYNC>), dim3(grid_for(tiles)),
                        dim3(CF::THREADS * WK), 0, s,
                        (int)g.M, (int)g.N, (int)g.K, g.A, (int)g.lda, g.B, (int)g.ldb, g.C, g.ldc,
-                       g.alpha, g.beta, (int)tm, (int)tn, (int)tiles, 0);
+                       g.alpha, g.beta, (int)tm, (int)tn, (int)tiles, 0, NoTail{});
     return hipGetLastError();
 }
 
@@ -667,7 +758,7 @@ hipError_t launch_k4_cfg_splitk(const GemmArgs& g, int splits, int kchunk, float
     hipLaunchKernelGGL((k4_mfma<CF, OCC, GROUP_M, true, SPLIT, true, WK, false, UNCHK, PIPE, NOSYNC>), dim3(grid_for(tiles), splits),
                        dim3(CF::THREADS * WK), 0, s,
                        (int)g.M, (int)g.N, (int)g.K, g.A, (int)g.lda, g.B, (int)g.ldb, ws, ldw,
-                       1.0f, 0.0f, (int)tm, (int)tn, (int)tiles, kchunk);
+                       1.0f, 0.0f, (int)tm, (int)tn, (int)tiles, kchunk, NoTail{});
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     return launch_splitk_reduce(g, splits, ws, ldw, s);
@@ -825,6 +916,47 @@ hipError_t launch_k4_t64_wk4(const GemmArgs& g, hipStream_t s, int splits, int k
                                     float* ws) {
     if (vec_ok(g)) return launch_k4_orient<2, 2, 1, 1, 32, true, 4, true, 2, 4, true, 4, 2, false, true>(g, s, splits, kchunk, ws);
     return launch_k4_t32_wk4(g, s, splits, kchunk, ws);
+}
+
+// The gated form on the tile configurations above, BH = BN / 2 columns of H
+// per tile.  Weights K x F take the KRows layout, F x K the KMajor one.
+template <class CF, int OCC, bool SPLIT, int WK, bool PRIO, bool PIPE, bool NOSYNC>
+static hipError_t launch_glu_cfg(const GluArgs& g, hipStream_t s) {
+    const int64_t tm = ceil_div(g.M, CF::BM), tn = ceil_div(g.F, CF::BH), tiles = tm * tn;
+    hipLaunchKernelGGL((k4_mfma<CF, OCC, GROUP_M, true, SPLIT, false, WK, PRIO, 2, PIPE, NOSYNC>),
+                       dim3(grid_for(tiles)), dim3(CF::THREADS * WK), 0, s, (int)g.M, (int)g.F, (int)g.K,
+                       g.X, (int)g.ldx, g.Wg, (int)g.ldw, g.H, g.ldh, 1.0f, 0.0f, (int)tm, (int)tn,
+                       (int)tiles, 0, GluTail{g.Wu, g.G, g.U, g.ldgu, g.act});
+    return hipGetLastError();
+}
+
+template <int WM, int WN, int TM, int TN, int BK, bool V, int NS, bool MF16, int OCC, bool SPLIT, int WK,
+          bool PRIO, bool PIPE, bool NOSYNC>
+static hipError_t launch_glu_orient(const GluArgs& g, hipStream_t s) {
+    using k4::Cfg;
+    if (g.transw)
+        return launch_glu_cfg<Cfg<WM, WN, TM, TN, BK, V, true, true, NS, MF16, true>, OCC, SPLIT, WK, PRIO, PIPE, NOSYNC>(g, s);
+    return launch_glu_cfg<Cfg<WM, WN, TM, TN, BK, V, true, false, NS, MF16, true>, OCC, SPLIT, WK, PRIO, PIPE, NOSYNC>(g, s);
+}
+
+hipError_t launch_k4_glu(const GluArgs& g, int cfg, bool vec, hipStream_t s) {
+    switch (cfg) {
+        case K4_T128X256:
+            if (vec) return launch_glu_orient<2, 2, 2, 4, 16, true, 2, false, 2, true, 1, true, true, false>(g, s);
+            break;
+        case K4_T128:
+            if (vec) return launch_glu_orient<2, 2, 2, 2, 16, true, 2, true, 4, false, 1, false, false, false>(g, s);
+            break;
+        case K4_T64_WK4:
+            if (vec) return launch_glu_orient<2, 2, 1, 1, 32, true, 2, true, 4, true, 4, false, true, false>(g, s);
+            break;
+        case K4_T32_WK4:
+            if (vec) return launch_glu_orient<1, 1, 1, 1, 32, true, 2, true, 2, true, 4, false, true, true>(g, s);
+            return launch_glu_orient<1, 1, 1, 1, 16, false, 2, true, 4, false, 4, false, false, true>(g, s);
+        default: break;
+    }
+    if (vec) return launch_glu_orient<2, 2, 1, 1, 32, true, 2, true, 4, true, 1, false, false, false>(g, s);
+    return launch_glu_orient<2, 2, 1, 1, 16, false, 2, true, 8, false, 1, false, false, false>(g, s);
 }
 
 }  // namespace sgemm

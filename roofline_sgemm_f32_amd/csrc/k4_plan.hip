@@ -489,4 +489,22 @@ hipError_t launch_k4_mfma(const GemmArgs& g, hipStream_t s, int requested, bool 
     return e != hipSuccess ? e : f;
 }
 
+// The gated form as the product it costs: X times [Wg Wu], M x 2F.
+static GemmArgs glu_product(const GluArgs& g) {
+    GemmArgs p{g.M, 2 * g.F, g.K, g.X, g.ldx, g.Wg, g.ldw, g.H, g.ldh};
+    p.trans_b = g.transw;
+    return p;
+}
+
+hipError_t launch_glu(const GluArgs& g, hipStream_t s) {
+    GemmArgs p = glu_product(g), one = p;
+    one.N = g.F;
+    if (!k4_supports(p) || !k4_supports(one)) return launch_glu_general(g, s);
+    const bool vec = vec_ok(one) && rows_vec(g.Wu, g.ldw, g.transw ? g.K : g.F);
+    // The plan sees alignment through the product's operands: an unaligned up
+    // weight counts as an unaligned gate weight.
+    if (!vec) p.B = reinterpret_cast<const float*>(uintptr_t(4));
+    return launch_k4_glu(g, k4_plan(p, 1).cfg, vec, s);
+}
+
 }  // namespace sgemm

@@ -201,6 +201,11 @@ struct GluArgs {
     float *G, *U;
     int64_t ldgu;
 };
+// The matrix-core kernel's gated form in tile configuration cfg (K4Cfg), with
+// 16-byte loads (vec) or 4-byte ones.
+hipError_t launch_k4_glu(const GluArgs& g, int cfg, bool vec, hipStream_t s);
+// Shape-chosen forward pass.
+hipError_t launch_glu(const GluArgs& g, hipStream_t s);
 // General kernel (64-bit offsets, any strides).
 hipError_t launch_glu_general(const GluArgs& g, hipStream_t s);
 // Backward pass: dG, dU (M x F), then dX (M x K) unless null, and dWg, dWu

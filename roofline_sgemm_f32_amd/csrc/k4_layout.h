@@ -145,7 +145,8 @@ template <class T, class F> struct pick<false, T, F> { using type = F; };
 // columns are BH = BN / 2 columns of the first and the same BH columns of the
 // second, each staged as an image of its own, and the wave's blocks are NB / 2
 // of the first and NB / 2 of the second at the same columns, so a lane holds
-// both sums of each of its outputs.
+// both sums of each of its outputs.  B_INTERLEAVE applies to the NB / 2 = 2
+// blocks of each.
 template <int WAVES_M_, int WAVES_N_, int TM_, int TN_, int BK_, bool VEC_, bool A_KMAJOR_ = true,
           bool B_KMAJOR_ = false, int NSTAGE_ = 2, bool MF16_ = false, bool GLU_ = false>
 struct Cfg {
@@ -163,10 +164,11 @@ struct Cfg {
     static constexpr int THREADS = 64 * NWAVES;
     static constexpr int BM = WAVES_M * TM * 32, BN = WAVES_N * TN * 32;
     static constexpr int NBH = GLU ? NB / 2 : NB, BH = GLU ? BN / 2 : BN;
-    static constexpr bool B_INTERLEAVE = !B_KMAJOR && !GLU && (MF16 ? (NB == 2 || NB == 4) : TN == 4);
+    static constexpr bool B_INTERLEAVE =
+        !B_KMAJOR && (GLU ? NBH == 2 : MF16 ? (NB == 2 || NB == 4) : TN == 4);
     using LA = typename pick<A_KMAJOR, KMajor<BM, BK, VEC>, KRows<BM, BK, VEC>>::type;
     using LB = typename pick<B_KMAJOR, KMajor<BH, BK, VEC>,
-                             KRows<BH, BK, VEC, MF16 && B_INTERLEAVE && NB == 2>>::type;
+                             KRows<BH, BK, VEC, MF16 && B_INTERLEAVE && NBH == 2>>::type;
     static constexpr int A_BASE = 0, B_BASE = LA::STAGE;
     static constexpr int B_IMAGES = GLU ? 2 : 1;
     static constexpr int STAGE = LA::STAGE + B_IMAGES * LB::STAGE;
@@ -186,7 +188,8 @@ struct Cfg {
     // j = L % BLK).
     __host__ __device__ static constexpr int a_row(int wm, int mb, int j) { return wm * TM * 32 + mb * BLK + j; }
     __host__ __device__ static constexpr int b_col(int wn, int nb, int j) {
-        if constexpr (GLU) return (nb / NBH) * BH + wn * TN * 16 + (nb % NBH) * BLK + j;
+        if constexpr (GLU)
+            return (nb / NBH) * BH + wn * TN * 16 + (B_INTERLEAVE ? NBH * j + nb % NBH : (nb % NBH) * BLK + j);
         return B_INTERLEAVE ? wn * TN * 32 + NB * j + nb : wn * TN * 32 + nb * BLK + j;
     }
     // Row within its block of accumulator register r of a lane in k-slot

@@ -343,17 +343,22 @@ k4_mfma(int M, int N, int K, const float* __restrict__ A, int lda, const float* 
                     }
                 }
                 if constexpr (CF::B_INTERLEAVE) {
-                    // The lane's NB columns of one k: one 16- or 8-byte read.
-                    using BV = typename std::conditional<NB == 4, v4f, v2f>::type;
-                    static_assert(NB == 4 || NB == 2, "interleaved columns");
+                    // The lane's NB columns of one k: one 16- or 8-byte read (one
+                    // of each image in the gated form).
+                    constexpr int NBI = CF::NBH;
+                    using BV = typename std::conditional<NBI == 4, v4f, v2f>::type;
+                    static_assert(NBI == 4 || NBI == 2, "interleaved columns");
 #pragma unroll
                     for (int u = 0; u < KP; u++) {
-                        const BV v = *(const BV*)(st + CF::b_elem(CF::kslot(ls, h * KP + u), CF::b_col(wn, 0, li)));
 #pragma unroll
-                        for (int nb = 0; nb < NB; nb++) bf[nb][u] = v[nb];
-                        // Keep 8-byte reads single: paired into ds_read2_b64,
-                        // a lane's two rows would fall on the same banks.
-                        if constexpr (NB == 2) asm volatile("" ::: "memory");
+                        for (int i = 0; i < NB / NBI; i++) {
+                            const BV v = *(const BV*)(st + CF::b_elem(CF::kslot(ls, h * KP + u), CF::b_col(wn, i * NBI, li)));
+#pragma unroll
+                            for (int nb = 0; nb < NBI; nb++) bf[i * NBI + nb][u] = v[nb];
+                            // Keep 8-byte reads single: paired into ds_read2_b64,
+                            // a lane's two rows would fall on the same banks.
+                            if constexpr (NBI == 2) asm volatile("" ::: "memory");
+                        }
                     }
                 } else {
 #pragma unroll
@@ -394,7 +399,7 @@ k4_mfma(int M, int N, int K, const float* __restrict__ A, int lda, const float* 
             };
             // LDS read instructions of one half's fragments.
             constexpr int RD = (CF::A_KMAJOR ? MB * KP / 4 : MB * KP) +
-                               (CF::B_INTERLEAVE ? KP : CF::B_KMAJOR ? NB * KP / 4 : NB * KP);
+                               (CF::B_INTERLEAVE ? NB / CF::NBH * KP : CF::B_KMAJOR ? NB * KP / 4 : NB * KP);
             constexpr int MF = MB * NB;  // MFMAs per step
             if constexpr (PIPE && NH == 2 && decltype(whole)::value) {
                 static_assert(1 + PER <= 2 * KP * MF, "loads fit between the MFMAs");
@@ -489,17 +494,48 @@ k4_mfma(int M, int N, int K, const float* __restrict__ A, int lda, const float* 
 
         const bool read_c = beta != 0.0f;
         if constexpr (CF::GLU && WK == 1) {
+            // Through LDS (every stage is free after the loop's last barrier),
+            // 16 rows of the wave's columns at a time: a lane then finishes
+            // four neighbouring outputs, with 16-byte stores of up to three
+            // results, in a loop small enough for the instruction cache (the
+            // activation unrolled over the accumulators is not: 4096 x 8192 x
+            // 4096 with G and U kept 4.08 ms).
+            constexpr int COLS = CF::NBH * CF::BLK, PITCH = COLS + 4, RR = CF::MF16 ? 4 : 8;
+            constexpr int LPR = COLS / 4;  // lanes per row
+            static_assert(CF::NWAVES * 2 * 16 * PITCH * 4 <= LDS_TOTAL, "epilogue fits the stages");
+            float* const sg = reinterpret_cast<float*>(smem) + wave * (2 * 16 * PITCH);
+            float* const su = sg + 16 * PITCH;
+            const uintptr_t bits = reinterpret_cast<uintptr_t>(C) | reinterpret_cast<uintptr_t>(tail.G) |
+                                   reinterpret_cast<uintptr_t>(tail.U);
+            const bool vec_h = (bits & 15) == 0 && (ldc & 3) == 0 && (!tail.G || (tail.ldgu & 3) == 0);
 #pragma unroll
             for (int mb = 0; mb < MB; mb++)
 #pragma unroll
-                for (int nb = 0; nb < CF::NBH; nb++)
+                for (int rg = 0; rg < NREG / RR; rg++) {
+                    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                    for (int r = 0; r < NREG; r++) {
-                        const int row = row0 + CF::a_row(wm, mb, 0) + CF::acc_row(ls, r);
-                        const int col = col0 + CF::b_col(wn, nb, li);
-                        const float gv[1] = {acc[mb][nb][r]}, uv[1] = {acc[mb][nb + CF::NBH][r]};
-                        if (row < M) store_glu<1>(tail, C, ldc, row, col, N, gv, uv, false);
+                    for (int nb = 0; nb < CF::NBH; nb++)
+#pragma unroll
+                        for (int r = 0; r < RR; r++) {
+                            const int o = CF::acc_row(ls, r) * PITCH + CF::b_col(0, nb, li);
+                            sg[o] = acc[mb][nb][rg * RR + r];
+                            su[o] = acc[mb][nb + CF::NBH][rg * RR + r];
+                        }
+                    // The wave's own lanes exchange these; its LDS operations
+                    // complete in order.
+                    asm volatile("" ::: "memory");
+                    __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+                    for (int q = lane; q < 16 * LPR; q += 64) {
+                        const int lr = q / LPR, lc = q % LPR * 4;
+                        const int row = row0 + CF::a_row(wm, mb, 0) + rg * 16 + lr;
+                        const v4f gq = *(const v4f*)(sg + lr * PITCH + lc), uq = *(const v4f*)(su + lr * PITCH + lc);
+                        const float gv[4] = {gq[0], gq[1], gq[2], gq[3]}, uv[4] = {uq[0], uq[1], uq[2], uq[3]};
+                        if (row < M) store_glu<4>(tail, C, ldc, row, col0 + wn * CF::TN * 16 + lc, N, gv, uv, vec_h);
                     }
+                    asm volatile("" ::: "memory");
+                }
+            if (t + (int)gridDim.x < tiles) __syncthreads();
             continue;
         }
         if constexpr (WK > 1) {

@@ -43,6 +43,269 @@ hipError_t launch_glu_general(const GluArgs& g, hipStream_t s) {
     return hipGetLastError();
 }
 
+namespace {
+typedef float v4f __attribute__((ext_vector_type(4)));
+constexpr int kThinWaves = 8;  // per workgroup
+
+// Four floats from any 4-byte aligned address.
+__device__ __forceinline__ v4f load4(const float* p) {
+    v4f v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
+}
+
+// Four floats of a row of n from element k, zero past its end.
+__device__ __forceinline__ v4f load4_tail(const float* row, int64_t k, int64_t n) {
+    v4f v;
+#pragma unroll
+    for (int e = 0; e < 4; e++) v[e] = k + e < n ? row[k + e] : 0.0f;
+    return v;
+}
+
+// Sums of V values over the lanes that differ in lane bits OFF, OFF / 2, ...,
+// LAST.  Each step hands half of the values to the partner lane and adds the
+// partner's other half, so V - 1 exchanges do for up to log2 V steps; further
+// steps add the one value left.  Lane l then holds, in v[0 ..], values
+// first ... of the V, first returned.
+template <int OFF, int LAST, int N, int V>
+__device__ __forceinline__ int reduce_lanes(float (&v)[V], int lane) {
+    if constexpr (OFF < LAST) {
+        return 0;
+    } else if constexpr (N > 1) {
+        constexpr int H = N / 2;
+        const bool up = (lane & OFF) != 0;
+#pragma unroll
+        for (int i = 0; i < H; i++) {
+            const float keep = up ? v[i + H] : v[i], send = up ? v[i] : v[i + H];
+            v[i] = keep + __shfl_xor(send, OFF);
+        }
+        return (up ? H : 0) + reduce_lanes<OFF / 2, LAST, H>(v, lane);
+    } else {
+        v[0] += __shfl_xor(v[0], OFF);
+        return reduce_lanes<OFF / 2, LAST, 1>(v, lane);
+    }
+}
+
+// The result at (m, f) from its two finished sums.
+__device__ __forceinline__ void finish(const GluArgs& g, int64_t m, int64_t f, float sg, float su) {
+    g.H[m * g.ldh + f] = act_value(g.act, sg) * su;
+    if (g.G) {
+        g.G[m * g.ldgu + f] = sg;
+        g.U[m * g.ldgu + f] = su;
+    }
+}
+}  // namespace
+
+// One to eight rows of X (MR rounds M up to a power of two; rows past M repeat
+// the last): the weights are read once and bound the time, at two operations
+// per float and row.
+//
+// Weights F x K: a wave owns RF rows of both weights and its lanes split K,
+// four floats each, so its loads are 1 KiB contiguous; WKW waves share K.  X
+// comes from the caches.
+template <int MR, int RF, int WKW>
+__global__ void __launch_bounds__(64 * kThinWaves)
+glu_thin_fk(GluArgs g) {
+    constexpr int V = 2 * MR * RF, GROUPS = kThinWaves / WKW;
+    __shared__ float red[kThinWaves][V];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t f0 = (int64_t(blockIdx.x) * GROUPS + w / WKW) * RF;
+    const float* wrow[2][RF];
+#pragma unroll
+    for (int r = 0; r < RF; r++) {
+        const int64_t f = f0 + r < g.F ? f0 + r : g.F - 1;
+        wrow[0][r] = g.Wg + f * g.ldw;
+        wrow[1][r] = g.Wu + f * g.ldw;
+    }
+    const float* xrow[MR];
+#pragma unroll
+    for (int m = 0; m < MR; m++) xrow[m] = g.X + (m < g.M ? m : g.M - 1) * g.ldx;
+    float acc[V];  // [matrix][row of X][row of the weight]
+#pragma unroll
+    for (int i = 0; i < V; i++) acc[i] = 0.0f;
+    auto add = [&](const v4f (&wv)[2][RF], const v4f (&xv)[MR]) {
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+            for (int m = 0; m < MR; m++)
+#pragma unroll
+                for (int r = 0; r < RF; r++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        acc[(t * MR + m) * RF + r] = fmaf(xv[m][e], wv[t][r][e], acc[(t * MR + m) * RF + r]);
+    };
+    auto loadw = [&](v4f (&wv)[2][RF], int64_t k) {
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+            for (int r = 0; r < RF; r++) wv[t][r] = load4(wrow[t][r] + k);
+    };
+    const int64_t step = 256 * WKW, k0 = (w % WKW) * 256 + lane * 4;
+    int64_t k = k0;
+    v4f wv[2][RF];
+    if (k + 4 <= g.K) loadw(wv, k);
+    for (; k + 4 <= g.K; k += step) {
+        v4f xv[MR], next[2][RF];
+#pragma unroll
+        for (int m = 0; m < MR; m++) xv[m] = load4(xrow[m] + k);
+        const bool more = k + step + 4 <= g.K;
+        if (more) loadw(next, k + step);
+        add(wv, xv);
+        if (more) {
+#pragma unroll
+            for (int t = 0; t < 2; t++)
+#pragma unroll
+                for (int r = 0; r < RF; r++) wv[t][r] = next[t][r];
+        }
+    }
+    if (k < g.K) {  // one lane at most: the row's last, incomplete four
+        v4f xv[MR];
+#pragma unroll
+        for (int m = 0; m < MR; m++) xv[m] = load4_tail(xrow[m], k, g.K);
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+            for (int r = 0; r < RF; r++) wv[t][r] = load4_tail(wrow[t][r], k, g.K);
+        add(wv, xv);
+    }
+    constexpr int HELD = V > 64 ? V / 64 : 1;
+    const int first = reduce_lanes<32, 1, V>(acc, lane);
+#pragma unroll
+    for (int i = 0; i < HELD; i++) red[w][first + i] = acc[i];
+    __syncthreads();
+    for (int o = threadIdx.x; o < GROUPS * MR * RF; o += blockDim.x) {
+        const int grp = o / (MR * RF), m = o / RF % MR, r = o % RF;
+        const int64_t f = (int64_t(blockIdx.x) * GROUPS + grp) * RF + r;
+        if (m >= g.M || f >= g.F) continue;
+        float s[2];
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+            s[t] = red[grp * WKW][(t * MR + m) * RF + r];
+            for (int q = 1; q < WKW; q++) s[t] += red[grp * WKW + q][(t * MR + m) * RF + r];
+        }
+        finish(g, m, f, s[0], s[1]);
+    }
+}
+
+// Weights K x F: a lane owns four columns of both weights, LC lanes a stretch
+// of 4 LC columns, and the 64 / LC lane groups of the waves deal out K in blocks
+// of four rows, whose X values are then one load per row of X.
+template <int MR, int LC, int NW>
+__global__ void __launch_bounds__(64 * NW)
+glu_thin_kf(GluArgs g) {
+    constexpr int KG = 64 / LC, V = 8 * MR, HELD = V / KG > 0 ? V / KG : 1;
+    __shared__ float red[NW][LC][V];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lc = lane % LC, kg = lane / LC;
+    const int64_t c0 = int64_t(blockIdx.x) * (4 * LC) + lc * 4;
+    // Lanes at the end of a row take its last four columns again.
+    const int64_t c = c0 + 4 <= g.F ? c0 : g.F - 4;
+    const float* xrow[MR];
+#pragma unroll
+    for (int m = 0; m < MR; m++) xrow[m] = g.X + (m < g.M ? m : g.M - 1) * g.ldx;
+    float acc[V];  // [matrix][row of X][column]
+#pragma unroll
+    for (int i = 0; i < V; i++) acc[i] = 0.0f;
+    auto add = [&](const v4f (&wv)[2][4], const v4f (&xv)[MR]) {
+#pragma unroll
+        for (int q = 0; q < 4; q++)
+#pragma unroll
+            for (int t = 0; t < 2; t++)
+#pragma unroll
+                for (int m = 0; m < MR; m++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        acc[(t * MR + m) * 4 + e] = fmaf(xv[m][q], wv[t][q][e], acc[(t * MR + m) * 4 + e]);
+    };
+    auto loadw = [&](v4f (&wv)[2][4], int64_t k) {
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            wv[0][q] = load4(g.Wg + (k + q) * g.ldw + c);
+            wv[1][q] = load4(g.Wu + (k + q) * g.ldw + c);
+        }
+    };
+    const int64_t step = 4 * KG * NW;
+    int64_t k = (int64_t(w) * KG + kg) * 4;
+    v4f wv[2][4];
+    if (k + 4 <= g.K) loadw(wv, k);
+    for (; k + 4 <= g.K; k += step) {
+        v4f xv[MR], next[2][4];
+#pragma unroll
+        for (int m = 0; m < MR; m++) xv[m] = load4(xrow[m] + k);
+        const bool more = k + step + 4 <= g.K;
+        if (more) loadw(next, k + step);
+        add(wv, xv);
+        if (more) {
+#pragma unroll
+            for (int q = 0; q < 4; q++) wv[0][q] = next[0][q], wv[1][q] = next[1][q];
+        }
+    }
+    if (k < g.K) {  // the last, incomplete block of rows
+        v4f xv[MR];
+#pragma unroll
+        for (int m = 0; m < MR; m++) xv[m] = load4_tail(xrow[m], k, g.K);
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const bool in = k + q < g.K;
+            wv[0][q] = in ? load4(g.Wg + (k + q) * g.ldw + c) : v4f{0.0f, 0.0f, 0.0f, 0.0f};
+            wv[1][q] = in ? load4(g.Wu + (k + q) * g.ldw + c) : v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        add(wv, xv);
+    }
+    const int first = reduce_lanes<32, LC, V>(acc, lane);
+#pragma unroll
+    for (int i = 0; i < HELD; i++) red[w][lc][first + i] = acc[i];
+    __syncthreads();
+    for (int o = threadIdx.x; o < MR * LC * 4; o += blockDim.x) {
+        const int m = o / (LC * 4), l = o / 4 % LC, e = o % 4;
+        const int64_t l0 = int64_t(blockIdx.x) * (4 * LC) + l * 4;
+        if (m >= g.M || l0 >= g.F) continue;
+        const int64_t f = (l0 + 4 <= g.F ? l0 : g.F - 4) + e;
+        if (f < l0) continue;  // another lane's column
+        float s[2];
+#pragma unroll
+        for (int t = 0; t < 2; t++) {
+            s[t] = red[0][l][(t * MR + m) * 4 + e];
+            for (int q = 1; q < NW; q++) s[t] += red[q][l][(t * MR + m) * 4 + e];
+        }
+        finish(g, m, f, s[0], s[1]);
+    }
+}
+
+template <int MR>
+static hipError_t launch_thin_mr(const GluArgs& g, hipStream_t s) {
+    if (g.transw) {
+        constexpr int RF = MR >= 4 ? 4 : 2;
+        // Few rows of weights: more waves share K.
+        if (g.F >= 4096) {
+            constexpr int W = 1;
+            const dim3 grid(unsigned(ceil_div(g.F, RF * kThinWaves / W)));
+            hipLaunchKernelGGL((glu_thin_fk<MR, RF, W>), grid, dim3(64 * kThinWaves), 0, s, g);
+        } else {
+            constexpr int W = 4;
+            const dim3 grid(unsigned(ceil_div(g.F, RF * kThinWaves / W)));
+            hipLaunchKernelGGL((glu_thin_fk<MR, RF, W>), grid, dim3(64 * kThinWaves), 0, s, g);
+        }
+    } else {
+        constexpr int NW = MR <= 2 ? 16 : 8;
+        hipLaunchKernelGGL((glu_thin_kf<MR, 8, NW>), dim3(unsigned(ceil_div(g.F, 32))), dim3(64 * NW), 0, s, g);
+    }
+    return hipGetLastError();
+}
+
+bool glu_thin_ok(const GluArgs& g) {
+    // The grids' work-items (at most 256 and 32 per row or column of weights)
+    // stay below 2^32.
+    return g.M <= 8 && g.F < (int64_t(1) << 24) && (g.transw || g.F >= 4);
+}
+
+hipError_t launch_glu_thin(const GluArgs& g, hipStream_t s) {
+    if (g.M == 1) return launch_thin_mr<1>(g, s);
+    if (g.M == 2) return launch_thin_mr<2>(g, s);
+    if (g.M <= 4) return launch_thin_mr<4>(g, s);
+    return launch_thin_mr<8>(g, s);
+}
+
 // dG and dU; each may be stored over G, U or dH (every lane reads its three
 // inputs before it stores).
 __global__ void __launch_bounds__(256)

@@ -497,6 +497,7 @@ static GemmArgs glu_product(const GluArgs& g) {
 }
 
 hipError_t launch_glu(const GluArgs& g, hipStream_t s) {
+    if (glu_thin_ok(g)) return launch_glu_thin(g, s);
     GemmArgs p = glu_product(g), one = p;
     one.N = g.F;
     if (!k4_supports(p) || !k4_supports(one)) return launch_glu_general(g, s);

@@ -6,6 +6,8 @@
 #pragma once
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 namespace sgemm {
 
 // sgemm_act_t
@@ -26,6 +28,22 @@ __device__ __forceinline__ float act_value(int act, float g) {
         case ACT_GELU_TANH: return g * logistic(gelu_tanh_arg2(g));
         case ACT_RELU: return g <= 0.0f ? 0.0f : g;  // NaN stays NaN
         default: return logistic(g);
+    }
+}
+
+// N activations with one branch on which.
+template <int N>
+__device__ __forceinline__ void act_values(int act, const float (&g)[N], float (&a)[N]) {
+    auto all = [&](auto which) {
+#pragma unroll
+        for (int i = 0; i < N; i++) a[i] = act_value(decltype(which)::value, g[i]);
+    };
+    switch (act) {
+        case ACT_SILU: return all(std::integral_constant<int, ACT_SILU>{});
+        case ACT_GELU: return all(std::integral_constant<int, ACT_GELU>{});
+        case ACT_GELU_TANH: return all(std::integral_constant<int, ACT_GELU_TANH>{});
+        case ACT_RELU: return all(std::integral_constant<int, ACT_RELU>{});
+        default: return all(std::integral_constant<int, ACT_SIGMOID>{});
     }
 }
 

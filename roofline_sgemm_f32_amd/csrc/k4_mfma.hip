@@ -103,34 +103,33 @@ __device__ __forceinline__ const float* second_b(const float* B, const Tail& tai
     else return B;
 }
 
-// Store n (1, 2 or 4) neighbouring outputs of the gated form from their two
-// sums; vec: every output row suits accesses of n floats.
+// Store NV neighbouring outputs of the gated form from their two sums, as one
+// access each where they all lie in the row (any 4-byte alignment).
 template <int NV>
 __device__ __forceinline__ void store_glu(const GluTail& tail, float* H, int64_t ldh, int row, int col, int N,
-                                          const float (&g)[NV], const float (&u)[NV], bool vec) {
+                                          const float (&g)[NV], const float (&u)[NV]) {
+    typedef float vt __attribute__((ext_vector_type(NV), aligned(4)));
     float h[NV];
+    act_values<NV>(tail.act, g, h);
 #pragma unroll
-    for (int e = 0; e < NV; e++) h[e] = act_value(tail.act, g[e]) * u[e];
-    float* hp = H + (int64_t)row * ldh + col;
-    float* gp = tail.G ? tail.G + (int64_t)row * tail.ldgu + col : nullptr;
-    float* up = tail.G ? tail.U + (int64_t)row * tail.ldgu + col : nullptr;
-    if constexpr (NV > 1) {
-        typedef float vt __attribute__((ext_vector_type(NV)));
-        if (vec && col + NV <= N) {
-            vt a, b, c;
+    for (int e = 0; e < NV; e++) h[e] *= u[e];
+    auto put = [&](float* p, const float (&v)[NV]) {
+        if (col + NV <= N) {
+            vt w;
 #pragma unroll
-            for (int e = 0; e < NV; e++) a[e] = h[e], b[e] = g[e], c[e] = u[e];
-            *(vt*)hp = a;
-            if (gp) *(vt*)gp = b, *(vt*)up = c;
-            return;
+            for (int e = 0; e < NV; e++) w[e] = v[e];
+            *reinterpret_cast<vt*>(p) = w;
+        } else {
+#pragma unroll
+            for (int e = 0; e < NV; e++)
+                if (col + e < N) p[e] = v[e];
         }
+    };
+    put(H + (int64_t)row * ldh + col, h);
+    if (tail.G) {
+        put(tail.G + (int64_t)row * tail.ldgu + col, g);
+        put(tail.U + (int64_t)row * tail.ldgu + col, u);
     }
-#pragma unroll
-    for (int e = 0; e < NV; e++)
-        if (col + e < N) {
-            hp[e] = h[e];
-            if (gp) gp[e] = g[e], up[e] = u[e];
-        }
 }
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const float* base) {
@@ -505,9 +504,6 @@ k4_mfma(int M, int N, int K, const float* __restrict__ A, int lda, const float* 
             static_assert(CF::NWAVES * 2 * 16 * PITCH * 4 <= LDS_TOTAL, "epilogue fits the stages");
             float* const sg = reinterpret_cast<float*>(smem) + wave * (2 * 16 * PITCH);
             float* const su = sg + 16 * PITCH;
-            const uintptr_t bits = reinterpret_cast<uintptr_t>(C) | reinterpret_cast<uintptr_t>(tail.G) |
-                                   reinterpret_cast<uintptr_t>(tail.U);
-            const bool vec_h = (bits & 15) == 0 && (ldc & 3) == 0 && (!tail.G || (tail.ldgu & 3) == 0);
 #pragma unroll
             for (int mb = 0; mb < MB; mb++)
 #pragma unroll
@@ -531,7 +527,7 @@ k4_mfma(int M, int N, int K, const float* __restrict__ A, int lda, const float* 
                         const int row = row0 + CF::a_row(wm, mb, 0) + rg * 16 + lr;
                         const v4f gq = *(const v4f*)(sg + lr * PITCH + lc), uq = *(const v4f*)(su + lr * PITCH + lc);
                         const float gv[4] = {gq[0], gq[1], gq[2], gq[3]}, uv[4] = {uq[0], uq[1], uq[2], uq[3]};
-                        if (row < M) store_glu<4>(tail, C, ldc, row, col0 + wn * CF::TN * 16 + lc, N, gv, uv, vec_h);
+                        if (row < M) store_glu<4>(tail, C, ldc, row, col0 + wn * CF::TN * 16 + lc, N, gv, uv);
                     }
                     asm volatile("" ::: "memory");
                 }
@@ -569,9 +565,6 @@ k4_mfma(int M, int N, int K, const float* __restrict__ A, int lda, const float* 
                 // Two neighbouring outputs a lane: four sums over the groups.
                 constexpr int PAIRS = CF::BM * CF::BH / (2 * CF::THREADS * WK);
                 static_assert(PAIRS * 2 * CF::THREADS * WK == CF::BM * CF::BH, "whole pairs per lane");
-                const bool vec_h = ((reinterpret_cast<uintptr_t>(C) | reinterpret_cast<uintptr_t>(tail.G) |
-                                     reinterpret_cast<uintptr_t>(tail.U)) & 7) == 0 &&
-                                   (ldc & 1) == 0 && (!tail.G || (tail.ldgu & 1) == 0);
 #pragma unroll
                 for (int q = 0; q < PAIRS; q++) {
                     const int o = (tid + q * CF::THREADS * WK) * 2, row = o / CF::BH, col = o % CF::BH;
@@ -582,7 +575,7 @@ k4_mfma(int M, int N, int K, const float* __restrict__ A, int lda, const float* 
                         su += *(const v2f*)(red + (g * CF::BM + row) * RLD + CF::BH + col);
                     }
                     const float gv[2] = {sg[0], sg[1]}, uv[2] = {su[0], su[1]};
-                    if (row0 + row < M) store_glu<2>(tail, C, ldc, row0 + row, col0 + col, N, gv, uv, vec_h);
+                    if (row0 + row < M) store_glu<2>(tail, C, ldc, row0 + row, col0 + col, N, gv, uv);
                 }
                 if (t + (int)gridDim.x < tiles) __syncthreads();
                 continue;

@@ -202,6 +202,28 @@ struct PackPlan {
 };
 }  // namespace
 
+// Worth a copy launch: outputs of at least 512 tiles of 64 x 64; or a
+// product moving 64 MB or more whose copies are at most 1/8 of that, as
+// when a narrow or thin operand is the only unaligned one (8192 x 13 x
+// 8192: 82 -> 61 us; 13 x 8192 x 8191); or 4 GFLOP or more with copies
+// of at most 64 MB and 1 byte per 100 FLOP (767 x 769 x 4095: 91 -> 72
+// us; 1025 x 1025 x 2047: 78 -> 70), or with K >= 1536 from 1 GFLOP
+// (511 x 513 x 4095: 72 -> 42 us; 800 x 801 x 2047: 48.3 -> 43.3; 767 x
+// 769 x 2047: 48.1 -> 43.6).  The copy launch and the wait for it cost
+// about 9 us at 8 MB, so it did not pay for shorter K (1023^3: 32.2 ->
+// 33.0 us; 1024 x 1027 x 1024: 41.6 -> 42.1; 1023^2 x 511: 19.3 -> 20.7),
+// nor where a large operand of a memory-bound product is copied (1 x 8191
+// x 8192: 79 -> 144).
+static bool worth_packing(const GemmArgs& g, double copied) {
+    const double moved = 4.0 * (double(g.M) * g.K + double(g.K) * g.N + double(g.M) * g.N);
+    const double flop = 2.0 * double(g.M) * double(g.N) * double(g.K);
+    const bool big_output = ceil_div(g.M, 64) * ceil_div(g.N, 64) >= 512;
+    const bool thin_copy = moved >= 64e6 && copied <= moved / 8;
+    const bool heavy = (flop >= 4e9 || (flop >= 1e9 && g.K >= 1536)) && copied <= 64e6 &&
+                       copied <= flop / 100;
+    return big_output || thin_copy || heavy;
+}
+
 // Whether an eager shape-chosen call packs g's operands first, and then how.
 // The plan depends on the copies' addresses only through their 16-byte
 // alignment, which the workspace layout gives; until the copies exist gp
@@ -227,26 +249,7 @@ static bool packing_plan(const GemmArgs& g, PackPlan* pk) {
         pk->b_bytes = (size_t(pk->b_rows * gp.ldb) * sizeof(float) + 255) / 256 * 256;
     }
     if (!k4_supports(gp)) return false;
-    // Worth a copy launch: outputs of at least 512 tiles of 64 x 64; or a
-    // product moving 64 MB or more whose copies are at most 1/8 of that, as
-    // when a narrow or thin operand is the only unaligned one (8192 x 13 x
-    // 8192: 82 -> 61 us; 13 x 8192 x 8191); or 4 GFLOP or more with copies
-    // of at most 64 MB and 1 byte per 100 FLOP (767 x 769 x 4095: 91 -> 72
-    // us; 1025 x 1025 x 2047: 78 -> 70), or with K >= 1536 from 1 GFLOP
-    // (511 x 513 x 4095: 72 -> 42 us; 800 x 801 x 2047: 48.3 -> 43.3; 767 x
-    // 769 x 2047: 48.1 -> 43.6).  The copy launch and the wait for it cost
-    // about 9 us at 8 MB, so it did not pay for shorter K (1023^3: 32.2 ->
-    // 33.0 us; 1024 x 1027 x 1024: 41.6 -> 42.1; 1023^2 x 511: 19.3 -> 20.7),
-    // nor where a large operand of a memory-bound product is copied (1 x 8191
-    // x 8192: 79 -> 144).
-    const double moved = 4.0 * (double(g.M) * g.K + double(g.K) * g.N + double(g.M) * g.N);
-    const double flop = 2.0 * double(g.M) * double(g.N) * double(g.K);
-    const double copied = double(pk->a_bytes + pk->b_bytes);
-    const bool big_output = ceil_div(g.M, 64) * ceil_div(g.N, 64) >= 512;
-    const bool thin_copy = moved >= 64e6 && copied <= moved / 8;
-    const bool heavy = (flop >= 4e9 || (flop >= 1e9 && g.K >= 1536)) && copied <= 64e6 &&
-                       copied <= flop / 100;
-    if (!big_output && !thin_copy && !heavy) return false;
+    if (!worth_packing(g, double(pk->a_bytes + pk->b_bytes))) return false;
     pk->p = k4_plan(gp, 0);
     pk->gp = gp;
     return true;
@@ -501,11 +504,47 @@ hipError_t launch_glu(const GluArgs& g, hipStream_t s) {
     GemmArgs p = glu_product(g), one = p;
     one.N = g.F;
     if (!k4_supports(p) || !k4_supports(one)) return launch_glu_general(g, s);
-    const bool vec = vec_ok(one) && rows_vec(g.Wu, g.ldw, g.transw ? g.K : g.F);
+    const bool x_vec = rows_vec(g.X, g.ldx, g.K);
+    const int64_t w_rows = g.transw ? g.F : g.K, w_run = g.transw ? g.K : g.F;
+    const bool w_vec = rows_vec(g.Wg, g.ldw, w_run) && rows_vec(g.Wu, g.ldw, w_run);
+    if (x_vec && w_vec) return launch_k4_glu(g, k4_plan(p, 1).cfg, true, s);
+
+    // Packed copies, as the product's own path makes them and under the same
+    // conditions: X, then both weights.
+    const auto bytes = [](int64_t rows, int64_t run) {
+        return (size_t(rows * packed_ld(run)) * sizeof(float) + 255) / 256 * 256;
+    };
+    const size_t x_bytes = x_vec ? 0 : bytes(g.M, g.K), w_bytes = w_vec ? 0 : bytes(w_rows, w_run);
+    Workspace ws;
+    if (worth_packing(p, double(x_bytes + 2 * w_bytes)) && !capturing(s)) {
+        if (workspace_acquire(x_bytes + 2 * w_bytes, s, &ws) == hipSuccess) {
+            char* base = static_cast<char*>(ws.ptr);
+            GluArgs q = g;
+            hipError_t e = hipSuccess;
+            if (!x_vec) {
+                q.X = reinterpret_cast<float*>(base);
+                q.ldx = packed_ld(g.K);
+                e = launch_pack(g.X, g.M, g.K, g.ldx, reinterpret_cast<float*>(base), nullptr, 0, 0, 0, nullptr, s);
+            }
+            if (!w_vec && e == hipSuccess) {
+                float *pg = reinterpret_cast<float*>(base + x_bytes), *pu = reinterpret_cast<float*>(base + x_bytes + w_bytes);
+                q.Wg = pg;
+                q.Wu = pu;
+                q.ldw = packed_ld(w_run);
+                e = launch_pack(g.Wg, w_rows, w_run, g.ldw, pg, g.Wu, w_rows, w_run, g.ldw, pu, s);
+            }
+            GemmArgs pp = glu_product(q);
+            pp.runs_padded = true;
+            if (e == hipSuccess) e = launch_k4_glu(q, k4_plan(pp, 1).cfg, true, s);
+            const hipError_t f = workspace_release(&ws, s);
+            return e != hipSuccess ? e : f;
+        }
+        (void)hipGetLastError();
+    }
     // The plan sees alignment through the product's operands: an unaligned up
     // weight counts as an unaligned gate weight.
-    if (!vec) p.B = reinterpret_cast<const float*>(uintptr_t(4));
-    return launch_k4_glu(g, k4_plan(p, 1).cfg, vec, s);
+    if (!w_vec) p.B = reinterpret_cast<const float*>(uintptr_t(4));
+    return launch_k4_glu(g, k4_plan(p, 1).cfg, false, s);
 }
 
 }  // namespace sgemm

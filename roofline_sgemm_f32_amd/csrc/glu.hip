@@ -307,24 +307,45 @@ hipError_t launch_glu_thin(const GluArgs& g, hipStream_t s) {
 }
 
 // dG and dU; each may be stored over G, U or dH (every lane reads its three
-// inputs before it stores).
+// inputs before it stores, and no other lane reads them).  A lane takes four
+// columns of a row at a time: five streams of one access each, bound by memory
+// (20 bytes per element).
 __global__ void __launch_bounds__(256)
 glu_pregrad(int act, int64_t M, int64_t F, const float* G, const float* U, int64_t ldgu,
-            const float* dH, int64_t lddh, float* dG, float* dU, int64_t lddgu) {
-    const int64_t total = M * F, stride = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += stride) {
-        const int64_t r = i / F, c = i % F;
+            const float* dH, int64_t lddh, float* dG, float* dU, int64_t lddgu, int64_t strips,
+            int64_t tiles) {
+    typedef float v4u __attribute__((ext_vector_type(4), aligned(4)));
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int64_t r = t / strips, c = (t - r * strips) * 1024 + threadIdx.x * 4;
+        const float *gp = G + r * ldgu + c, *up = U + r * ldgu + c, *hp = dH + r * lddh + c;
+        float *gq = dG + r * lddgu + c, *uq = dU + r * lddgu + c;
         float a, da;
-        act_grad(act, G[r * ldgu + c], &a, &da);
-        const float d = dH[r * lddh + c], u = U[r * ldgu + c];
-        dG[r * lddgu + c] = d * u * da;
-        dU[r * lddgu + c] = d * a;
+        if (c + 4 <= F) {
+            const v4u g = *(const v4u*)gp, u = *(const v4u*)up, d = *(const v4u*)hp;
+            v4u og, ou;
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                act_grad(act, g[e], &a, &da);
+                og[e] = d[e] * u[e] * da;
+                ou[e] = d[e] * a;
+            }
+            *(v4u*)gq = og;
+            *(v4u*)uq = ou;
+        } else {
+            for (int64_t e = 0; c + e < F; e++) {
+                const float d = hp[e], u = up[e];
+                act_grad(act, gp[e], &a, &da);
+                gq[e] = d * u * da;
+                uq[e] = d * a;
+            }
+        }
     }
 }
 
-hipError_t launch_glu_pregrad(const GluGradArgs& g, hipStream_t s) {
-    hipLaunchKernelGGL(glu_pregrad, dim3(grid_for(ceil_div(g.M * g.F, 256))), dim3(256), 0, s,
-                       g.act, g.M, g.F, g.G, g.U, g.ldgu, g.dH, g.lddh, g.dG, g.dU, g.lddgu);
+static hipError_t launch_glu_pregrad(const GluGradArgs& g, hipStream_t s) {
+    const int64_t strips = ceil_div(g.F, 1024), tiles = g.M * strips;
+    hipLaunchKernelGGL(glu_pregrad, dim3(grid_for(tiles)), dim3(256), 0, s, g.act, g.M, g.F, g.G, g.U,
+                       g.ldgu, g.dH, g.lddh, g.dG, g.dU, g.lddgu, strips, tiles);
     return hipGetLastError();
 }
 

@@ -104,10 +104,13 @@ __device__ __forceinline__ const float* second_b(const float* B, const Tail& tai
 }
 
 // Store NV neighbouring outputs of the gated form from their two sums, as one
-// access each where they all lie in the row (any 4-byte alignment).
+// access each where they all lie in the row (any 4-byte alignment).  nt:
+// non-temporal stores, for results whose rows are all 16-byte aligned (4096 x
+// 8192 x 4096 about 1 % faster; rows that share cache lines lose by it, 3001 x
+// 4099 x 2047 812 -> 854 us).
 template <int NV>
 __device__ __forceinline__ void store_glu(const GluTail& tail, float* H, int64_t ldh, int row, int col, int N,
-                                          const float (&g)[NV], const float (&u)[NV]) {
+                                          const float (&g)[NV], const float (&u)[NV], bool nt) {
     typedef float vt __attribute__((ext_vector_type(NV), aligned(4)));
     float h[NV];
     act_values<NV>(tail.act, g, h);
@@ -118,7 +121,8 @@ __device__ __forceinline__ void store_glu(const GluTail& tail, float* H, int64_t
             vt w;
 #pragma unroll
             for (int e = 0; e < NV; e++) w[e] = v[e];
-            *reinterpret_cast<vt*>(p) = w;
+            if (nt) __builtin_nontemporal_store(w, reinterpret_cast<vt*>(p));
+            else *reinterpret_cast<vt*>(p) = w;
         } else {
 #pragma unroll
             for (int e = 0; e < NV; e++)
@@ -504,6 +508,9 @@ k4_mfma(int M, int N, int K, const float* __restrict__ A, int lda, const float* 
             static_assert(CF::NWAVES * 2 * 16 * PITCH * 4 <= LDS_TOTAL, "epilogue fits the stages");
             float* const sg = reinterpret_cast<float*>(smem) + wave * (2 * 16 * PITCH);
             float* const su = sg + 16 * PITCH;
+            const uintptr_t bits = reinterpret_cast<uintptr_t>(C) | reinterpret_cast<uintptr_t>(tail.G) |
+                                   reinterpret_cast<uintptr_t>(tail.U);
+            const bool nt = (bits & 15) == 0 && (ldc & 3) == 0 && (!tail.G || (tail.ldgu & 3) == 0);
 #pragma unroll
             for (int mb = 0; mb < MB; mb++)
 #pragma unroll
@@ -527,7 +534,7 @@ k4_mfma(int M, int N, int K, const float* __restrict__ A, int lda, const float* 
                         const int row = row0 + CF::a_row(wm, mb, 0) + rg * 16 + lr;
                         const v4f gq = *(const v4f*)(sg + lr * PITCH + lc), uq = *(const v4f*)(su + lr * PITCH + lc);
                         const float gv[4] = {gq[0], gq[1], gq[2], gq[3]}, uv[4] = {uq[0], uq[1], uq[2], uq[3]};
-                        if (row < M) store_glu<4>(tail, C, ldc, row, col0 + wn * CF::TN * 16 + lc, N, gv, uv);
+                        if (row < M) store_glu<4>(tail, C, ldc, row, col0 + wn * CF::TN * 16 + lc, N, gv, uv, nt);
                     }
                     asm volatile("" ::: "memory");
                 }
@@ -575,7 +582,7 @@ k4_mfma(int M, int N, int K, const float* __restrict__ A, int lda, const float* 
                         su += *(const v2f*)(red + (g * CF::BM + row) * RLD + CF::BH + col);
                     }
                     const float gv[2] = {sg[0], sg[1]}, uv[2] = {su[0], su[1]};
-                    if (row0 + row < M) store_glu<2>(tail, C, ldc, row0 + row, col0 + col, N, gv, uv);
+                    if (row0 + row < M) store_glu<2>(tail, C, ldc, row0 + row, col0 + col, N, gv, uv, false);
                 }
                 if (t + (int)gridDim.x < tiles) __syncthreads();
                 continue;

@@ -499,14 +499,15 @@ static hipError_t launch_rows(const Q4Args& g, hipStream_t s) {
 // all waves of the group read, is staged in LDS in slabs of 64 k as the
 // instruction takes it (float X split on the way), two slabs in turn with one
 // barrier each.
-// LDS of a slab: TM x 4 steps x P parts of 1 KiB (lane L's 16 bytes at 16 L:
-// row L % 32, eight k of half L / 32), 64 bytes apart so that the pieces a
-// wave writes at once (8 pieces of 8 rows) spread over the banks.
+// LDS of a slab: TM x 4 steps x P parts of two halves of 512 bytes (row L % 32
+// of half L / 32 at 16 (L % 32): eight k each).  Halves are 128 bytes further
+// apart than that and parts 32 (modulo the banks' 256), so that the 8 pieces
+// each of two rows that 16 lanes write at once fall on different banks.
 template <int XT, int GS, int NWT, int TM, int WN, int WK, bool S32>
 __global__ void __launch_bounds__(64 * WN * WK)
 q4_tile(Q4Args g, int tiles_m, int tiles_n) {
     constexpr int P = parts<XT>(), NS = 4 / GS, BM = 32 * TM, BN = 32 * WN;
-    constexpr int FRAG = 1024 + 64, SLAB = TM * 4 * P * FRAG;
+    constexpr int HALF = 512 + 128, FRAG = 5 * 256 + 32, SLAB = TM * 4 * P * FRAG;
     constexpr int RED = WK > 1 ? (WK - 1) * WN * NWT * TM * 4096 : 0;
     constexpr int LDS = 2 * WK * SLAB > RED ? 2 * WK * SLAB : RED;
     constexpr int PIECES = BM * 8 / (64 * WN);  // of 8 elements, per lane and slab
@@ -608,7 +609,7 @@ q4_tile(Q4Args g, int tiles_m, int tiles_n) {
                 operand_x<XT>(x[p], out);
 #pragma unroll
                 for (int q = 0; q < P; q++)
-                    *reinterpret_cast<u32x4*>(base + ((m / 32 * 4 + kk / 2) * P + q) * FRAG + (kk % 2 * 32 + m % 32) * 16) = out[q];
+                    *reinterpret_cast<u32x4*>(base + ((m / 32 * 4 + kk / 2) * P + q) * FRAG + kk % 2 * HALF + m % 32 * 16) = out[q];
             }
         };
 
@@ -643,7 +644,7 @@ q4_tile(Q4Args g, int tiles_m, int tiles_n) {
         static_assert(TM * PIECE == 4, "four words of a step's weights over TM pieces");
         auto do_slab = [&](const Unit& u, int buf, auto hc) {
             constexpr int h = decltype(hc)::value, PER = 2 * GS;  // PER: steps that share a scale
-            const char* base = smem + (buf * WK + kg) * SLAB + lane * 16;
+            const char* base = smem + (buf * WK + kg) * SLAB + half * HALF + r * 16;
             u32x4 x[RING][P], q[2][NWT];
             auto read = [&](int c) {
                 const int j = c / TM, b = c % TM;
@@ -797,7 +798,9 @@ static hipError_t launch_tiles(const Q4Args& g, hipStream_t s) {
     constexpr bool f = XT == T_F32;
     const int64_t big = ceil_div(g.M, NWT == 2 ? 64 : 128) * ceil_div(g.N, 256);
     if (big >= 200) return launch_tile<XT, GS, NWT, NWT == 2 ? 2 : 4, 8, 1>(g, s);
-    if (ceil_div(g.M, 64) * ceil_div(g.N, 64) >= 200 && NWT == 1) return launch_tile<XT, GS, NWT, 2, 2, f ? 2 : 4>(g, s);
+    if constexpr (NWT == 1) {
+        if (ceil_div(g.M, 64) * ceil_div(g.N, 64) >= 200) return launch_tile<XT, GS, NWT, 2, 2, f ? 2 : 4>(g, s);
+    }
     return launch_tile<XT, GS, NWT, 1, 1, f ? 4 : 8>(g, s);
 }
 

@@ -29,6 +29,7 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kUnit = 128;      // K per step of a wave: 4 lane groups of 32 weights
+constexpr int64_t kRowsLds = 80 * 1024;  // LDS of a q4_rows workgroup: half a CU's
 constexpr int kRowsMax = 8;     // rows of X of one q4_rows workgroup
 
 // bfloat16 parts of X for the matrix cores: 3 for float, 1 for 16-bit types.
@@ -150,12 +151,14 @@ __device__ __forceinline__ u32x4 order_x(u32x4 x) {
 
 // A float as three bfloat16 parts (each a float whose lower half is zero):
 // the upper 8 bits of its mantissa, of the rest, and of what is left, which
-// has no more than 8.  An infinity is its own first part (the differences
-// would be NaN); a NaN becomes a quiet one, whose mark is in the upper half.
+// has no more than 8.  Where a value may not be finite (FINITE false) an
+// infinity is its own first part (the differences would be NaN), and a NaN
+// becomes a quiet one, whose mark is in the upper half.
+template <bool FINITE>
 __device__ __forceinline__ void split3(float x, float (&p)[3]) {
-    x = __builtin_canonicalizef(x);
+    if (!FINITE) x = __builtin_canonicalizef(x);
     p[0] = __uint_as_float(__float_as_uint(x) & 0xFFFF0000u);
-    const float r = __builtin_isinf(x) ? 0.0f : x - p[0];
+    const float r = !FINITE && __builtin_isinf(x) ? 0.0f : x - p[0];
     p[1] = __uint_as_float(__float_as_uint(r) & 0xFFFF0000u);
     p[2] = r - p[1];
 }
@@ -193,15 +196,24 @@ __device__ __forceinline__ void load_x_checked(const void* p, int left, RawX<XT>
 template <int XT>
 __device__ __forceinline__ void operand_x(const RawX<XT>& raw, u32x4 (&out)[parts<XT>()]) {
     if constexpr (XT == T_F32) {
+        auto split = [&](auto finite) {
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-            float a[3], b[3];
-            split3(__uint_as_float(raw.v[e / 2][2 * (e % 2)]), a);
-            split3(__uint_as_float(raw.v[e / 2][2 * (e % 2) + 1]), b);
+            for (int e = 0; e < 4; e++) {
+                float a[3], b[3];
+                split3<decltype(finite)::value>(__uint_as_float(raw.v[e / 2][2 * (e % 2)]), a);
+                split3<decltype(finite)::value>(__uint_as_float(raw.v[e / 2][2 * (e % 2) + 1]), b);
 #pragma unroll
-            for (int p = 0; p < 3; p++)
-                out[p][e] = __builtin_amdgcn_perm(__float_as_uint(b[p]), __float_as_uint(a[p]), 0x07060302u);
-        }
+                for (int p = 0; p < 3; p++)
+                    out[p][e] = __builtin_amdgcn_perm(__float_as_uint(b[p]), __float_as_uint(a[p]), 0x07060302u);
+            }
+        };
+        // 0 times each value, added up, is 0 unless one is not finite: a third
+        // fewer operations than treating every value as if it might be.
+        float zero = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; e++) zero = fmaf(__uint_as_float(raw.v[e / 4][e % 4]), 0.0f, zero);
+        if (__any(zero != 0.0f)) split(std::false_type{});
+        else split(std::true_type{});
     } else {
         out[0] = order_x<XT>(raw.v[0]);
     }
@@ -271,20 +283,21 @@ struct ScaleZero {
     uint32_t z;
 };
 
-template <int XT, int GS, int NWT, int PF>
-__global__ void __launch_bounds__(512, 4)
-q4_rows(Q4Args g, int chunk, int64_t tiles_m, int64_t tiles) {
+template <int XT, int GS, int NWT, int PF, int NW>
+__global__ void __launch_bounds__(64 * NW, 4)
+q4_rows(Q4Args g, int chunk, int tiles_m, int tiles) {
     // 32-bit offsets within a tile: the host sends larger strides elsewhere.
     constexpr int P = parts<XT>(), NS = 4 / GS, XS = XT == T_F32 ? 4 : 2;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int nw = blockDim.x >> 6;
+    constexpr int nw = NW, nt = 64 * NW;
     const int r = lane & 15, lg = lane >> 4;
     const int K = int(g.K), bytes = (K + 1) / 2, last = (K - 1) >> g.shift;
     // All units, and those wholly inside a row.
     const int units = (K + kUnit - 1) / kUnit, full = bytes / (kUnit / 2);
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int64_t n0 = tile / tiles_m * 16, m0 = tile % tiles_m * kRowsMax;
+    for (int tile = blockIdx.x; tile < tiles; tile += int(gridDim.x)) {
+        const int tn = tiles_m == 1 ? tile : tile / tiles_m;
+        const int64_t n0 = int64_t(tn) * 16, m0 = int64_t(tile - tn * tiles_m) * kRowsMax;
         const int rows = int(g.M - m0 < kRowsMax ? g.M - m0 : kRowsMax);
         const int cols = int(g.N - n0 < 16 ? g.N - n0 : 16);
         const int mr = r < rows ? r : rows - 1;
@@ -360,7 +373,7 @@ q4_rows(Q4Args g, int chunk, int64_t tiles_m, int64_t tiles) {
         // weights': loads complete in order, so the staging then waits for
         // them alone while the weights are on their way.
         constexpr int BX = 2, BS = 2;
-        const int nt = blockDim.x, tid = threadIdx.x;
+        const int tid = threadIdx.x;
         for (int c0 = 0; c0 < units; c0 += chunk) {
             const int cn = units - c0 < chunk ? units - c0 : chunk;
             // Pieces of X: (row xm, piece kk) by consecutive lanes along K;
@@ -454,7 +467,7 @@ q4_rows(Q4Args g, int chunk, int64_t tiles_m, int64_t tiles) {
 #pragma unroll
             for (int e = 0; e < 4; e++) red[(wave * NWT + t) * 256 + (4 * lg + e) * 16 + r] = acc[t][e];
         __syncthreads();
-        for (int o = threadIdx.x; o < rows * 16; o += blockDim.x) {
+        for (int o = threadIdx.x; o < rows * 16; o += nt) {
             float sum[NWT];
 #pragma unroll
             for (int t = 0; t < NWT; t++) {
@@ -465,29 +478,37 @@ q4_rows(Q4Args g, int chunk, int64_t tiles_m, int64_t tiles) {
             if (nn < g.N)
                 store_as<XT>(g.Y, m * g.ldy + nn, NWT == 2 ? act_value(g.act, sum[0]) * sum[NWT - 1] : sum[0]);
         }
-        if (tile + gridDim.x < tiles) __syncthreads();
+        if (tile + int(gridDim.x) < tiles) __syncthreads();
     }
+}
+
+// X and the scales are staged whole, or in chunks of whole rounds of the waves,
+// PF units each.
+template <int XT, int GS, int NWT, int PF, int NW>
+static hipError_t launch_rows_cfg(const Q4Args& g, int64_t unit_bytes, hipStream_t s) {
+    const int64_t units = ceil_div(g.K, kUnit), rows = g.M < kRowsMax ? g.M : kRowsMax;
+    const int64_t fixed = 64 * rows, round = NW * PF;
+    int64_t chunk = (kRowsLds - fixed) / unit_bytes / round * round;
+    if (chunk < round) chunk = round;
+    if (chunk > units) chunk = units;
+    size_t lds = size_t(NW) * NWT * 1024;
+    if (size_t(chunk * unit_bytes + fixed) > lds) lds = size_t(chunk * unit_bytes + fixed);
+    const int64_t tm = ceil_div(g.M, kRowsMax), tiles = ceil_div(g.N, 16) * tm;
+    hipLaunchKernelGGL((q4_rows<XT, GS, NWT, PF, NW>), dim3(grid_for(tiles)), dim3(64 * NW), lds, s, g,
+                       int(chunk), int(tm), int(tiles));
+    return hipGetLastError();
 }
 
 template <int XT, int GS, int NWT>
 static hipError_t launch_rows(const Q4Args& g, hipStream_t s) {
-    constexpr int nw = 8, PF = 2;
     const int64_t units = ceil_div(g.K, kUnit), rows = g.M < kRowsMax ? g.M : kRowsMax;
     const int64_t unit_bytes = 4 * parts<XT>() * 4 * rows * 16 + NWT * (4 / GS) * 16 * int64_t(sizeof(ScaleZero));
-    // X and the scales are staged whole, or in chunks of whole rounds of the
-    // waves, PF units each, that leave room for two workgroups in a CU's LDS
-    // (float X of more than 6 rows: one).
-    constexpr int64_t kLds = 80 * 1024, round = nw * PF;
-    const int64_t fixed = 64 * rows;
-    int64_t chunk = (kLds - fixed) / unit_bytes / round * round;
-    if (chunk < round) chunk = round;
-    if (chunk > units) chunk = units;
-    size_t lds = size_t(nw) * NWT * 1024;
-    if (size_t(chunk * unit_bytes + fixed) > lds) lds = size_t(chunk * unit_bytes + fixed);
-    const int64_t tm = ceil_div(g.M, kRowsMax), tiles = ceil_div(g.N, 16) * tm;
-    const dim3 grid(grid_for(tiles)), block(64 * nw);
-    hipLaunchKernelGGL((q4_rows<XT, GS, NWT, PF>), grid, block, lds, s, g, int(chunk), tm, tiles);
-    return hipGetLastError();
+    // Four units ahead in eight waves where that much of X leaves room for two
+    // workgroups in a CU's LDS; more of it (float X of several rows) takes one
+    // workgroup, of sixteen waves that load one unit ahead.
+    if ((units < 32 ? units : 32) * unit_bytes + 64 * rows <= kRowsLds)
+        return launch_rows_cfg<XT, GS, NWT, NWT == 1 ? 4 : 2, 8>(g, unit_bytes, s);
+    return launch_rows_cfg<XT, GS, NWT, 1, 16>(g, unit_bytes, s);
 }
 
 // More rows of X: tiles on the 32 x 32 x 16 instruction.  A workgroup is WK
@@ -521,8 +542,9 @@ q4_tile(Q4Args g, int tiles_m, int tiles_n) {
     const int iters = (units + WK - 1) / WK;
     constexpr int XS = XT == T_F32 ? 4 : 2, SB = S32 ? 4 : 2, SW = (NS * SB + 3) / 4;
 
-    // Each XCD a contiguous range of tiles, rows of tiles fastest: the tiles
-    // it runs at a time share their weights in its L2.
+    // Each XCD a contiguous range of tiles, four rows of tiles at a time: the
+    // 32 tiles it runs together are about as wide as they are high in bytes,
+    // which is the least to bring into its L2.
     const int tiles = tiles_m * tiles_n;
     for (int t0 = blockIdx.x; t0 < tiles; t0 += gridDim.x) {
         int lin = t0;
@@ -530,7 +552,9 @@ q4_tile(Q4Args g, int tiles_m, int tiles_n) {
             const int q = tiles / 8, rem = tiles % 8, x = t0 % 8;
             lin = x * q + (x < rem ? x : rem) + t0 / 8;
         }
-        const int64_t m0 = int64_t(lin % tiles_m) * BM, n0 = int64_t(lin / tiles_m) * BN + wn * 32;
+        const int per_group = 4 * tiles_n, first = lin / per_group * 4;
+        const int high = tiles_m - first < 4 ? tiles_m - first : 4, in = lin % per_group;
+        const int64_t m0 = int64_t(first + in % high) * BM, n0 = int64_t(in / high) * BN + wn * 32;
         // The lane's row of the weights, from the wave's first (or the last row
         // there is), and its pieces of X, from the tile's first row.
         const int64_t nb = n0 < g.N ? n0 : g.N - 1;
@@ -767,16 +791,64 @@ q4_tile(Q4Args g, int tiles_m, int tiles_n) {
         }
         // Accumulator register e of a lane is row 8 (e / 4) + 4 half + e % 4 of
         // its block, column r.
-        if (kg == 0 && n0 + r < g.N) {
+        if (kg == 0 && n0 < g.N) {
+            const int rows = int(g.M - m0 < BM ? g.M - m0 : BM);
+            if constexpr (NWT == 2) {
 #pragma unroll
-            for (int b = 0; b < TM; b++)
+                for (int b = 0; b < TM; b++) {
+                    float gate[16];
 #pragma unroll
-                for (int e = 0; e < 16; e++) {
-                    const int64_t m = m0 + b * 32 + 8 * (e / 4) + 4 * half + e % 4;
-                    if (m < g.M)
-                        store_as<XT>(g.Y, m * g.ldy + n0 + r,
-                                     NWT == 2 ? act_value(g.act, acc[0][b][e]) * acc[NWT - 1][b][e] : acc[0][b][e]);
+                    for (int e = 0; e < 16; e++) gate[e] = acc[0][b][e];
+                    act_values<16>(g.act, gate, gate);
+#pragma unroll
+                    for (int e = 0; e < 16; e++) acc[0][b][e] = gate[e] * acc[NWT - 1][b][e];
                 }
+            }
+            constexpr int kRow[4] = {0, 8, 16, 24};
+            if constexpr (WK == 1 && XS == 2) {
+                // Through LDS (its stages are free), a block at a time, for
+                // 16-byte stores: 2 bytes a lane took 9 % of a prompt's time
+                // (floats, whose 32 lanes fill cache lines, lose by it).
+                constexpr int PITCH = 32 * XS + 16, EL = 16 / XS, LPR = 32 / EL;
+                static_assert(WN * 32 * PITCH <= LDS, "blocks fit the stages");
+                char* const st = smem + wn * (32 * PITCH);
+                const int cols = int(g.N - n0 < 32 ? g.N - n0 : 32);
+#pragma unroll
+                for (int b = 0; b < TM; b++) {
+                    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                    for (int e = 0; e < 16; e++)
+                        store_as<XT>(st + (kRow[e / 4] + e % 4 + 4 * half) * PITCH, r, acc[0][b][e]);
+                    // Exchanged within the wave, whose LDS operations complete
+                    // in order.
+                    asm volatile("" ::: "memory");
+                    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                    for (int q = 0; q < 32 * LPR; q += 64) {
+                        const int row = (q + lane) / LPR, c = lane % LPR * EL;
+                        if (b * 32 + row >= rows) continue;
+                        const u32x4 v = *reinterpret_cast<const u32x4*>(st + row * PITCH + c * XS);
+                        char* yp = static_cast<char*>(g.Y) + ((m0 + b * 32 + row) * g.ldy + n0 + c) * XS;
+                        if (c + EL <= cols) {
+                            __builtin_memcpy(yp, &v, 16);
+                        } else {
+                            for (int i = 0; i < EL; i++)
+                                if (c + i < cols) __builtin_memcpy(yp + i * XS, st + row * PITCH + (c + i) * XS, XS);
+                        }
+                    }
+                    asm volatile("" ::: "memory");
+                }
+            } else if (n0 + r < g.N) {
+                char* yp = static_cast<char*>(g.Y) + (m0 * g.ldy + n0) * XS;
+                const uint32_t yoff = (4 * half * uint32_t(g.ldy) + r) * XS;
+#pragma unroll
+                for (int b = 0; b < TM; b++)
+#pragma unroll
+                    for (int e = 0; e < 16; e++) {
+                        const int row = b * 32 + kRow[e / 4] + e % 4;
+                        if (row < rows - 4 * half) store_as<XT>(yp + int64_t(row) * g.ldy * XS + yoff, 0, acc[0][b][e]);
+                    }
+            }
         }
         if (t0 + int(gridDim.x) < tiles) __syncthreads();
     }

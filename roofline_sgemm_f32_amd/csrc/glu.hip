@@ -106,6 +106,7 @@ __device__ __forceinline__ void finish(const GluArgs& g, int64_t m, int64_t f, f
 template <int MR, int RF, int WKW>
 __global__ void __launch_bounds__(64 * kThinWaves)
 glu_thin_fk(GluArgs g) {
+    constexpr bool XPRE = MR <= 2;
     constexpr int V = 2 * MR * RF, GROUPS = kThinWaves / WKW;
     __shared__ float red[kThinWaves][V];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -142,24 +143,34 @@ glu_thin_fk(GluArgs g) {
     };
     const int64_t step = 256 * WKW, k0 = (w % WKW) * 256 + lane * 4;
     int64_t k = k0;
-    v4f wv[2][RF];
-    if (k + 4 <= g.K) loadw(wv, k);
-    for (; k + 4 <= g.K; k += step) {
-        v4f xv[MR], next[2][RF];
+    // A step ahead: its weights, and with one or two rows its X (from the
+    // caches; of more rows it takes the registers of a resident wave).
+    auto loadx = [&](v4f (&xv)[MR], int64_t at) {
 #pragma unroll
-        for (int m = 0; m < MR; m++) xv[m] = load4(xrow[m] + k);
+        for (int m = 0; m < MR; m++) xv[m] = load4(xrow[m] + at);
+    };
+    v4f wv[2][RF], xv[MR];
+    if (k + 4 <= g.K) {
+        loadw(wv, k);
+        if (XPRE) loadx(xv, k);
+    }
+    for (; k + 4 <= g.K; k += step) {
+        v4f wn[2][RF], xn[MR];
         const bool more = k + step + 4 <= g.K;
-        if (more) loadw(next, k + step);
+        if (!XPRE) loadx(xv, k);
+        if (more) {
+            loadw(wn, k + step);
+            if (XPRE) loadx(xn, k + step);
+        }
         add(wv, xv);
         if (more) {
 #pragma unroll
-            for (int t = 0; t < 2; t++)
+            for (int r = 0; r < RF; r++) wv[0][r] = wn[0][r], wv[1][r] = wn[1][r];
 #pragma unroll
-                for (int r = 0; r < RF; r++) wv[t][r] = next[t][r];
+            for (int m = 0; m < MR && XPRE; m++) xv[m] = xn[m];
         }
     }
     if (k < g.K) {  // one lane at most: the row's last, incomplete four
-        v4f xv[MR];
 #pragma unroll
         for (int m = 0; m < MR; m++) xv[m] = load4_tail(xrow[m], k, g.K);
 #pragma unroll
@@ -193,11 +204,16 @@ glu_thin_fk(GluArgs g) {
 template <int MR, int LC, int NW>
 __global__ void __launch_bounds__(64 * NW)
 glu_thin_kf(GluArgs g) {
+    constexpr bool XPRE = MR <= 2;
     constexpr int KG = 64 / LC, V = 8 * MR, HELD = V / KG > 0 ? V / KG : 1;
     __shared__ float red[NW][LC][V];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lc = lane % LC, kg = lane / LC;
-    const int64_t c0 = int64_t(blockIdx.x) * (4 * LC) + lc * 4;
+    // Neighbouring stretches on one XCD: where they share a cache line its L2
+    // then brings it in once.
+    const int q8 = gridDim.x / 8, r8 = gridDim.x % 8, x8 = blockIdx.x % 8;
+    const int64_t tile = x8 * q8 + (x8 < r8 ? x8 : r8) + blockIdx.x / 8;
+    const int64_t c0 = tile * (4 * LC) + lc * 4;
     // Lanes at the end of a row take its last four columns again.
     const int64_t c = c0 + 4 <= g.F ? c0 : g.F - 4;
     const float* xrow[MR];
@@ -226,22 +242,32 @@ glu_thin_kf(GluArgs g) {
     };
     const int64_t step = 4 * KG * NW;
     int64_t k = (int64_t(w) * KG + kg) * 4;
-    v4f wv[2][4];
-    if (k + 4 <= g.K) loadw(wv, k);
-    for (; k + 4 <= g.K; k += step) {
-        v4f xv[MR], next[2][4];
+    auto loadx = [&](v4f (&xv)[MR], int64_t at) {
 #pragma unroll
-        for (int m = 0; m < MR; m++) xv[m] = load4(xrow[m] + k);
+        for (int m = 0; m < MR; m++) xv[m] = load4(xrow[m] + at);
+    };
+    v4f wv[2][4], xv[MR];
+    if (k + 4 <= g.K) {
+        loadw(wv, k);
+        if (XPRE) loadx(xv, k);
+    }
+    for (; k + 4 <= g.K; k += step) {
+        v4f wn[2][4], xn[MR];
         const bool more = k + step + 4 <= g.K;
-        if (more) loadw(next, k + step);
+        if (!XPRE) loadx(xv, k);
+        if (more) {
+            loadw(wn, k + step);
+            if (XPRE) loadx(xn, k + step);
+        }
         add(wv, xv);
         if (more) {
 #pragma unroll
-            for (int q = 0; q < 4; q++) wv[0][q] = next[0][q], wv[1][q] = next[1][q];
+            for (int q = 0; q < 4; q++) wv[0][q] = wn[0][q], wv[1][q] = wn[1][q];
+#pragma unroll
+            for (int m = 0; m < MR && XPRE; m++) xv[m] = xn[m];
         }
     }
     if (k < g.K) {  // the last, incomplete block of rows
-        v4f xv[MR];
 #pragma unroll
         for (int m = 0; m < MR; m++) xv[m] = load4_tail(xrow[m], k, g.K);
 #pragma unroll
@@ -258,7 +284,7 @@ glu_thin_kf(GluArgs g) {
     __syncthreads();
     for (int o = threadIdx.x; o < MR * LC * 4; o += blockDim.x) {
         const int m = o / (LC * 4), l = o / 4 % LC, e = o % 4;
-        const int64_t l0 = int64_t(blockIdx.x) * (4 * LC) + l * 4;
+        const int64_t l0 = tile * (4 * LC) + l * 4;
         if (m >= g.M || l0 >= g.F) continue;
         const int64_t f = (l0 + 4 <= g.F ? l0 : g.F - 4) + e;
         if (f < l0) continue;  // another lane's column
@@ -272,23 +298,42 @@ glu_thin_kf(GluArgs g) {
     }
 }
 
+// Waves share K, in steps of 256, until there are two workgroups per CU.
+template <int MR, int RF>
+static hipError_t launch_thin_fk(const GluArgs& g, hipStream_t s) {
+    int w = 1;
+    while (w < kThinWaves && ceil_div(g.F, RF * kThinWaves / w) < 512 && g.K >= 512 * w) w *= 2;
+    const dim3 grid(unsigned(ceil_div(g.F, RF * kThinWaves / w))), block(64 * kThinWaves);
+    switch (w) {
+        case 1: hipLaunchKernelGGL((glu_thin_fk<MR, RF, 1>), grid, block, 0, s, g); break;
+        case 2: hipLaunchKernelGGL((glu_thin_fk<MR, RF, 2>), grid, block, 0, s, g); break;
+        case 4: hipLaunchKernelGGL((glu_thin_fk<MR, RF, 4>), grid, block, 0, s, g); break;
+        default: hipLaunchKernelGGL((glu_thin_fk<MR, RF, 8>), grid, block, 0, s, g); break;
+    }
+    return hipGetLastError();
+}
+
 template <int MR>
 static hipError_t launch_thin_mr(const GluArgs& g, hipStream_t s) {
     if (g.transw) {
-        constexpr int RF = MR >= 4 ? 4 : 2;
-        // Few rows of weights: more waves share K.
-        if (g.F >= 4096) {
-            constexpr int W = 1;
-            const dim3 grid(unsigned(ceil_div(g.F, RF * kThinWaves / W)));
-            hipLaunchKernelGGL((glu_thin_fk<MR, RF, W>), grid, dim3(64 * kThinWaves), 0, s, g);
-        } else {
-            constexpr int W = 4;
-            const dim3 grid(unsigned(ceil_div(g.F, RF * kThinWaves / W)));
-            hipLaunchKernelGGL((glu_thin_fk<MR, RF, W>), grid, dim3(64 * kThinWaves), 0, s, g);
+        // Four rows of the weights a wave reuse its X more, two leave more
+        // waves resident: 8 x 8192 x 4096 54.9 us against 60.4, 5 x 4099 x 2047
+        // 26.9 against 20.7, 8 x 1024 x 1024 6.1 against 5.0.
+        if constexpr (MR >= 4) {
+            if (g.F >= 6144) return launch_thin_fk<MR, 4>(g, s);
         }
+        return launch_thin_fk<MR, 2>(g, s);
     } else {
         constexpr int NW = MR <= 2 ? 16 : 8;
-        hipLaunchKernelGGL((glu_thin_kf<MR, 8, NW>), dim3(unsigned(ceil_div(g.F, 32))), dim3(64 * NW), 0, s, g);
+        // Stretches of 16 columns (64 bytes) occupy the CUs of outputs up to
+        // 6144 wide (8 x 4096 x 4096 44 -> 38 us), if they are aligned; those of
+        // unaligned rows straddle two cache lines each (7 x 4099 x 2047 26 -> 29)
+        // and keep 32.
+        const bool lines = (reinterpret_cast<uintptr_t>(g.Wg) | reinterpret_cast<uintptr_t>(g.Wu)) % 64 == 0 && g.ldw % 16 == 0;
+        if (g.F < 6144 && lines)
+            hipLaunchKernelGGL((glu_thin_kf<MR, 4, NW>), dim3(unsigned(ceil_div(g.F, 16))), dim3(64 * NW), 0, s, g);
+        else
+            hipLaunchKernelGGL((glu_thin_kf<MR, 8, NW>), dim3(unsigned(ceil_div(g.F, 32))), dim3(64 * NW), 0, s, g);
     }
     return hipGetLastError();
 }
@@ -369,9 +414,13 @@ hipError_t launch_glu_backward(const GluGradArgs& g, hipStream_t s) {
     // with both halves along its K (dX) or its M or N (dW).
     const bool d_pair = g.dU == g.dG + g.F && g.lddgu >= 2 * g.F;
     if (g.dX) {
+        // One sum over 2F for dX up to the length of sum the separate products
+        // have at F = 8192: beyond it, the longer float sums cost accuracy
+        // (4096 x 8192 x 4096: 2.3e-6 of dX's size in one sum, 1.6e-6 in two)
+        // and the second product's pass over dX little time (20 us of 7.5 ms).
         const bool w_pair = g.transw ? g.Wu == g.Wg + g.F * g.ldw
                                      : g.Wu == g.Wg + g.F && g.ldw >= 2 * g.F;
-        if (d_pair && w_pair) {
+        if (d_pair && w_pair && g.F <= 4096) {
             e = product(false, !g.transw, g.M, g.K, 2 * g.F, g.dG, g.lddgu, g.Wg, g.ldw, 0.0f, g.dX,
                         g.lddx, s);
         } else {

@@ -70,7 +70,7 @@ template <int XT> hipError_t launch_q4_xt(const Q4Args& g, hipStream_t s);
 static bool offsets_fit(const Q4Args& g) {
     const int64_t lim = int64_t(1) << 31;
     return g.K < lim - 128 && 256 * g.ldw < lim && 256 * 4 * g.lds < lim && 256 * g.ldz < lim &&
-           128 * 4 * g.ldx < lim && 32 * g.ldy < lim && ceil_div(g.M, 8) * ceil_div(g.N, 16) < lim;
+           128 * 4 * g.ldx < lim && 32 * g.ldy < lim && ceil_div(g.M, 8) * ceil_div(g.N, 16) < lim / 2;
 }
 
 hipError_t launch_q4(const Q4Args& g, hipStream_t s) {

@@ -552,8 +552,9 @@ q4_tile(Q4Args g, int tiles_m, int tiles_n) {
             const int q = tiles / 8, rem = tiles % 8, x = t0 % 8;
             lin = x * q + (x < rem ? x : rem) + t0 / 8;
         }
-        const int per_group = 4 * tiles_n, first = lin / per_group * 4;
-        const int high = tiles_m - first < 4 ? tiles_m - first : 4, in = lin % per_group;
+        const int64_t per_group = 4 * int64_t(tiles_n);
+        const int first = int(lin / per_group) * 4, in = int(lin % per_group);
+        const int high = tiles_m - first < 4 ? tiles_m - first : 4;
         const int64_t m0 = int64_t(first + in % high) * BM, n0 = int64_t(in / high) * BN + wn * 32;
         // The lane's row of the weights, from the wave's first (or the last row
         // there is), and its pieces of X, from the tile's first row.

@@ -63,8 +63,9 @@ q4_general(Q4Args g, int64_t tiles) {
     }
 }
 
-// The kernels of q4_kernels.h, one type of X each (q4_f32.hip, ...).
-template <int XT> hipError_t launch_q4_xt(const Q4Args& g, hipStream_t s);
+// The kernels of q4_kernels.h, by type of X and form (q4_f32.hip, q4_glu_f32.hip,
+// ...): NWT 1 the product, 2 the gated form.
+template <int XT, int NWT> hipError_t launch_q4_kernels(const Q4Args& g, hipStream_t s);
 
 // Whether a tile's 32-bit offsets reach every operand.
 static bool offsets_fit(const Q4Args& g) {
@@ -79,10 +80,11 @@ hipError_t launch_q4(const Q4Args& g, hipStream_t s) {
         hipLaunchKernelGGL(q4_general, dim3(grid_for(tiles)), dim3(64), 0, s, g, tiles);
         return hipGetLastError();
     }
+    const bool two = g.act >= 0;
     switch (g.xtype) {
-        case T_F32: return launch_q4_xt<T_F32>(g, s);
-        case T_F16: return launch_q4_xt<T_F16>(g, s);
-        default: return launch_q4_xt<T_BF16>(g, s);
+        case T_F32: return two ? launch_q4_kernels<T_F32, 2>(g, s) : launch_q4_kernels<T_F32, 1>(g, s);
+        case T_F16: return two ? launch_q4_kernels<T_F16, 2>(g, s) : launch_q4_kernels<T_F16, 1>(g, s);
+        default: return two ? launch_q4_kernels<T_BF16, 2>(g, s) : launch_q4_kernels<T_BF16, 1>(g, s);
     }
 }
 

@@ -1,6 +1,7 @@
-// The kernels of q4_kernels.h for X of one type (compiled side by side).
+// The kernels of q4_kernels.h for one type of X and one form (a source each, to
+// compile side by side).
 #include "q4_kernels.h"
 
 namespace sgemm {
-template hipError_t launch_q4_xt<T_F16>(const Q4Args& g, hipStream_t s);
-}
+template hipError_t launch_q4_kernels<T_F16, 1>(const Q4Args& g, hipStream_t s);
+}  // namespace sgemm

@@ -866,15 +866,40 @@ static hipError_t launch_tile(const Q4Args& g, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Tile by shape.  One round of workgroups, one per CU, takes about the same time
+// whatever its number, and that time grows much more slowly than the tile (a
+// small tile shares out K instead), so the choice is the configuration with the
+// least rounds x time of a round.  Times measured on MI355X at K = 4096 (us; the
+// ratios at K = 2048 are alike): bfloat16 and float16 / float, of one product and
+// of the gated pair.  Over 9 to 1024 rows by 1024 to 8192 columns the choice is
+// the fastest of these, or within 15 % of it; always the 128 x 256 tile would
+// take 70 us for 9 rows where 14 do, always the 32 x 32 one 383 for 1024 rows
+// where 78 do.
 template <int XT, int GS, int NWT>
 static hipError_t launch_tiles(const Q4Args& g, hipStream_t s) {
-    constexpr bool f = XT == T_F32;
-    const int64_t big = ceil_div(g.M, NWT == 2 ? 64 : 128) * ceil_div(g.N, 256);
-    if (big >= 200) return launch_tile<XT, GS, NWT, NWT == 2 ? 2 : 4, 8, 1>(g, s);
-    if constexpr (NWT == 1) {
-        if (ceil_div(g.M, 64) * ceil_div(g.N, 64) >= 200) return launch_tile<XT, GS, NWT, 2, 2, f ? 2 : 4>(g, s);
+    constexpr bool f = XT == T_F32, two = NWT == 2;
+    constexpr int kTiles[5][2] = {{32, 32}, {32, 64}, {32, 128}, {64, 128}, {two ? 64 : 128, 256}};
+    constexpr int kTime[5] = {two ? (f ? 37 : 23) : (f ? 28 : 14), two ? (f ? 44 : 29) : (f ? 29 : 16),
+                              two ? (f ? 68 : 49) : (f ? 41 : 23), two ? (f ? 117 : 61) : (f ? 62 : 31),
+                              two ? (f ? 162 : 101) : (f ? 160 : 70)};
+    constexpr int64_t kCUs = 256;
+    int best = 0;
+    int64_t best_time = 0;
+    for (int c = 0; c < 5; c++) {
+        const int64_t tiles = ceil_div(g.M, kTiles[c][0]) * ceil_div(g.N, kTiles[c][1]);
+        const int64_t time = ceil_div(tiles, kCUs) * kTime[c];
+        if (c == 0 || time < best_time) {
+            best = c;
+            best_time = time;
+        }
     }
-    return launch_tile<XT, GS, NWT, 1, 1, f ? 4 : 8>(g, s);
+    switch (best) {
+        case 0: return launch_tile<XT, GS, NWT, 1, 1, f ? 4 : 8>(g, s);
+        case 1: return launch_tile<XT, GS, NWT, 1, 2, 4>(g, s);
+        case 2: return launch_tile<XT, GS, NWT, 1, 4, 2>(g, s);
+        case 3: return launch_tile<XT, GS, NWT, 2, 4, two ? 1 : 2>(g, s);
+        default: return launch_tile<XT, GS, NWT, two ? 2 : 4, 8, 1>(g, s);
+    }
 }
 
 template <int XT, int GS, int NWT>
@@ -882,17 +907,12 @@ static hipError_t launch_gs(const Q4Args& g, hipStream_t s) {
     return g.M <= kRowsMax ? launch_rows<XT, GS, NWT>(g, s) : launch_tiles<XT, GS, NWT>(g, s);
 }
 
-// The kernels of one type of X.
+// The kernels of one type of X and one form (NWT 1: the product, 2: gated).
 template <int XT, int NWT>
-static hipError_t launch_nwt(const Q4Args& g, hipStream_t s) {
+hipError_t launch_q4_kernels(const Q4Args& g, hipStream_t s) {
     if (g.shift >= 7) return launch_gs<XT, 4, NWT>(g, s);
     if (g.shift == 6) return launch_gs<XT, 2, NWT>(g, s);
     return launch_gs<XT, 1, NWT>(g, s);
-}
-
-template <int XT>
-hipError_t launch_q4_xt(const Q4Args& g, hipStream_t s) {
-    return g.act >= 0 ? launch_nwt<XT, 2>(g, s) : launch_nwt<XT, 1>(g, s);
 }
 
 }  // namespace sgemm

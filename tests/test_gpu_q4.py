@@ -68,6 +68,41 @@ def test_gated(shape, x):
     assert H.intact()
 
 
+# Rows by 8190 columns that take each tile of the rule in turn (32 x 64, 32 x
+# 128, 64 x 128, the largest), with K of whole and cut units.
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("x", TYPES)
+@pytest.mark.parametrize("M", [61, 125, 250, 1000])
+def test_every_tile(M, x, group):
+    gen = torch.Generator().manual_seed(M)
+    N, K = 8190, {32: 384, 64: 290, 128: 135}[group]
+    X = torch.randn((M, K), generator=gen).to(TYPES[x])
+    stype = TYPES[x] if group != 64 else torch.float32
+    w, s, z = q4_make(gen, N, K, group, stype, group != 32)
+    Y = Guarded(M, N, TYPES[x], gap=2 if group == 64 else 0)
+    rs.q4_matmul(X.cuda(), w, s, z, group=group, out=Y.view)
+    ref, err = q4_64(X, w, s, z, group)
+    assert_within(Y.view, ref, rounded(ref, err, TYPES[x]))
+    assert Y.intact()
+
+
+@pytest.mark.parametrize("x", TYPES)
+@pytest.mark.parametrize("M", [61, 125, 250, 500])
+def test_every_gated_tile(M, x):
+    gen = torch.Generator().manual_seed(M)
+    group = 32 << (M // 125 % 3)
+    N, K, stype = 8190, 300, torch.float32 if M == 125 else torch.bfloat16
+    X = torch.randn((M, K), generator=gen).to(TYPES[x])
+    gate, up = (q4_make(gen, N, K, group, stype, M != 61) for _ in range(2))
+    H = Guarded(M, N, TYPES[x], gap=1)
+    rs.q4_glu(X.cuda(), gate[0], gate[1], up[0], up[1], gate[2], up[2], group=group, act="gelu_tanh",
+              out=H.view)
+    g, eg = q4_64(X, *gate, group)
+    u, eu = q4_64(X, *up, group)
+    assert_within(H.view, *glu_bound("gelu_tanh", g, eg, u, eu, TYPES[x]))
+    assert H.intact()
+
+
 @pytest.mark.parametrize("st", TYPES)
 @pytest.mark.parametrize("x", TYPES)
 @pytest.mark.parametrize("M", [1, 6, 40, 200])

@@ -96,9 +96,12 @@ __device__ __forceinline__ void finish(const GluArgs& g, int64_t m, int64_t f, f
 }
 }  // namespace
 
-// One to eight rows of X (MR rounds M up to a power of two; rows past M repeat
+// One to sixteen rows of X (MR rounds M up to a power of two; rows past M repeat
 // the last): the weights are read once and bound the time, at two operations
-// per float and row.
+// per float and row; a matrix-core tile would stage them through LDS beside as
+// much of X.  Measured at F = 8192, K = 4096 (268 MB, 41 us at the copy's rate):
+// 46.8 us for one row and weights F x K, 54.9 for 8, 70.8 for 16 (83 on matrix
+// tiles); K x F 55.7, 56.1 and 64.1 (79).
 //
 // Weights F x K: a wave owns RF rows of both weights and its lanes split K,
 // four floats each, so its loads are 1 KiB contiguous; WKW waves share K.  X
@@ -107,6 +110,7 @@ template <int MR, int RF, int WKW>
 __global__ void __launch_bounds__(64 * kThinWaves)
 glu_thin_fk(GluArgs g) {
     constexpr bool XPRE = MR <= 2;
+    constexpr int MX = MR < 8 ? MR : 8;
     constexpr int V = 2 * MR * RF, GROUPS = kThinWaves / WKW;
     __shared__ float red[kThinWaves][V];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -118,22 +122,23 @@ glu_thin_fk(GluArgs g) {
         wrow[0][r] = g.Wg + f * g.ldw;
         wrow[1][r] = g.Wu + f * g.ldw;
     }
-    const float* xrow[MR];
-#pragma unroll
-    for (int m = 0; m < MR; m++) xrow[m] = g.X + (m < g.M ? m : g.M - 1) * g.ldx;
+    const auto xrow = [&](int m) { return g.X + (m < g.M ? m : g.M - 1) * g.ldx; };
     float acc[V];  // [matrix][row of X][row of the weight]
 #pragma unroll
     for (int i = 0; i < V; i++) acc[i] = 0.0f;
-    auto add = [&](const v4f (&wv)[2][RF], const v4f (&xv)[MR]) {
+    // MX rows of X from row mg on.
+    auto add = [&](const v4f (&wv)[2][RF], const v4f (&xv)[MX], int mg) {
 #pragma unroll
         for (int t = 0; t < 2; t++)
 #pragma unroll
-            for (int m = 0; m < MR; m++)
+            for (int m = 0; m < MX; m++)
 #pragma unroll
                 for (int r = 0; r < RF; r++)
 #pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        acc[(t * MR + m) * RF + r] = fmaf(xv[m][e], wv[t][r][e], acc[(t * MR + m) * RF + r]);
+                    for (int e = 0; e < 4; e++) {
+                        float& a = acc[(t * MR + mg + m) * RF + r];
+                        a = fmaf(xv[m][e], wv[t][r][e], a);
+                    }
     };
     auto loadw = [&](v4f (&wv)[2][RF], int64_t k) {
 #pragma unroll
@@ -145,39 +150,47 @@ glu_thin_fk(GluArgs g) {
     int64_t k = k0;
     // A step ahead: its weights, and with one or two rows its X (from the
     // caches; of more rows it takes the registers of a resident wave).
-    auto loadx = [&](v4f (&xv)[MR], int64_t at) {
+    auto loadx = [&](v4f (&xv)[MX], int64_t at, int mg) {
 #pragma unroll
-        for (int m = 0; m < MR; m++) xv[m] = load4(xrow[m] + at);
+        for (int m = 0; m < MX; m++) xv[m] = load4(xrow(mg + m) + at);
     };
-    v4f wv[2][RF], xv[MR];
+    v4f wv[2][RF], xv[MX];
     if (k + 4 <= g.K) {
         loadw(wv, k);
-        if (XPRE) loadx(xv, k);
+        if (XPRE) loadx(xv, k, 0);
     }
     for (; k + 4 <= g.K; k += step) {
-        v4f wn[2][RF], xn[MR];
+        v4f wn[2][RF], xn[MX];
         const bool more = k + step + 4 <= g.K;
-        if (!XPRE) loadx(xv, k);
+        if (!XPRE) loadx(xv, k, 0);
         if (more) {
             loadw(wn, k + step);
-            if (XPRE) loadx(xn, k + step);
+            if (XPRE) loadx(xn, k + step, 0);
         }
-        add(wv, xv);
+        add(wv, xv, 0);
+#pragma unroll
+        for (int mg = MX; mg < MR; mg += MX) {
+            loadx(xv, k, mg);
+            add(wv, xv, mg);
+        }
         if (more) {
 #pragma unroll
             for (int r = 0; r < RF; r++) wv[0][r] = wn[0][r], wv[1][r] = wn[1][r];
 #pragma unroll
-            for (int m = 0; m < MR && XPRE; m++) xv[m] = xn[m];
+            for (int m = 0; m < MX && XPRE; m++) xv[m] = xn[m];
         }
     }
     if (k < g.K) {  // one lane at most: the row's last, incomplete four
 #pragma unroll
-        for (int m = 0; m < MR; m++) xv[m] = load4_tail(xrow[m], k, g.K);
-#pragma unroll
         for (int t = 0; t < 2; t++)
 #pragma unroll
             for (int r = 0; r < RF; r++) wv[t][r] = load4_tail(wrow[t][r], k, g.K);
-        add(wv, xv);
+#pragma unroll
+        for (int mg = 0; mg < MR; mg += MX) {
+#pragma unroll
+            for (int m = 0; m < MX; m++) xv[m] = load4_tail(xrow(mg + m), k, g.K);
+            add(wv, xv, mg);
+        }
     }
     constexpr int HELD = V > 64 ? V / 64 : 1;
     const int first = reduce_lanes<32, 1, V>(acc, lane);
@@ -205,6 +218,7 @@ template <int MR, int LC, int NW>
 __global__ void __launch_bounds__(64 * NW)
 glu_thin_kf(GluArgs g) {
     constexpr bool XPRE = MR <= 2;
+    constexpr int MX = MR < 8 ? MR : 8;
     constexpr int KG = 64 / LC, V = 8 * MR, HELD = V / KG > 0 ? V / KG : 1;
     __shared__ float red[NW][LC][V];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -216,22 +230,23 @@ glu_thin_kf(GluArgs g) {
     const int64_t c0 = tile * (4 * LC) + lc * 4;
     // Lanes at the end of a row take its last four columns again.
     const int64_t c = c0 + 4 <= g.F ? c0 : g.F - 4;
-    const float* xrow[MR];
-#pragma unroll
-    for (int m = 0; m < MR; m++) xrow[m] = g.X + (m < g.M ? m : g.M - 1) * g.ldx;
+    const auto xrow = [&](int m) { return g.X + (m < g.M ? m : g.M - 1) * g.ldx; };
     float acc[V];  // [matrix][row of X][column]
 #pragma unroll
     for (int i = 0; i < V; i++) acc[i] = 0.0f;
-    auto add = [&](const v4f (&wv)[2][4], const v4f (&xv)[MR]) {
+    // MX rows of X from row mg on.
+    auto add = [&](const v4f (&wv)[2][4], const v4f (&xv)[MX], int mg) {
 #pragma unroll
         for (int q = 0; q < 4; q++)
 #pragma unroll
             for (int t = 0; t < 2; t++)
 #pragma unroll
-                for (int m = 0; m < MR; m++)
+                for (int m = 0; m < MX; m++)
 #pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        acc[(t * MR + m) * 4 + e] = fmaf(xv[m][q], wv[t][q][e], acc[(t * MR + m) * 4 + e]);
+                    for (int e = 0; e < 4; e++) {
+                        float& a = acc[(t * MR + mg + m) * 4 + e];
+                        a = fmaf(xv[m][q], wv[t][q][e], a);
+                    }
     };
     auto loadw = [&](v4f (&wv)[2][4], int64_t k) {
 #pragma unroll
@@ -242,41 +257,49 @@ glu_thin_kf(GluArgs g) {
     };
     const int64_t step = 4 * KG * NW;
     int64_t k = (int64_t(w) * KG + kg) * 4;
-    auto loadx = [&](v4f (&xv)[MR], int64_t at) {
+    auto loadx = [&](v4f (&xv)[MX], int64_t at, int mg) {
 #pragma unroll
-        for (int m = 0; m < MR; m++) xv[m] = load4(xrow[m] + at);
+        for (int m = 0; m < MX; m++) xv[m] = load4(xrow(mg + m) + at);
     };
-    v4f wv[2][4], xv[MR];
+    v4f wv[2][4], xv[MX];
     if (k + 4 <= g.K) {
         loadw(wv, k);
-        if (XPRE) loadx(xv, k);
+        if (XPRE) loadx(xv, k, 0);
     }
     for (; k + 4 <= g.K; k += step) {
-        v4f wn[2][4], xn[MR];
+        v4f wn[2][4], xn[MX];
         const bool more = k + step + 4 <= g.K;
-        if (!XPRE) loadx(xv, k);
+        if (!XPRE) loadx(xv, k, 0);
         if (more) {
             loadw(wn, k + step);
-            if (XPRE) loadx(xn, k + step);
+            if (XPRE) loadx(xn, k + step, 0);
         }
-        add(wv, xv);
+        add(wv, xv, 0);
+#pragma unroll
+        for (int mg = MX; mg < MR; mg += MX) {
+            loadx(xv, k, mg);
+            add(wv, xv, mg);
+        }
         if (more) {
 #pragma unroll
             for (int q = 0; q < 4; q++) wv[0][q] = wn[0][q], wv[1][q] = wn[1][q];
 #pragma unroll
-            for (int m = 0; m < MR && XPRE; m++) xv[m] = xn[m];
+            for (int m = 0; m < MX && XPRE; m++) xv[m] = xn[m];
         }
     }
     if (k < g.K) {  // the last, incomplete block of rows
-#pragma unroll
-        for (int m = 0; m < MR; m++) xv[m] = load4_tail(xrow[m], k, g.K);
 #pragma unroll
         for (int q = 0; q < 4; q++) {
             const bool in = k + q < g.K;
             wv[0][q] = in ? load4(g.Wg + (k + q) * g.ldw + c) : v4f{0.0f, 0.0f, 0.0f, 0.0f};
             wv[1][q] = in ? load4(g.Wu + (k + q) * g.ldw + c) : v4f{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        add(wv, xv);
+#pragma unroll
+        for (int mg = 0; mg < MR; mg += MX) {
+#pragma unroll
+            for (int m = 0; m < MX; m++) xv[m] = load4_tail(xrow(mg + m), k, g.K);
+            add(wv, xv, mg);
+        }
     }
     const int first = reduce_lanes<32, LC, V>(acc, lane);
 #pragma unroll
@@ -341,14 +364,19 @@ static hipError_t launch_thin_mr(const GluArgs& g, hipStream_t s) {
 bool glu_thin_ok(const GluArgs& g) {
     // The grids' work-items (at most 256 and 32 per row or column of weights)
     // stay below 2^32.
-    return g.M <= 8 && g.F < (int64_t(1) << 24) && (g.transw || g.F >= 4);
+    if (g.F >= (int64_t(1) << 24)) return false;
+    if (g.transw) return g.M <= 16;
+    // Weights K x F, 9 to 16 rows: few columns occupy too few workgroups of that
+    // many sums (9 x 1024 x 1024 11.2 us, 9.3 on matrix tiles).
+    return g.F >= 4 && (g.M <= 8 || (g.M <= 16 && g.K * g.F >= (int64_t(1) << 22)));
 }
 
 hipError_t launch_glu_thin(const GluArgs& g, hipStream_t s) {
     if (g.M == 1) return launch_thin_mr<1>(g, s);
     if (g.M == 2) return launch_thin_mr<2>(g, s);
     if (g.M <= 4) return launch_thin_mr<4>(g, s);
-    return launch_thin_mr<8>(g, s);
+    if (g.M <= 8) return launch_thin_mr<8>(g, s);
+    return launch_thin_mr<16>(g, s);
 }
 
 // dG and dU; each may be stored over G, U or dH (every lane reads its three

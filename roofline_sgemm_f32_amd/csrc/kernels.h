@@ -204,7 +204,7 @@ struct GluArgs {
 // The matrix-core kernel's gated form in tile configuration cfg (K4Cfg), with
 // 16-byte loads (vec) or 4-byte ones.
 hipError_t launch_k4_glu(const GluArgs& g, int cfg, bool vec, hipStream_t s);
-// One to eight rows of X on the vector units, and whether they can run g.
+// One to sixteen rows of X on the vector units, and whether they can run g.
 bool glu_thin_ok(const GluArgs& g);
 hipError_t launch_glu_thin(const GluArgs& g, hipStream_t s);
 // Shape-chosen forward pass.

@@ -44,8 +44,8 @@ def operands(M, K, F, transw, seed, kind="halves", integer=False):
     return X.cuda(), *dev, host
 
 
-SHAPES = [(1, 64, 64), (1, 4096, 512), (2, 100, 37), (3, 1, 1), (5, 33, 257), (8, 2048, 300),
-          (9, 16, 31), (16, 512, 128), (31, 65, 33), (33, 128, 96), (64, 256, 1024), (65, 127, 129),
+SHAPES = [(1, 64, 64), (1, 4096, 512), (2, 100, 37), (3, 1, 1), (5, 33, 257), (7, 515, 6151), (8, 2048, 300),
+          (9, 16, 31), (9, 600, 7001), (13, 2050, 2052), (16, 512, 128), (16, 1024, 6200), (31, 65, 33), (33, 128, 96), (64, 256, 1024), (65, 127, 129),
           (129, 300, 260), (257, 64, 512), (512, 96, 640), (1000, 130, 700)]
 
 

@@ -74,12 +74,16 @@ static bool offsets_fit(const Q4Args& g) {
            128 * 4 * g.ldx < lim && 32 * g.ldy < lim && ceil_div(g.M, 8) * ceil_div(g.N, 16) < lim / 2;
 }
 
-hipError_t launch_q4(const Q4Args& g, hipStream_t s) {
+hipError_t launch_q4(const Q4Args& a, hipStream_t s) {
+    Q4Args g = a;
     if (g.K == 0 || !offsets_fit(g)) {
         const int64_t tiles = g.M * g.N;
         hipLaunchKernelGGL(q4_general, dim3(grid_for(tiles)), dim3(64), 0, s, g, tiles);
         return hipGetLastError();
     }
+    // The kernels shift 32-bit positions: a group longer than any row they take
+    // is one group all the same.
+    if (g.shift > 30) g.shift = 30;
     const bool two = g.act >= 0;
     switch (g.xtype) {
         case T_F32: return two ? launch_q4_kernels<T_F32, 2>(g, s) : launch_q4_kernels<T_F32, 1>(g, s);

@@ -397,11 +397,13 @@ q4_rows(Q4Args g, int chunk, int tiles_m, int tiles) {
                 for (int b = 0; b < BS; b++) {
                     const int q = sq + tid / 16;
                     if (st < NWT && q < nq) {
-                        int gi = ((c0 + q / NS) * kUnit + q % NS * (kUnit / NS)) >> g.shift;
-                        gi = gi < last ? gi : last;
+                        // Past the last group (X is zero there) the scale is 0.
+                        const int at = ((c0 + q / NS) * kUnit + q % NS * (kUnit / NS)) >> g.shift;
+                        const int gi = at < last ? at : last;
                         const void* sp = st ? g.S[NWT - 1] : g.S[0];
                         const uint8_t* zp = st ? g.Z[NWT - 1] : g.Z[0];
                         s[b] = load_raw(g.stype, sp, n * g.lds + gi);
+                        if (at > last) s[b] = 0;
                         z[b] = zp ? zp[n * g.ldz + gi] : 8;
                     }
                     sq += nt / 16;
@@ -603,10 +605,10 @@ q4_tile(Q4Args g, int tiles_m, int tiles_n) {
                     for (int q = 0; q < SW; q++) u.s[t][q] = 0;
 #pragma unroll
                     for (int q = 0; q < NS; q++) {
-                        // Groups past the last one repeat it: X is zero there.
-                        int gq = (idx * kUnit + q * (kUnit / NS)) >> g.shift;
-                        gq = gq < last ? gq : last;
-                        u.s[t][q * SB / 4] |= load_raw(g.stype, sp, (soff / SB) + uint32_t(gq)) << (S32 ? 0 : q % 2 * 16);
+                        // Past the last group (X is zero there) the scale is 0.
+                        const int at = (idx * kUnit + q * (kUnit / NS)) >> g.shift, gq = at < last ? at : last;
+                        const uint32_t raw = at > last ? 0u : load_raw(g.stype, sp, (soff / SB) + uint32_t(gq));
+                        u.s[t][q * SB / 4] |= raw << (S32 ? 0 : q % 2 * 16);
                         u.z[t] |= uint32_t(zp ? zp[zoff + uint32_t(gq)] : 0) << (8 * q);
                     }
                 }

@@ -8,6 +8,7 @@ from tests.ff_util import (ACTS, LIPSCHITZ, TYPES, U, Guarded, act64, act_err, a
                            q4_int, q4_make, rounded)
 
 pytestmark = pytest.mark.gpu
+TINY_F32 = 2.0 ** -149
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -220,6 +221,36 @@ def test_non_finite_values(M):
         got = rs.q4_matmul(Xt.cuda(), w, s2, z, group=group)
         cols = torch.arange(N) != 9
         assert torch.isnan(got[:, 9]).all() and torch.equal(got[:, cols], base[:, cols])
+
+
+@pytest.mark.parametrize("M", [1, 5, 40])
+def test_infinite_last_scale(M):
+    """An infinite scale gives infinities of its group's sign, not NaN, also
+    where the row ends inside a step of the kernels (K = 96 + 32)."""
+    for K in (96, 97, 160, 288):
+        group = 32
+        groups = -(-K // group)
+        X = torch.ones((M, K))
+        w = torch.full((16, (K + 1) // 2), 0x99, dtype=torch.uint8, device="cuda")  # q - z = 1
+        s = torch.ones((16, groups), device="cuda")
+        s[3, -1] = float("inf")
+        for x in TYPES:
+            Y = rs.q4_matmul(X.to(TYPES[x]).cuda(), w, s, group=group)
+            assert torch.isinf(Y[:, 3]).all() and (Y[:, 3] > 0).all(), (K, x)
+            assert (Y[:, 2].float() == K).all()
+
+
+@pytest.mark.parametrize("M", [1, 9, 70])
+@pytest.mark.parametrize("group", [1 << 31, 1 << 40, 1 << 62])
+def test_one_group_of_any_length(M, group):
+    gen = torch.Generator().manual_seed(M)
+    N, K = 40, 700
+    X = torch.randn((M, K), generator=gen)
+    w, s, z = q4_make(gen, N, K, 1024, torch.float32, True)
+    Y = rs.q4_matmul(X.cuda(), w, s, z, group=group)
+    assert torch.equal(Y, rs.q4_matmul(X.cuda(), w, s, z, group=1024))
+    ref, err = q4_64(X, w, s, z, 1024)
+    assert_within(Y, ref, err + TINY_F32)
 
 
 def test_nan_payload_of_low_bits():

@@ -283,3 +283,78 @@ def test_run_to_run():
         got = (H, G, U, *rs.glu_backward(dH, X, Wg, Wu, G, U, act="gelu"))
         first = first or got
         assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+def test_refusals():
+    M, K, F = 6, 12, 10
+    X, Wg, Wu, _ = operands(M, K, F, False, seed=1)
+    with pytest.raises(ValueError, match="shape"):
+        rs.glu(X, Wg, Wu, transw=True)
+    with pytest.raises(ValueError, match="row stride"):
+        rs.glu(X, Wg, Wu.contiguous())
+    with pytest.raises(ValueError, match="column stride"):
+        rs.glu(torch.randn((K, M), device="cuda").t(), Wg, Wu)
+    with pytest.raises(ValueError, match="row stride"):
+        rs.glu(X, Wg[:1].expand(K, F), Wu[:1].expand(K, F))
+    with pytest.raises(TypeError):
+        rs.glu(X.half(), Wg, Wu)
+    with pytest.raises(ValueError, match="GPU"):
+        rs.glu(X, Wg.cpu(), Wu.cpu())
+    with pytest.raises(ValueError, match="shape"):
+        rs.glu(X, Wg, Wu, out=torch.empty((M, F + 1), device="cuda"))
+    buf = torch.zeros((M, 2 * F), device="cuda")
+    with pytest.raises(rs.SgemmError) as e:
+        rs.glu(X, Wg, Wu, out=buf[:, :F], save=(buf[:, 1:F + 1], buf[:, F:]))
+    assert e.value.status == 5  # SGEMM_ERR_ALIAS
+    H, G, U = rs.glu(X, Wg, Wu, save=True)
+    with pytest.raises(ValueError, match="beta"):
+        rs.glu_backward(H, X, Wg, Wu, G, U, beta=1.0)
+    with pytest.raises(ValueError, match="shape"):
+        rs.glu_backward(H[:, :F - 1], X, Wg, Wu, G, U)
+    with pytest.raises(rs.SgemmError) as e:
+        rs.glu_backward(H, X, Wg, Wu, G, U, dX=X)
+    assert e.value.status == 5
+
+
+def test_same_rows_twice_and_shared_weights():
+    """One tensor as both weights, and dH, G and U as one tensor: inputs may
+    overlap."""
+    M, K, F = 20, 48, 36
+    X, Wg, _, host = operands(M, K, F, False, seed=2, kind="separate")
+    H, G, U = rs.glu(X, Wg, Wg, act="relu", save=True)
+    ref, err = glu64("relu", host[0], host[1], host[1])
+    for o, r, e in zip((H, G, U), ref, err):
+        assert_within(o, r, e)
+    assert torch.equal(G, U)
+    dX, dWg, dWu = rs.glu_backward(G, X, Wg, Wg, G, G, act="relu")
+    g = G.cpu().double()
+    ref, err = glu_backward64("relu", host[0], host[1], host[1], g, g, g)
+    for o, r, e in zip((dX, dWg, dWu), ref[2:], err[2:]):
+        assert_within(o, r, e)
+
+
+@pytest.mark.parametrize("rows", [3, 24])
+def test_two_streams_at_once(rows):
+    """Calls that pack (a workspace) on two streams together."""
+    M, K, F = 700 + rows, 515, 771
+    sets = [operands(M, K, F, False, seed=s) for s in (1, 2)]
+    want = [rs.glu(X, Wg, Wu, act="gelu") for X, Wg, Wu, _ in sets]
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in sets], []
+    for _ in range(4):
+        for st, (X, Wg, Wu, _) in zip(streams, sets):
+            with torch.cuda.stream(st):
+                outs.append(rs.glu(X, Wg, Wu, act="gelu"))
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        assert torch.equal(o, want[i % 2])
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 results, rows from both ends and the middle checked."""
+    M, K, F = 66000, 16, 33000
+    X, Wg, Wu, host = operands(M, K, F, True, seed=3, kind="separate")
+    H = rs.glu(X, Wg, Wu, transw=True)
+    rows = torch.tensor([0, 1, 32767, 40001, M - 2, M - 1])
+    ref, err = glu64("silu", host[0][rows], host[1], host[2])
+    assert_within(H[rows.cuda()], ref[0], err[0])

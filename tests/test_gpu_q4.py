@@ -349,3 +349,58 @@ def test_a_block_trained_then_served():
     assert_within(Hq, h, eh, "served")
     # The float weights are products rounded once more: K more roundings.
     assert_within(want, h, eh * 4 * K, "float")
+
+
+def test_refusals():
+    gen = torch.Generator().manual_seed(1)
+    N, K, group = 24, 96, 32
+    w, s, z = q4_make(gen, N, K, group, torch.float16, True)
+    X = torch.randn((3, K), device="cuda")
+    for bad in (48, 16, 0, -32):
+        with pytest.raises(ValueError, match="power of two"):
+            rs.q4_matmul(X, w, s, z, group=bad)
+    with pytest.raises(ValueError, match="shape"):
+        rs.q4_matmul(X, w, s, z, group=64)
+    with pytest.raises(ValueError, match="shape"):
+        rs.q4_matmul(X[:, :-2].contiguous(), w, s, z, group=group)
+    with pytest.raises(TypeError):
+        rs.q4_matmul(X, w.to(torch.int8), s, z, group=group)
+    with pytest.raises(TypeError):
+        rs.q4_matmul(X.double(), w, s, z, group=group)
+    with pytest.raises(TypeError):
+        rs.q4_matmul(X, w, s.double(), z, group=group)
+    with pytest.raises(TypeError):
+        rs.q4_matmul(X, w, s, z, group=group, out=torch.empty((3, N), device="cuda", dtype=torch.float16))
+    with pytest.raises(ValueError, match="GPU"):
+        rs.q4_matmul(X, w.cpu(), s, z, group=group)
+    with pytest.raises(TypeError, match="scales"):
+        rs.q4_glu(X, w, s, w, s.float(), group=group)
+    with pytest.raises(ValueError, match="activation"):
+        rs.q4_glu(X, w, s, w, s, group=group, act="tanh")
+    square = q4_make(gen, K, K, group, torch.float16, False)
+    with pytest.raises(rs.SgemmError) as e:
+        rs.q4_matmul(X, square[0], square[1], group=group, out=X)
+    assert e.value.status == 5  # SGEMM_ERR_ALIAS
+
+
+def test_one_weight_as_gate_and_up():
+    gen = torch.Generator().manual_seed(2)
+    N, K, group = 50, 130, 64
+    w, s, z = q4_make(gen, N, K, group, torch.bfloat16, True)
+    for M in (2, 30):
+        X = torch.randn((M, K), generator=gen)
+        H = rs.q4_glu(X.cuda(), w, s, w, s, z, z, group=group, act="relu")
+        g, eg = q4_64(X, w, s, z, group)
+        assert_within(H, *glu_bound("relu", g, eg, g, eg, torch.float32))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 results, rows from both ends and the middle checked."""
+    gen = torch.Generator().manual_seed(4)
+    M, N, K, group = 66000, 33000, 40, 32
+    X = torch.randn((M, K), generator=gen).to(torch.float16)
+    w, s, z = q4_make(gen, N, K, group, torch.float16, False)
+    Y = rs.q4_matmul(X.cuda(), w, s, group=group)
+    rows = torch.tensor([0, 1, 32767, 40001, M - 2, M - 1])
+    ref, err = q4_64(X[rows], w, s, z, group)
+    assert_within(Y[rows.cuda()], ref, rounded(ref, err, torch.float16))

@@ -56,9 +56,9 @@
  *       being captured into a graph.
  *   Every other case of these entry points (products that neither split nor
  *   pack, K == 0, alpha == 0) allocates nothing and never synchronises.
- *   sgemm_glu_f32 (to pack unaligned operands) and the products of
- *   sgemm_glu_backward_f32 use the workspace in the same way; sgemm_q4 and
- *   sgemm_q4_glu never do.
+ *   sgemm_glu_f32 (to pack unaligned operands and to split K) and the
+ *   products of sgemm_glu_backward_f32 use the workspace in the same way;
+ *   sgemm_q4 and sgemm_q4_glu never do.
  *
  * Errors
  *   Arguments are validated on the host before any HIP call; a bad argument

@@ -432,6 +432,7 @@ static hipError_t product(bool ta, bool tb, int64_t M, int64_t N, int64_t K, con
     g.trans_a = ta;
     g.trans_b = tb;
     g.beta = beta;
+    g.pack_long = true;
     return k4_supports(g) ? launch_k4_mfma(g, s) : launch_k1_general(g, s);
 }
 

@@ -136,6 +136,21 @@ __device__ __forceinline__ void store_glu(const GluTail& tail, float* H, int64_t
     }
 }
 
+// NV neighbouring sums of a K split's slab (glu_split_ld floats a row: the gate
+// sums in its first half, the up sums in its second).
+template <int NV>
+__device__ __forceinline__ void store_glu_slab(float* slab, int64_t ld, int row, int col, int N,
+                                               const float (&g)[NV], const float (&u)[NV]) {
+    typedef float vt __attribute__((ext_vector_type(NV)));
+    if (col >= N) return;  // a row's halves hold whole groups of four
+    vt a, b;
+#pragma unroll
+    for (int e = 0; e < NV; e++) a[e] = g[e], b[e] = u[e];
+    float* p = slab + (int64_t)row * ld + col;
+    *reinterpret_cast<vt*>(p) = a;
+    *reinterpret_cast<vt*>(p + ld / 2) = b;
+}
+
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const float* base) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(base), (short)0, (int)OOB,
                                              RSRC_WORD3);
@@ -185,12 +200,12 @@ k4_mfma(int M, int N, int K, const float* __restrict__ A, int lda, const float* 
     // workgroups per CU, and their LDS must fit the CU's 160 KiB.
     static_assert((OCC * 4 / (CF::NWAVES * WK)) * LDS_TOTAL <= 160 * 1024,
                   "occupancy target exceeds the CU's LDS");
-    static_assert(!CF::GLU || !SPLITK, "the gated form has no split mode");
     if constexpr (SPLITK) {
         const int z = blockIdx.y, k0 = z * kchunk;
         K = K - k0 < kchunk ? K - k0 : kchunk;
         A += CF::A_KMAJOR ? (int64_t)k0 : (int64_t)k0 * lda;
         B += CF::B_KMAJOR ? (int64_t)k0 : (int64_t)k0 * ldb;
+        if constexpr (CF::GLU) tail.B2 += CF::B_KMAJOR ? (int64_t)k0 : (int64_t)k0 * ldb;
         C += (int64_t)z * M * ldc;
     }
     using LA = typename CF::LA;
@@ -534,7 +549,10 @@ k4_mfma(int M, int N, int K, const float* __restrict__ A, int lda, const float* 
                         const int row = row0 + CF::a_row(wm, mb, 0) + rg * 16 + lr;
                         const v4f gq = *(const v4f*)(sg + lr * PITCH + lc), uq = *(const v4f*)(su + lr * PITCH + lc);
                         const float gv[4] = {gq[0], gq[1], gq[2], gq[3]}, uv[4] = {uq[0], uq[1], uq[2], uq[3]};
-                        if (row < M) store_glu<4>(tail, C, ldc, row, col0 + wn * CF::TN * 16 + lc, N, gv, uv, nt);
+                        const int col = col0 + wn * CF::TN * 16 + lc;
+                        if (row >= M) continue;
+                        if constexpr (SPLITK) store_glu_slab<4>(C, ldc, row, col, N, gv, uv);
+                        else store_glu<4>(tail, C, ldc, row, col, N, gv, uv, nt);
                     }
                     asm volatile("" ::: "memory");
                 }
@@ -582,7 +600,9 @@ k4_mfma(int M, int N, int K, const float* __restrict__ A, int lda, const float* 
                         su += *(const v2f*)(red + (g * CF::BM + row) * RLD + CF::BH + col);
                     }
                     const float gv[2] = {sg[0], sg[1]}, uv[2] = {su[0], su[1]};
-                    if (row0 + row < M) store_glu<2>(tail, C, ldc, row0 + row, col0 + col, N, gv, uv, false);
+                    if (row0 + row >= M) continue;
+                    if constexpr (SPLITK) store_glu_slab<2>(C, ldc, row0 + row, col0 + col, N, gv, uv);
+                    else store_glu<2>(tail, C, ldc, row0 + row, col0 + col, N, gv, uv, false);
                 }
                 if (t + (int)gridDim.x < tiles) __syncthreads();
                 continue;
@@ -954,45 +974,83 @@ hipError_t launch_k4_t64_wk4(const GemmArgs& g, hipStream_t s, int splits, int k
     return launch_k4_t32_wk4(g, s, splits, kchunk, ws);
 }
 
+// Second pass of a gated K split: G and U from S slabs, added in split order,
+// and the results; four columns a lane.
+__global__ void __launch_bounds__(64)
+glu_splitk_reduce(GluArgs g, int S, const float* __restrict__ W, int64_t ldw) {
+    const int nq = (int)((g.F + 3) / 4);
+    const int64_t total = g.M * nq, slab = g.M * ldw;
+    const GluTail tail{nullptr, g.G, g.U, g.ldgu, g.act};
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total;
+         i += (int64_t)gridDim.x * blockDim.x) {
+        const int r = (int)(i / nq), c = (int)(i % nq) * 4;
+        const float* w = W + (int64_t)r * ldw + c;
+        v4f sg = *(const v4f*)w, su = *(const v4f*)(w + ldw / 2);
+#pragma unroll 4
+        for (int z = 1; z < S; z++) {
+            sg += *(const v4f*)(w + z * slab);
+            su += *(const v4f*)(w + z * slab + ldw / 2);
+        }
+        const float gv[4] = {sg[0], sg[1], sg[2], sg[3]}, uv[4] = {su[0], su[1], su[2], su[3]};
+        store_glu<4>(tail, g.H, g.ldh, r, c, (int)g.F, gv, uv, false);
+    }
+}
+
 // The gated form on the tile configurations above, BH = BN / 2 columns of H
 // per tile.  Weights K x F take the KRows layout, F x K the KMajor one.
-template <class CF, int OCC, bool SPLIT, int WK, bool PRIO, bool PIPE, bool NOSYNC>
-static hipError_t launch_glu_cfg(const GluArgs& g, hipStream_t s) {
+// splits > 1 (CAN_SPLIT): chunks of kchunk of K into ws, then the reduction.
+template <class CF, int OCC, bool SPLIT, int WK, bool PRIO, bool PIPE, bool NOSYNC, bool CAN_SPLIT>
+static hipError_t launch_glu_cfg(const GluArgs& g, hipStream_t s, int splits, int kchunk, float* ws) {
     const int64_t tm = ceil_div(g.M, CF::BM), tn = ceil_div(g.F, CF::BH), tiles = tm * tn;
+    const GluTail tail{g.Wu, g.G, g.U, g.ldgu, g.act};
+    if constexpr (CAN_SPLIT) {
+        if (splits > 1) {
+            const int64_t ldw = glu_split_ld(g.F);
+            hipLaunchKernelGGL((k4_mfma<CF, OCC, GROUP_M, true, SPLIT, true, WK, PRIO, 2, PIPE, NOSYNC>),
+                               dim3(grid_for(tiles), splits), dim3(CF::THREADS * WK), 0, s, (int)g.M, (int)g.F,
+                               (int)g.K, g.X, (int)g.ldx, g.Wg, (int)g.ldw, ws, ldw, 1.0f, 0.0f, (int)tm,
+                               (int)tn, (int)tiles, kchunk, tail);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            const dim3 grid(grid_for(ceil_div(g.M * ceil_div(g.F, 4), 64)));
+            hipLaunchKernelGGL(glu_splitk_reduce, grid, dim3(64), 0, s, g, splits, ws, ldw);
+            return hipGetLastError();
+        }
+    }
     hipLaunchKernelGGL((k4_mfma<CF, OCC, GROUP_M, true, SPLIT, false, WK, PRIO, 2, PIPE, NOSYNC>),
                        dim3(grid_for(tiles)), dim3(CF::THREADS * WK), 0, s, (int)g.M, (int)g.F, (int)g.K,
                        g.X, (int)g.ldx, g.Wg, (int)g.ldw, g.H, g.ldh, 1.0f, 0.0f, (int)tm, (int)tn,
-                       (int)tiles, 0, GluTail{g.Wu, g.G, g.U, g.ldgu, g.act});
+                       (int)tiles, 0, tail);
     return hipGetLastError();
 }
 
 template <int WM, int WN, int TM, int TN, int BK, bool V, int NS, bool MF16, int OCC, bool SPLIT, int WK,
-          bool PRIO, bool PIPE, bool NOSYNC>
-static hipError_t launch_glu_orient(const GluArgs& g, hipStream_t s) {
+          bool PRIO, bool PIPE, bool NOSYNC, bool CAN_SPLIT>
+static hipError_t launch_glu_orient(const GluArgs& g, hipStream_t s, int splits, int kchunk, float* ws) {
     using k4::Cfg;
     if (g.transw)
-        return launch_glu_cfg<Cfg<WM, WN, TM, TN, BK, V, true, true, NS, MF16, true>, OCC, SPLIT, WK, PRIO, PIPE, NOSYNC>(g, s);
-    return launch_glu_cfg<Cfg<WM, WN, TM, TN, BK, V, true, false, NS, MF16, true>, OCC, SPLIT, WK, PRIO, PIPE, NOSYNC>(g, s);
+        return launch_glu_cfg<Cfg<WM, WN, TM, TN, BK, V, true, true, NS, MF16, true>, OCC, SPLIT, WK, PRIO, PIPE, NOSYNC, CAN_SPLIT>(g, s, splits, kchunk, ws);
+    return launch_glu_cfg<Cfg<WM, WN, TM, TN, BK, V, true, false, NS, MF16, true>, OCC, SPLIT, WK, PRIO, PIPE, NOSYNC, CAN_SPLIT>(g, s, splits, kchunk, ws);
 }
 
-hipError_t launch_k4_glu(const GluArgs& g, int cfg, bool vec, hipStream_t s) {
+hipError_t launch_k4_glu(const GluArgs& g, int cfg, bool vec, hipStream_t s, int splits, int kchunk, float* ws) {
     switch (cfg) {
         case K4_T128X256:
-            if (vec) return launch_glu_orient<2, 2, 2, 4, 16, true, 2, false, 2, true, 1, true, true, false>(g, s);
+            if (vec) return launch_glu_orient<2, 2, 2, 4, 16, true, 2, false, 2, true, 1, true, true, false, false>(g, s, 1, 0, nullptr);
             break;
         case K4_T128:
-            if (vec) return launch_glu_orient<2, 2, 2, 2, 16, true, 2, true, 4, false, 1, false, false, false>(g, s);
+            if (vec) return launch_glu_orient<2, 2, 2, 2, 16, true, 2, true, 4, false, 1, false, false, false, false>(g, s, 1, 0, nullptr);
             break;
         case K4_T64_WK4:
-            if (vec) return launch_glu_orient<2, 2, 1, 1, 32, true, 2, true, 4, true, 4, false, true, false>(g, s);
+            if (vec) return launch_glu_orient<2, 2, 1, 1, 32, true, 2, true, 4, true, 4, false, true, false, true>(g, s, splits, kchunk, ws);
             break;
         case K4_T32_WK4:
-            if (vec) return launch_glu_orient<1, 1, 1, 1, 32, true, 2, true, 2, true, 4, false, true, true>(g, s);
-            return launch_glu_orient<1, 1, 1, 1, 16, false, 2, true, 4, false, 4, false, false, true>(g, s);
+            if (vec) return launch_glu_orient<1, 1, 1, 1, 32, true, 2, true, 2, true, 4, false, true, true, true>(g, s, splits, kchunk, ws);
+            return launch_glu_orient<1, 1, 1, 1, 16, false, 2, true, 4, false, 4, false, false, true, true>(g, s, splits, kchunk, ws);
         default: break;
     }
-    if (vec) return launch_glu_orient<2, 2, 1, 1, 32, true, 2, true, 4, true, 1, false, false, false>(g, s);
-    return launch_glu_orient<2, 2, 1, 1, 16, false, 2, true, 8, false, 1, false, false, false>(g, s);
+    if (vec) return launch_glu_orient<2, 2, 1, 1, 32, true, 2, true, 4, true, 1, false, false, false, true>(g, s, splits, kchunk, ws);
+    return launch_glu_orient<2, 2, 1, 1, 16, false, 2, true, 8, false, 1, false, false, false, true>(g, s, splits, kchunk, ws);
 }
 
 }  // namespace sgemm

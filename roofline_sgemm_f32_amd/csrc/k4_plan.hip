@@ -221,7 +221,12 @@ static bool worth_packing(const GemmArgs& g, double copied) {
     const bool thin_copy = moved >= 64e6 && copied <= moved / 8;
     const bool heavy = (flop >= 4e9 || (flop >= 1e9 && g.K >= 1536)) && copied <= 64e6 &&
                        copied <= flop / 100;
-    return big_output || thin_copy || heavy;
+    // The feed-forward products (g.pack_long) pack longer operands too, where
+    // the copies are a quarter of the product's time at most and 4-byte loads
+    // cost more (the backward pass of 421 x 5871 x 3874, copies of 102 MB for
+    // each product, 932 -> 816 us).
+    const bool longer = g.pack_long && flop >= 4e9 && copied <= flop / 150;
+    return big_output || thin_copy || heavy || longer;
 }
 
 // Whether an eager shape-chosen call packs g's operands first, and then how.
@@ -496,6 +501,7 @@ hipError_t launch_k4_mfma(const GemmArgs& g, hipStream_t s, int requested, bool 
 static GemmArgs glu_product(const GluArgs& g) {
     GemmArgs p{g.M, 2 * g.F, g.K, g.X, g.ldx, g.Wg, g.ldw, g.H, g.ldh};
     p.trans_b = g.transw;
+    p.pack_long = true;
     return p;
 }
 
@@ -507,44 +513,70 @@ hipError_t launch_glu(const GluArgs& g, hipStream_t s) {
     const bool x_vec = rows_vec(g.X, g.ldx, g.K);
     const int64_t w_rows = g.transw ? g.F : g.K, w_run = g.transw ? g.K : g.F;
     const bool w_vec = rows_vec(g.Wg, g.ldw, w_run) && rows_vec(g.Wu, g.ldw, w_run);
-    if (x_vec && w_vec) return launch_k4_glu(g, k4_plan(p, 1).cfg, true, s);
 
-    // Packed copies, as the product's own path makes them and under the same
-    // conditions: X, then both weights.
+    // As the product's own path: packed copies of unaligned operands and a K
+    // split where the plan has one, both in the workspace, which captured calls
+    // do without.  Splits, weights F x K: 217 x 4160 x 3000 148 -> 114 us, 64 x
+    // 4096 x 4096 68 -> 41 us, 256 x 1024 x 8192 133 -> 70 us, 24 x 256 x 16384
+    // 86 -> 16 us.
+    const bool eager = !capturing(s);
     const auto bytes = [](int64_t rows, int64_t run) {
         return (size_t(rows * packed_ld(run)) * sizeof(float) + 255) / 256 * 256;
     };
-    const size_t x_bytes = x_vec ? 0 : bytes(g.M, g.K), w_bytes = w_vec ? 0 : bytes(w_rows, w_run);
+    size_t x_bytes = x_vec ? 0 : bytes(g.M, g.K), w_bytes = w_vec ? 0 : bytes(w_rows, w_run);
+    const bool vec = x_vec && w_vec;
+    const bool pack = !vec && eager && worth_packing(p, double(x_bytes + 2 * w_bytes));
+    if (pack) {
+        // The plan sees the copies' alignment, here through placeholders.
+        if (!x_vec) {
+            p.A = reinterpret_cast<const float*>(uintptr_t(256));
+            p.lda = packed_ld(g.K);
+        }
+        if (!w_vec) {
+            p.B = reinterpret_cast<const float*>(uintptr_t(256));
+            p.ldb = packed_ld(w_run);
+        }
+        p.runs_padded = true;
+    } else {
+        x_bytes = w_bytes = 0;
+        // An unaligned up weight counts as an unaligned gate weight.
+        if (!w_vec) p.B = reinterpret_cast<const float*>(uintptr_t(4));
+    }
+    SplitPlan plan = k4_plan(p, eager ? 0 : 1);
+    const size_t copies = x_bytes + 2 * w_bytes;
+    const size_t slabs = plan.splits > 1 ? size_t(plan.splits) * g.M * glu_split_ld(g.F) * sizeof(float) : 0;
     Workspace ws;
-    if (worth_packing(p, double(x_bytes + 2 * w_bytes)) && !capturing(s)) {
-        if (workspace_acquire(x_bytes + 2 * w_bytes, s, &ws) == hipSuccess) {
+    if (copies + slabs > 0) {
+        if (workspace_acquire(copies + slabs, s, &ws) == hipSuccess) {
             char* base = static_cast<char*>(ws.ptr);
             GluArgs q = g;
             hipError_t e = hipSuccess;
-            if (!x_vec) {
-                q.X = reinterpret_cast<float*>(base);
+            if (x_bytes) {
+                float* px = reinterpret_cast<float*>(base);
+                q.X = px;
                 q.ldx = packed_ld(g.K);
-                e = launch_pack(g.X, g.M, g.K, g.ldx, reinterpret_cast<float*>(base), nullptr, 0, 0, 0, nullptr, s);
+                e = launch_pack(g.X, g.M, g.K, g.ldx, px, nullptr, 0, 0, 0, nullptr, s);
             }
-            if (!w_vec && e == hipSuccess) {
+            if (w_bytes && e == hipSuccess) {
                 float *pg = reinterpret_cast<float*>(base + x_bytes), *pu = reinterpret_cast<float*>(base + x_bytes + w_bytes);
                 q.Wg = pg;
                 q.Wu = pu;
                 q.ldw = packed_ld(w_run);
                 e = launch_pack(g.Wg, w_rows, w_run, g.ldw, pg, g.Wu, w_rows, w_run, g.ldw, pu, s);
             }
-            GemmArgs pp = glu_product(q);
-            pp.runs_padded = true;
-            if (e == hipSuccess) e = launch_k4_glu(q, k4_plan(pp, 1).cfg, true, s);
+            if (e == hipSuccess)
+                e = launch_k4_glu(q, plan.cfg, vec || pack, s, plan.splits, (int)plan.kchunk,
+                                  reinterpret_cast<float*>(base + copies));
             const hipError_t f = workspace_release(&ws, s);
             return e != hipSuccess ? e : f;
         }
+        // No workspace: unsplit, on the operands as stored.
         (void)hipGetLastError();
+        GemmArgs r = glu_product(g);
+        if (!w_vec) r.B = reinterpret_cast<const float*>(uintptr_t(4));
+        plan = k4_plan(r, 1);
     }
-    // The plan sees alignment through the product's operands: an unaligned up
-    // weight counts as an unaligned gate weight.
-    if (!w_vec) p.B = reinterpret_cast<const float*>(uintptr_t(4));
-    return launch_k4_glu(g, k4_plan(p, 1).cfg, false, s);
+    return launch_k4_glu(g, plan.cfg, vec, s);
 }
 
 }  // namespace sgemm

@@ -24,6 +24,8 @@ struct GemmArgs {
     // Rows of A and B as stored hold their run rounded up to 4 floats, the
     // extra ones zero (packed operands: see pack.hip).
     bool runs_padded = false;
+    // Packed copies may be made of longer operands (worth_packing).
+    bool pack_long = false;
 };
 
 // Upper bound on the number of workgroups a launch uses; kernels loop over
@@ -202,8 +204,12 @@ struct GluArgs {
     int64_t ldgu;
 };
 // The matrix-core kernel's gated form in tile configuration cfg (K4Cfg), with
-// 16-byte loads (vec) or 4-byte ones.
-hipError_t launch_k4_glu(const GluArgs& g, int cfg, bool vec, hipStream_t s);
+// 16-byte loads (vec) or 4-byte ones; splits > 1 runs that many chunks of
+// kchunk of K into ws (splits slabs of M rows of glu_split_ld(F) floats: the
+// gate sums, then the up sums), then a reduction that finishes the results.
+hipError_t launch_k4_glu(const GluArgs& g, int cfg, bool vec, hipStream_t s, int splits = 1,
+                         int kchunk = 0, float* ws = nullptr);
+inline int64_t glu_split_ld(int64_t F) { return 2 * split_ld(F); }
 // One to sixteen rows of X on the vector units, and whether they can run g.
 bool glu_thin_ok(const GluArgs& g);
 hipError_t launch_glu_thin(const GluArgs& g, hipStream_t s);

@@ -82,6 +82,43 @@ def test_integer_operands_are_exact(shape, transw):
     assert torch.equal(H.cpu().double(), h)
 
 
+# Outputs of few tiles under a long K, which eager calls split across
+# workgroups: 32 x 32 tiles (the last two F with 4-byte loads, as no row of
+# the weights or of X is aligned), 64 x 64 tiles, chunks that end inside a
+# slab, and packed copies that are split too (417 x 3001).
+SPLIT_SHAPES = [(17, 4096, 256), (24, 2052, 130), (64, 1028, 60), (33, 16384, 4), (20, 2047, 255),
+                (17, 1537, 1), (217, 2100, 1200), (65, 4100, 2052), (300, 2048, 516), (417, 3001, 1025)]
+
+
+@pytest.mark.parametrize("transw", [False, True], ids=["KxF", "FxK"])
+@pytest.mark.parametrize("shape", SPLIT_SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_long_sums_over_few_tiles(shape, transw):
+    M, K, F = shape
+    i = SPLIT_SHAPES.index(shape)
+    act = ACTS[i % len(ACTS)]
+    X, Wg, Wu, host = operands(M, K, F, transw, seed=100 + i, kind=("halves", "separate", "gaps")[i % 3])
+    H, G, U = (Guarded(M, F, gap=g) for g in (3, 0, 0))
+    U.ld = G.ld
+    rs.glu(X, Wg, Wu, act=act, transw=transw, out=H.view, save=(G.view, U.view))
+    ref, err = glu64(act, *host)
+    for o, r, e, n in zip((H, G, U), ref, err, "HGU"):
+        assert_within(o.view, r, e, n)
+        assert o.intact(), f"{n}: wrote outside its view"
+    for _ in range(3):
+        assert torch.equal(rs.glu(X, Wg, Wu, act=act, transw=transw), H.view)
+    # A captured call runs unsplit, within the same bounds on every replay.
+    out = torch.empty((M, F), device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rs.glu(X, Wg, Wu, act=act, transw=transw, out=out)
+    for _ in range(3):
+        out.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert_within(out, ref[0], err[0], "replay")
+        assert torch.equal(rs.glu(X, Wg, Wu, act=act, transw=transw), H.view)
+
+
 @pytest.mark.parametrize("act", ACTS)
 def test_every_activation_over_its_range(act):
     # K = 1: G = x wg and U = x wu exactly representable, so only the

@@ -505,6 +505,23 @@ static GemmArgs glu_product(const GluArgs& g) {
     return p;
 }
 
+// The gated form's tile and K split: those of its product p, but 32 x 32 tiles
+// for 32 rows at most of F x K weights, half of whose 64-row tiles would be
+// empty (32 x 8192 x 4096 85 -> 60 us, 32 x 22016 x 2048 109 -> 80 us, 32 x
+// 22016 x 4097, 4-byte loads, 520 -> 483 us).  Two of their workgroups share a
+// CU; one and a half rounds run as three halves of K (32 x 10240 x 4096 91 -> 82
+// us, but 32 x 14336 x 4096, nearly two full rounds, 106 -> 113 us).  Weights K
+// x F, read 16 columns a row, gain nothing from it (32 x 22016 x 8192 386 -> 388
+// us, 24 x 11008 x 4096 106 -> 119 us).
+static SplitPlan glu_plan(const GluArgs& g, const GemmArgs& p, bool may_split) {
+    const SplitPlan plan = k4_plan(p, may_split ? 0 : 1);
+    if (!g.transw || g.M > 32 || plan.cfg == K4_T32_WK4) return plan;
+    const int64_t T = ceil_div(p.N, 32), half = ceil_div(ceil_div(g.K, 2), 32) * 32;
+    const bool split = may_split && T > 2 * kCUs && T <= 3 * kCUs && g.K >= 2048;
+    // ws_floats sizes a product's slabs; launch_glu sizes its own.
+    return {split ? 2 : 1, split ? half : g.K, 0, K4_T32_WK4};
+}
+
 hipError_t launch_glu(const GluArgs& g, hipStream_t s) {
     if (glu_thin_ok(g)) return launch_glu_thin(g, s);
     GemmArgs p = glu_product(g), one = p;
@@ -542,7 +559,7 @@ hipError_t launch_glu(const GluArgs& g, hipStream_t s) {
         // An unaligned up weight counts as an unaligned gate weight.
         if (!w_vec) p.B = reinterpret_cast<const float*>(uintptr_t(4));
     }
-    SplitPlan plan = k4_plan(p, eager ? 0 : 1);
+    SplitPlan plan = glu_plan(g, p, eager);
     const size_t copies = x_bytes + 2 * w_bytes;
     const size_t slabs = plan.splits > 1 ? size_t(plan.splits) * g.M * glu_split_ld(g.F) * sizeof(float) : 0;
     Workspace ws;
@@ -574,7 +591,7 @@ hipError_t launch_glu(const GluArgs& g, hipStream_t s) {
         (void)hipGetLastError();
         GemmArgs r = glu_product(g);
         if (!w_vec) r.B = reinterpret_cast<const float*>(uintptr_t(4));
-        plan = k4_plan(r, 1);
+        plan = glu_plan(g, r, false);
     }
     return launch_k4_glu(g, plan.cfg, vec, s);
 }

@@ -522,6 +522,20 @@ static SplitPlan glu_plan(const GluArgs& g, const GemmArgs& p, bool may_split) {
     return {split ? 2 : 1, split ? half : g.K, 0, K4_T32_WK4};
 }
 
+// Whether a gated call packs its unaligned operands: as its product would, but
+// wide unaligned weights are not copied for few rows, each of which pays for
+// the copy with M products per weight only.  F x K: up to 32 rows (32 x 22016 x
+// 4097: packed 495 us, not 255; 20 x 16384 x 2047: 197, 89), or one or two full
+// 64-row tiles, whose loads need no row checks (64 x 16384 x 2047: 220, 131; 128
+// rows: 247, 186; but 48 rows: 196, 245; 100 rows: 243, 255).  K x F: below 300
+// rows (64 x 16385 x 1023: 100, 66; 200 rows: 199, 188; 300 rows: 232, 215).
+static bool glu_worth_packing(const GluArgs& g, const GemmArgs& p, size_t x_bytes, size_t w_bytes) {
+    const bool wide = ceil_div(p.M, 64) * ceil_div(p.N, 64) >= 512;
+    const bool few = g.transw ? g.M <= 32 || g.M == 64 || g.M == 128 : g.M < 300;
+    if (w_bytes > 0 && wide && few) return false;
+    return worth_packing(p, double(x_bytes + 2 * w_bytes));
+}
+
 hipError_t launch_glu(const GluArgs& g, hipStream_t s) {
     if (glu_thin_ok(g)) return launch_glu_thin(g, s);
     GemmArgs p = glu_product(g), one = p;
@@ -542,7 +556,7 @@ hipError_t launch_glu(const GluArgs& g, hipStream_t s) {
     };
     size_t x_bytes = x_vec ? 0 : bytes(g.M, g.K), w_bytes = w_vec ? 0 : bytes(w_rows, w_run);
     const bool vec = x_vec && w_vec;
-    const bool pack = !vec && eager && worth_packing(p, double(x_bytes + 2 * w_bytes));
+    const bool pack = !vec && eager && glu_worth_packing(g, p, x_bytes, w_bytes);
     if (pack) {
         // The plan sees the copies' alignment, here through placeholders.
         if (!x_vec) {

@@ -86,10 +86,12 @@ def test_integer_operands_are_exact(shape, transw):
 # workgroups: 32 x 32 tiles (the last two F with 4-byte loads, as no row of
 # the weights or of X is aligned), 64 x 64 tiles, chunks that end inside a
 # slab, and packed copies that are split too (417 x 3001); and at most 32 rows
-# of wide weights, split in two or not.
+# of wide weights, split in two or not; and wide unaligned weights under few
+# rows (packed or not) and many.
 SPLIT_SHAPES = [(17, 4096, 256), (24, 2052, 130), (64, 1028, 60), (33, 16384, 4), (20, 2047, 255),
                 (17, 1537, 1), (217, 2100, 1200), (65, 4100, 2052), (300, 2048, 516), (417, 3001, 1025),
-                (32, 2080, 9216), (23, 2049, 9001), (17, 260, 8200), (32, 95, 16400)]
+                (32, 2080, 9216), (23, 2049, 9001), (17, 260, 8200), (32, 95, 16400),
+                (20, 67, 16385), (64, 131, 16385), (128, 35, 8200), (100, 69, 8193), (310, 37, 4098)]
 
 
 @pytest.mark.parametrize("transw", [False, True], ids=["KxF", "FxK"])

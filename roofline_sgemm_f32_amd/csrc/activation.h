@@ -65,8 +65,12 @@ __device__ __forceinline__ void act_grad(int act, float g, float* a, float* da) 
         case ACT_GELU_TANH: {
             const float s = logistic(gelu_tanh_arg2(g));
             *a = g * s;
-            // d/dg of 2 c (g + 0.044715 g^3) = 2 c (1 + 0.134145 g^2)
-            *da = s * fmaf(g * (1.0f - s), 1.5957691216057308f * fmaf(0.134145f * g, g, 1.0f), 1.0f);
+            // da = s + g s (1 - s) v', v' = 2 c (1 + 0.134145 g^2).  s (1 - s) is
+            // exp(-|v|) or less, 0 in float from |g| = 11 on (v = 112): formed
+            // first, and with g cut there in the other factors, the product is 0
+            // and not 0 times an overflow.
+            const float t = s * (1.0f - s), gc = fminf(fmaxf(g, -12.0f), 12.0f);
+            *da = fmaf(gc * t, 1.5957691216057308f * fmaf(0.134145f * gc, gc, 1.0f), s);
             return;
         }
         case ACT_RELU:

@@ -1,8 +1,8 @@
 // Activations of the gated feed-forward block and their derivatives, in
-// float.  Written so that both tails keep their relative accuracy: the
-// logistic form for silu and tanh-gelu (0.5 (1 + tanh v) = 1 / (1 + exp(-2v)))
-// and erfc for gelu (0.5 (1 + erf(g / sqrt 2)) = 0.5 erfc(-g / sqrt 2)),
-// which do not cancel for negative g.
+// float.  Written so that the tails do not cancel: the logistic function for
+// silu, sigmoid and tanh-gelu (0.5 (1 + tanh v) = 1 / (1 + exp(-2v))), with its
+// complement for the derivatives, each from the exponential that is small on
+// its side, and erfc for gelu (0.5 (1 + erf(g / sqrt 2)) = 0.5 erfc(-g / sqrt 2)).
 #pragma once
 #include <hip/hip_runtime.h>
 
@@ -14,6 +14,14 @@ namespace sgemm {
 enum Act { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2, ACT_RELU = 3, ACT_SIGMOID = 4 };
 constexpr int kActCount = 5;
 
+// 1 / (1 + exp(-v)) and its complement 1 / (1 + exp(v)).
+struct Logistic {
+    float s, r;
+};
+__device__ __forceinline__ Logistic logistic2(float v) {
+    const float e = expf(-fabsf(v)), q = 1.0f / (1.0f + e);
+    return v < 0.0f ? Logistic{e * q, q} : Logistic{q, e * q};
+}
 __device__ __forceinline__ float logistic(float v) { return 1.0f / (1.0f + expf(-v)); }
 
 // 2 c (g + 0.044715 g^3), c = sqrt(2 / pi): twice the argument of tanh.
@@ -51,9 +59,9 @@ __device__ __forceinline__ void act_values(int act, const float (&g)[N], float (
 __device__ __forceinline__ void act_grad(int act, float g, float* a, float* da) {
     switch (act) {
         case ACT_SILU: {
-            const float s = logistic(g);
-            *a = g * s;
-            *da = s * fmaf(g, 1.0f - s, 1.0f);
+            const Logistic l = logistic2(g);
+            *a = g * l.s;
+            *da = l.s * fmaf(g, l.r, 1.0f);
             return;
         }
         case ACT_GELU: {
@@ -63,14 +71,14 @@ __device__ __forceinline__ void act_grad(int act, float g, float* a, float* da) 
             return;
         }
         case ACT_GELU_TANH: {
-            const float s = logistic(gelu_tanh_arg2(g));
-            *a = g * s;
+            const Logistic l = logistic2(gelu_tanh_arg2(g));
+            *a = g * l.s;
             // da = s + g s (1 - s) v', v' = 2 c (1 + 0.134145 g^2).  s (1 - s) is
             // exp(-|v|) or less, 0 in float from |g| = 11 on (v = 112): formed
             // first, and with g cut there in the other factors, the product is 0
             // and not 0 times an overflow.
-            const float t = s * (1.0f - s), gc = fminf(fmaxf(g, -12.0f), 12.0f);
-            *da = fmaf(gc * t, 1.5957691216057308f * fmaf(0.134145f * gc, gc, 1.0f), s);
+            const float t = l.s * l.r, gc = fminf(fmaxf(g, -12.0f), 12.0f);
+            *da = fmaf(gc * t, 1.5957691216057308f * fmaf(0.134145f * gc, gc, 1.0f), l.s);
             return;
         }
         case ACT_RELU:
@@ -78,9 +86,9 @@ __device__ __forceinline__ void act_grad(int act, float g, float* a, float* da) 
             *da = g > 0.0f ? 1.0f : 0.0f;
             return;
         default: {
-            const float s = logistic(g);
-            *a = s;
-            *da = s * (1.0f - s);
+            const Logistic l = logistic2(g);
+            *a = l.s;
+            *da = l.s * l.r;
             return;
         }
     }

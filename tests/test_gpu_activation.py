@@ -97,3 +97,12 @@ def test_tails_of_the_backward_pass(act):
     da, a = derivative(act, g)
     assert_tails(act, "derivative", g, da, der, eder)
     assert_tails(act, "value", g, a, val, eval_)
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_tails_of_the_forward_pass(act):
+    g = tail_points()
+    val, _, err, _ = tails64(act, g.double())
+    one = torch.ones((1, 1), device="cuda")
+    H = rs.glu(one, g[None].cuda(), torch.ones((1, g.numel()), device="cuda"), act=act)
+    assert_tails(act, "forward", g, H[0].cpu(), val, err)

@@ -48,9 +48,11 @@ q4_general(Q4Args g, int64_t tiles) {
                     const int v = (k & 1 ? b >> 4 : b & 15) - z;
                     part = fmaf(load_float(g.xtype, g.X, m * g.ldx + k), float(v), part);
                 }
+                // The group's whole sum meets its scale: lanes without a part of
+                // it (groups of 32) would make NaN of an infinite one.
+                for (int o = 32; o > 0; o >>= 1) part += __shfl_xor(part, o);
                 sum = fmaf(load_float(g.stype, g.S[w], n * g.lds + q), part, sum);
             }
-            for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
             out[w] = sum;
         }
         const float y = g.act >= 0 ? act_value(g.act, out[0]) * out[1] : out[0];

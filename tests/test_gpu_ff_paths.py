@@ -1,0 +1,101 @@
+"""The gated feed-forward block and the 4-bit products on the paths that only
+large strides, large outputs or long rows take."""
+import pytest
+import torch
+
+import roofline_sgemm_f32_amd as rs
+from tests.ff_util import (ACTS, LIPSCHITZ, TYPES, U, Guarded, act64, act_err, assert_within, glu64,
+                           glu_backward64, q4_64, q4_int, q4_make, rounded)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    rs.load()
+
+
+def strided(t, ld):
+    """t with rows ld apart in a buffer of its own; what lies between is NaN
+    (255 for bytes)."""
+    fill = float("nan") if t.dtype.is_floating_point else 255
+    buf = torch.full(((t.shape[0] - 1) * ld + t.shape[1],), fill, dtype=t.dtype, device="cuda")
+    v = torch.as_strided(buf, t.shape, (ld, 1))
+    v.copy_(t)
+    return v
+
+
+# Rows too long for 32-bit offsets within a tile: 4 Mi elements of X, 8 MiB of
+# packed weights.
+LONG_X, LONG_W = 1 << 22, 1 << 23
+
+
+@pytest.mark.parametrize("x", TYPES)
+@pytest.mark.parametrize("shape", [(1, 5, 70, 32), (3, 4, 257, 64), (2, 7, 1000, 128), (2, 3, 333, 512)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_4bit_rows_of_any_stride(shape, x):
+    M, N, K, group = shape
+    gen = torch.Generator().manual_seed(N)
+    X = torch.randn((M, K), generator=gen).to(TYPES[x])
+    w, s, z = q4_make(gen, N, K, group, TYPES[x], N % 2 == 0)
+    ref, err = q4_64(X, w, s, z, group)
+    wide_w = strided(w, LONG_W)
+    Y = Guarded(M, N, TYPES[x], gap=2)
+    rs.q4_matmul(X.cuda(), wide_w, s, z, group=group, out=Y.view)
+    assert_within(Y.view, ref, rounded(ref, err, TYPES[x]), "long rows of weights")
+    assert Y.intact()
+    if M > 1:
+        got = rs.q4_matmul(strided(X, LONG_X), w, s, z, group=group)
+        assert_within(got, ref, rounded(ref, err, TYPES[x]), "long rows of X")
+    up = q4_make(gen, N, K, group, TYPES[x], N % 2 == 0)
+    u, eu = q4_64(X, *up, group)
+    H = rs.q4_glu(X.cuda(), wide_w, s, strided(up[0], LONG_W), up[1], z, up[2], group=group, act="gelu")
+    h = act64("gelu", ref)[0] * u
+    eh = (LIPSCHITZ * err + act_err(ref)) * (u.abs() + eu) + act64("gelu", ref)[0].abs() * eu + 2 * U * h.abs()
+    assert_within(H, h, rounded(h, eh, TYPES[x]), "gated")
+
+
+@pytest.mark.parametrize("K", [96, 97, 288])
+def test_4bit_infinite_scale_of_any_stride(K):
+    """An infinite scale gives infinities of its group's sign, as on rows of
+    ordinary strides, though the group is shared out over lanes."""
+    group = 32
+    X = torch.ones((2, K), device="cuda")
+    X[1] = -1.0
+    w = strided(torch.full((3, (K + 1) // 2), 0x99, dtype=torch.uint8, device="cuda"), LONG_W)  # q - z = 1
+    s = torch.ones((3, -(-K // group)), device="cuda")
+    s[1, 1] = float("inf")
+    Y = rs.q4_matmul(X, w, s, group=group)
+    assert Y[0, 1] == float("inf") and Y[1, 1] == -float("inf")
+    assert (Y[0, [0, 2]] == K).all() and (Y[1, [0, 2]] == -K).all()
+
+
+@pytest.mark.parametrize("save", [False, True])
+def test_gated_rows_of_any_stride(save):
+    """Rows of X of 4.2 Mi floats and rows of K x F weights of 17.4 Mi, past
+    the matrix kernel's 32-bit offsets; and the products of the backward pass
+    there."""
+    gen = torch.Generator().manual_seed(1)
+    M, K, F = 18, 21, 37
+    X, W = torch.randn((M, K), generator=gen), torch.randn((2, K, F), generator=gen)
+    ref, err = glu64("gelu_tanh", X.double(), W[0].double(), W[1].double())
+    def check(X, Wg, Wu, transw):
+        H, G, Up = Guarded(M, F, gap=1), Guarded(M, F), Guarded(M, F)
+        rs.glu(X, Wg, Wu, act="gelu_tanh", transw=transw, out=H.view,
+               save=(G.view, Up.view) if save else False)
+        for o, r, e in zip((H, G, Up) if save else (H,), ref, err):
+            assert_within(o.view, r, e)
+            assert o.intact()
+    T = W.transpose(1, 2).contiguous().cuda()
+    check(strided(X, 4230000), T[0], T[1], True)
+    wide = [strided(W[i, :6], 17400000) for i in range(2)]
+    ref, err = glu64("gelu_tanh", X[:, :6].double(), W[0, :6].double(), W[1, :6].double())
+    check(X[:, :6].contiguous().cuda(), wide[0], wide[1], False)
+    G, Up, dH = (torch.randn((M, F), generator=gen) for _ in range(3))
+    want, err = glu_backward64("silu", X[:, :6].double(), W[0, :6].double(), W[1, :6].double(), G.double(),
+                               Up.double(), dH.double())
+    dX, dWg, dWu = rs.glu_backward(dH.cuda(), X[:, :6].contiguous().cuda(), *wide, G.cuda(), Up.cuda())
+    for o, r, e in zip((dX, dWg, dWu), want[2:], err[2:]):
+        assert_within(o, r, e)

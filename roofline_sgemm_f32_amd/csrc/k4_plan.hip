@@ -556,18 +556,22 @@ hipError_t launch_glu(const GluArgs& g, hipStream_t s) {
     };
     size_t x_bytes = x_vec ? 0 : bytes(g.M, g.K), w_bytes = w_vec ? 0 : bytes(w_rows, w_run);
     const bool vec = x_vec && w_vec;
-    const bool pack = !vec && eager && glu_worth_packing(g, p, x_bytes, w_bytes);
+    // The product on the copies; the plan sees their alignment, here through
+    // placeholders.  Their rows may be a few floats longer than the originals':
+    // past the 32-bit offsets, the operands stay as stored.
+    GemmArgs c = p;
+    if (!x_vec) {
+        c.A = reinterpret_cast<const float*>(uintptr_t(256));
+        c.lda = packed_ld(g.K);
+    }
+    if (!w_vec) {
+        c.B = reinterpret_cast<const float*>(uintptr_t(256));
+        c.ldb = packed_ld(w_run);
+    }
+    c.runs_padded = true;
+    const bool pack = !vec && eager && k4_supports(c) && glu_worth_packing(g, p, x_bytes, w_bytes);
     if (pack) {
-        // The plan sees the copies' alignment, here through placeholders.
-        if (!x_vec) {
-            p.A = reinterpret_cast<const float*>(uintptr_t(256));
-            p.lda = packed_ld(g.K);
-        }
-        if (!w_vec) {
-            p.B = reinterpret_cast<const float*>(uintptr_t(256));
-            p.ldb = packed_ld(w_run);
-        }
-        p.runs_padded = true;
+        p = c;
     } else {
         x_bytes = w_bytes = 0;
         // An unaligned up weight counts as an unaligned gate weight.

@@ -99,3 +99,17 @@ def test_gated_rows_of_any_stride(save):
     dX, dWg, dWu = rs.glu_backward(dH.cuda(), X[:, :6].contiguous().cuda(), *wide, G.cuda(), Up.cuda())
     for o, r, e in zip((dX, dWg, dWu), want[2:], err[2:]):
         assert_within(o, r, e)
+
+
+def test_packed_weights_past_the_offset_limit():
+    """K x F weights whose rows just fit the matrix kernel's 32-bit offsets and
+    whose packed copies, a few floats longer, do not.  Integers: every
+    operation is exact."""
+    M, K, F = 300, 32, 17318403
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    X = torch.randint(-2, 3, (M, K), generator=gen, device="cuda").float()
+    Wg, Wu = (torch.randint(-2, 3, (K, F), generator=gen, device="cuda", dtype=torch.float32) for _ in range(2))
+    H = rs.glu(X, Wg, Wu, act="relu")
+    for c in (slice(0, 300), slice(F // 2, F // 2 + 300), slice(F - 300, F)):
+        (h, _, _), _ = glu64("relu", *(t.cpu().double() for t in (X, Wg[:, c], Wu[:, c])))
+        assert torch.equal(H[:, c].cpu().double(), h)

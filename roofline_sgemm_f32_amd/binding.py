@@ -9,8 +9,6 @@ from __future__ import annotations
 import ctypes
 import os
 
-import torch
-
 HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(HERE, "libsgemm.so")
 _lib = None
@@ -54,9 +52,12 @@ OP_N, OP_T = 0, 1
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}
 
 
-# sgemm_type_t
-_F32 = torch.float32
-_FLOATS = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+# Importing this module does not import torch: the feed-forward functions,
+# whose calls take microseconds, do so once, through _use_torch, which sets
+# these (sgemm_type_t of the tensor types; a device's current stream's handle).
+torch = None
+_FLOATS = {}
+_raw_stream = None
 
 
 class SgemmError(RuntimeError):
@@ -296,14 +297,14 @@ def sgemm_colmajor(A, B, out, transa=False, transb=False, alpha=1.0, beta=0.0):
     return out
 
 
-def _raw_stream(dev: int) -> int:
-    """Handle of device dev's current stream."""
-    return torch._C._cuda_getCurrentRawStream(dev)
-
-
-if not hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the public way, 2 us slower
-    def _raw_stream(dev: int) -> int:  # noqa: F811
-        return torch.cuda.current_stream(dev).cuda_stream
+def _use_torch() -> None:
+    global torch, _raw_stream
+    import torch
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if _raw_stream is None:  # the public way, 2 us slower
+        def _raw_stream(dev):
+            return torch.cuda.current_stream(dev).cuda_stream
+    _FLOATS.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
 
 
 def _act_id(act) -> int:
@@ -316,7 +317,7 @@ def _rows(t, name, shape=None, dtypes=None):
     """Leading dimension of a 2-D row-major GPU tensor, checked."""
     try:  # the usual case in few steps: these calls take microseconds
         (rows, cols), (ld, step) = t.shape, t.stride()
-        if (t.is_cuda and (t.dtype in dtypes if dtypes else t.dtype == _F32)
+        if (t.is_cuda and (t.dtype in dtypes if dtypes else t.dtype == torch.float32)
                 and (shape is None or (rows, cols) == shape) and (step == 1 or cols == 1)):
             if rows > 1 and ld >= cols > 0:
                 return ld
@@ -324,10 +325,11 @@ def _rows(t, name, shape=None, dtypes=None):
                 return cols
     except (AttributeError, ValueError):
         pass
-    return _rows_checked(t, name, shape, dtypes or (_F32,))
+    return _rows_checked(t, name, shape, dtypes)
 
 
 def _rows_checked(t, name, shape, dtypes):
+    dtypes = dtypes or (torch.float32,)
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
         raise TypeError(f"{name} must be a tensor of {' or '.join(str(d) for d in dtypes)}")
     if t.device.type != "cuda":
@@ -380,6 +382,7 @@ def glu(X, Wg, Wu, act="silu", transw=False, out=None, save=False):
     gelu, gelu_tanh, relu or sigmoid.  Returns H (M x F, ``out`` when given);
     with ``save`` true (H, G, U), with G = X Wg and U = X Wu, which
     glu_backward takes.  ``save`` may also be the pair (G, U) to write."""
+    _FLOATS or _use_torch()
     a = _act_id(act)
     ldx = _rows(X, "X")
     M, K = X.shape
@@ -411,6 +414,7 @@ def glu_backward(dH, X, Wg, Wu, G, U, act="silu", transw=False, need_dx=True, ne
     ``dX`` and ``dW`` = (dWg, dWu) may be supplied; with ``beta`` the weight
     gradients are added to beta times what dW holds.  ``inplace`` overwrites
     G and U with dG and dU instead of allocating M x 2F floats for them."""
+    _FLOATS or _use_torch()
     a = _act_id(act)
     ldx = _rows(X, "X")
     M, K = X.shape
@@ -471,6 +475,7 @@ def q4_matmul(X, w, scales, zeros=None, group=128, out=None):
     bfloat16, and so is Y; ``scales`` is N x ceil(K / group) of any of these
     types, ``zeros`` uint8 of that shape (None: 8).  ``group`` is a power of
     two, 32 or more.  Sums are kept in float32 and rounded once."""
+    _FLOATS or _use_torch()
     group = _q4_group(group)
     ldx = _rows(X, "X", None, _FLOATS)
     M, K = X.shape
@@ -492,6 +497,7 @@ def q4_glu(X, gate_w, gate_scales, up_w, up_scales, gate_zeros=None, up_zeros=No
     """The gated feed-forward block with 4-bit weights, H = act(G) * U, where G
     and U are q4_matmul's products of X with the gate and the up weights (the
     same shapes, types and row strides); G and U stay in float32."""
+    _FLOATS or _use_torch()
     a, group = _act_id(act), _q4_group(group)
     ldx = _rows(X, "X", None, _FLOATS)
     M, K = X.shape

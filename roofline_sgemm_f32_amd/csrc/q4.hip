@@ -28,31 +28,47 @@ __device__ __forceinline__ void store_as(void* p, int64_t i, float v) {
 
 }  // namespace
 
-// Any strides and sizes (64-bit offsets): one output per wave, a group at a
-// time, its K dealt to the lanes.  The fallback for operands whose rows are
-// too long for the 32-bit offsets of the kernels above.
+// Any strides and sizes (64-bit offsets): one output per wave, four groups at a
+// time, their K dealt to the lanes.  The fallback for operands whose rows are
+// too long for the 32-bit offsets of the kernels above.  A group's whole sum
+// meets its scale: lanes without a part of it (groups of 32) would make NaN of
+// an infinite one.  The four sums meet by halving exchanges, seven in all, and
+// lanes 16 i .. hold group i's (8 x 4096 x 4096, float16: groups of 32 321 us, of
+// 128 122; with every lane scaling its part of each group 333 and 126; one
+// group's exchanges at a time 443 and 150).
 __global__ void __launch_bounds__(64)
 q4_general(Q4Args g, int64_t tiles) {
     const int64_t group = int64_t(1) << g.shift, groups = (g.K + group - 1) >> g.shift;
+    const int lane = threadIdx.x;
     for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
         const int64_t m = t / g.N, n = t % g.N;
         float out[2] = {0.0f, 0.0f};
         for (int w = 0; w < (g.act >= 0 ? 2 : 1); w++) {
             float sum = 0.0f;
-            for (int64_t q = 0; q < groups; q++) {
-                const int64_t k0 = q << g.shift, k1 = k0 + group < g.K ? k0 + group : g.K;
-                const int z = g.Z[w] ? g.Z[w][n * g.ldz + q] : 8;
-                float part = 0.0f;
-                for (int64_t k = k0 + threadIdx.x; k < k1; k += 64) {
-                    const int b = g.W[w][n * g.ldw + k / 2];
-                    const int v = (k & 1 ? b >> 4 : b & 15) - z;
-                    part = fmaf(load_float(g.xtype, g.X, m * g.ldx + k), float(v), part);
+            for (int64_t q0 = 0; q0 < groups; q0 += 4) {
+                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int64_t q = q0 + i;
+                    if (q >= groups) break;
+                    const int64_t k0 = q << g.shift, k1 = k0 + group < g.K ? k0 + group : g.K;
+                    const int z = g.Z[w] ? g.Z[w][n * g.ldz + q] : 8;
+                    for (int64_t k = k0 + lane; k < k1; k += 64) {
+                        const int b = g.W[w][n * g.ldw + k / 2];
+                        const int v = (k & 1 ? b >> 4 : b & 15) - z;
+                        part[i] = fmaf(load_float(g.xtype, g.X, m * g.ldx + k), float(v), part[i]);
+                    }
                 }
-                // The group's whole sum meets its scale: lanes without a part of
-                // it (groups of 32) would make NaN of an infinite one.
-                for (int o = 32; o > 0; o >>= 1) part += __shfl_xor(part, o);
-                sum = fmaf(load_float(g.stype, g.S[w], n * g.lds + q), part, sum);
+                const bool hi = lane & 32, odd = lane & 16;
+                const float a = (hi ? part[2] : part[0]) + __shfl_xor(hi ? part[0] : part[2], 32);
+                const float b = (hi ? part[3] : part[1]) + __shfl_xor(hi ? part[1] : part[3], 32);
+                float d = (odd ? b : a) + __shfl_xor(odd ? a : b, 16);
+                for (int o = 8; o > 0; o >>= 1) d += __shfl_xor(d, o);
+                const int64_t q = q0 + lane / 16;
+                if (q < groups) sum = fmaf(load_float(g.stype, g.S[w], n * g.lds + q), d, sum);
             }
+            sum += __shfl_xor(sum, 32);
+            sum += __shfl_xor(sum, 16);
             out[w] = sum;
         }
         const float y = g.act >= 0 ? act_value(g.act, out[0]) * out[1] : out[0];

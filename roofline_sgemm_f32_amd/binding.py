@@ -369,6 +369,18 @@ def _call(fn, where, X, others, *args):
         raise SgemmError(st, where)
 
 
+def _dim(t, i) -> int:
+    """Size i of a 2-D tensor; 0 of anything else, which the checks then name."""
+    return t.shape[i] if isinstance(t, torch.Tensor) and t.dim() == 2 else 0
+
+
+def _two(pair, name):
+    """The two tensors of a pair that come together."""
+    if not isinstance(pair, (tuple, list)) or len(pair) != 2 or any(t is None for t in pair):
+        raise ValueError(f"{name} must be a pair of tensors")
+    return pair
+
+
 def _halves(rows, cols, like):
     """Two rows x cols float32 tensors, the column halves of one buffer."""
     buf = torch.empty((rows, 2 * cols), dtype=torch.float32, device=like.device)
@@ -386,7 +398,7 @@ def glu(X, Wg, Wu, act="silu", transw=False, out=None, save=False):
     a = _act_id(act)
     ldx = _rows(X, "X")
     M, K = X.shape
-    F = Wg.shape[0 if transw else 1] if isinstance(Wg, torch.Tensor) and Wg.dim() == 2 else 0
+    F = _dim(Wg, 0 if transw else 1)
     ldw = _pair_ld(Wg, Wu, "weights", (F, K) if transw else (K, F))
     if out is None:
         H, ldh = torch.empty((M, F), dtype=torch.float32, device=X.device), max(F, 1)
@@ -395,7 +407,7 @@ def glu(X, Wg, Wu, act="silu", transw=False, out=None, save=False):
     G = U = None
     ldgu = 1
     if isinstance(save, (tuple, list)):
-        G, U = save
+        G, U = _two(save, "save")
     elif save:
         G, U = _halves(M, F, X)
     if G is not None:
@@ -418,7 +430,7 @@ def glu_backward(dH, X, Wg, Wu, G, U, act="silu", transw=False, need_dx=True, ne
     a = _act_id(act)
     ldx = _rows(X, "X")
     M, K = X.shape
-    F = Wg.shape[0 if transw else 1] if isinstance(Wg, torch.Tensor) and Wg.dim() == 2 else 0
+    F = _dim(Wg, 0 if transw else 1)
     wshape = (F, K) if transw else (K, F)
     ldw = _pair_ld(Wg, Wu, "weights", wshape)
     ldgu = _pair_ld(G, U, "G, U", (M, F))
@@ -441,7 +453,7 @@ def glu_backward(dH, X, Wg, Wu, G, U, act="silu", transw=False, need_dx=True, ne
                 dW = buf[:F], buf[F:]
             else:
                 dW = _halves(K, F, X)
-        dWg, dWu = dW
+        dWg, dWu = _two(dW, "dW")
         lddw = _pair_ld(dWg, dWu, "dW", wshape)
     # Empty tensors have no address; the entry point takes null for "skip".
     x_null, w_null = dX is None or dX.numel() == 0, dWg is None or dWg.numel() == 0
@@ -479,7 +491,7 @@ def q4_matmul(X, w, scales, zeros=None, group=128, out=None):
     group = _q4_group(group)
     ldx = _rows(X, "X", None, _FLOATS)
     M, K = X.shape
-    N = w.shape[0]
+    N = _dim(w, 0)
     ldw, lds, ldz = _q4_weight(w, scales, zeros, N, K, group, "q4")
     if out is None:
         Y, ldy = torch.empty((M, N), dtype=X.dtype, device=X.device), max(N, 1)
@@ -501,7 +513,9 @@ def q4_glu(X, gate_w, gate_scales, up_w, up_scales, gate_zeros=None, up_zeros=No
     a, group = _act_id(act), _q4_group(group)
     ldx = _rows(X, "X", None, _FLOATS)
     M, K = X.shape
-    F = gate_w.shape[0]
+    F = _dim(gate_w, 0)
+    if (gate_zeros is None) != (up_zeros is None):
+        raise ValueError("gate_zeros and up_zeros must be given together")
     ld = _q4_weight(gate_w, gate_scales, gate_zeros, F, K, group, "gate")
     if _q4_weight(up_w, up_scales, up_zeros, F, K, group, "up") != ld:
         raise ValueError("gate and up weights must have the same row strides")

@@ -113,3 +113,104 @@ def test_packed_weights_past_the_offset_limit():
     for c in (slice(0, 300), slice(F // 2, F // 2 + 300), slice(F - 300, F)):
         (h, _, _), _ = glu64("relu", *(t.cpu().double() for t in (X, Wg[:, c], Wu[:, c])))
         assert torch.equal(H[:, c].cpu().double(), h)
+
+
+# Outputs of many tiles: 512 of 128 x 256 and 928 of them (the last round 13/16
+# full), both with rows and columns past the edge or none, K of whole and cut
+# slabs, and packed copies; then more than two rounds of 128 x 128 where the
+# larger tile would leave a partial round.
+TILE_SHAPES = [(2048, 64, 4096), (2040, 84, 4092), (3700, 20, 4096), (2040, 83, 4091),
+               (4090, 52, 4220), (4096, 16, 4224), (4090, 51, 4219)]
+
+
+def plan_tile(M, K, F, transw):
+    """The tile of the product the gated form is planned as (aligned or packed)."""
+    F, K = -(-F // 4) * 4, -(-K // 4) * 4
+    return rs.plan_config(M, 2 * F, K, transb=transw)["tile"]
+
+
+@pytest.mark.parametrize("transw", [False, True], ids=["KxF", "FxK"])
+@pytest.mark.parametrize("shape", TILE_SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_gated_large_tiles(shape, transw):
+    M, K, F = shape
+    assert plan_tile(M, K, F, transw) == ((128, 256) if M < 4090 else (128, 128))
+    i = TILE_SHAPES.index(shape)
+    act = ACTS[(i + transw) % len(ACTS)]
+    gen = torch.Generator().manual_seed(i)
+    X, W = torch.randn((M, K), generator=gen), torch.randn((2, K, F), generator=gen) / K ** 0.5
+    D = (W.transpose(1, 2).contiguous() if transw else W).cuda()
+    H, G, Up = Guarded(M, F, gap=(0, 3, 4)[i % 3]), Guarded(M, F), Guarded(M, F)
+    rs.glu(X.cuda(), D[0], D[1], act=act, transw=transw, out=H.view, save=(G.view, Up.view))
+    ref, err = glu64(act, X.double(), W[0].double(), W[1].double())
+    for o, r, e, n in zip((H, G, Up), ref, err, "HGU"):
+        assert_within(o.view, r, e, n)
+        assert o.intact(), n
+    assert torch.equal(rs.glu(X.cuda(), D[0], D[1], act=act, transw=transw), H.view)
+
+
+# (M, N, K, x, group): X and scales staged in one, two or three chunks of K, in
+# eight waves (small X) and sixteen (float X of several rows, or small groups of
+# a gated pair), the last chunk whole, cut, or the unit that rows end in alone.
+CHUNK_SHAPES = [(8, 33, 1700, "f32", 128), (8, 33, 2048, "f32", 128), (8, 40, 2050, "f32", 64),
+                (8, 16, 4500, "f32", 32), (3, 33, 8200, "f32", 64), (5, 20, 6144, "f32", 256),
+                (8, 33, 4097, "bf16", 128), (8, 17, 9000, "f16", 128), (1, 33, 8193, "f32", 128),
+                (1, 20, 40001, "f16", 64), (2, 20, 20000, "bf16", 32), (7, 24, 4223, "f16", 32)]
+
+
+@pytest.mark.parametrize("shape", CHUNK_SHAPES, ids=lambda s: "x".join(map(str, s)))
+def test_4bit_long_rows_in_chunks(shape):
+    M, N, K, x, group = shape
+    i = CHUNK_SHAPES.index(shape)
+    gen = torch.Generator().manual_seed(i)
+    X = torch.randn((M, K), generator=gen).to(TYPES[x])
+    stype, zeros = list(TYPES.values())[i % 3], i % 2 == 0
+    gate, up = (q4_make(gen, N, K, group, stype, zeros) for _ in range(2))
+    g, eg = q4_64(X, *gate, group)
+    u, eu = q4_64(X, *up, group)
+    Y = Guarded(M, N, TYPES[x], gap=1)
+    rs.q4_matmul(X.cuda(), *gate, group=group, out=Y.view)
+    assert_within(Y.view, g, rounded(g, eg, TYPES[x]))
+    assert Y.intact()
+    for _ in range(3):
+        assert torch.equal(rs.q4_matmul(X.cuda(), *gate, group=group), Y.view)
+    H = Guarded(M, N, TYPES[x], gap=1)
+    rs.q4_glu(X.cuda(), gate[0], gate[1], up[0], up[1], gate[2], up[2], group=group, out=H.view)
+    a, _ = act64("silu", g)
+    eh = (LIPSCHITZ * eg + act_err(g)) * (u.abs() + eu) + a.abs() * eu + 2 * U * (a * u).abs()
+    assert_within(H.view, a * u, rounded(a * u, eh, TYPES[x]), "gated")
+    assert H.intact()
+
+
+def test_workspace_calls_of_two_streams_at_once():
+    """Gated calls that pack, split K, or both, and one whose copies pass the
+    cached workspace, from two streams together: the smaller calls of one run
+    while the other's grow the buffer."""
+    def make(M, K, F, seed):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        X = torch.randn((M, K), generator=gen, device="cuda")
+        W = torch.randn((2, F, K), generator=gen, device="cuda") / K ** 0.5
+        return X, W[0], W[1]
+    # Split 32 x 32 tiles; split 64 x 64 tiles; packed (18 MB) and split; packed,
+    # 39 MB, 145 MB, and 305 MB (more than the cached buffer holds).
+    shapes = [(24, 2052, 130), (64, 4096, 4096), (300, 4097, 401), (700, 2047, 2053),
+              (600, 4099, 4101), (2100, 4099, 8200)]
+    plans = [rs.plan_config(M, 2 * F, K, transb=True) for M, K, F in shapes]
+    assert [(p["packed"], p["splits"] > 1) for p in plans] == [
+        (False, True), (False, True), (True, True), (True, False), (True, False), (True, False)]
+    sets = [make(*s, i) for i, s in enumerate(shapes)]
+    want = [rs.glu(*t, act="gelu", transw=True) for t in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for _ in range(3):
+        for i in range(len(sets)):
+            # The streams go through the shapes in opposite orders.
+            for st, j in zip(streams, (i, len(sets) - 1 - i)):
+                with torch.cuda.stream(st):
+                    outs.append((j, rs.glu(*sets[j], act="gelu", transw=True)))
+    torch.cuda.synchronize()
+    for j, o in outs:
+        assert torch.equal(o, want[j]), shapes[j]
+    for j in (0, 2):
+        ref, err = glu64("gelu", *(t.cpu().double() for t in (sets[j][0], sets[j][1].t(), sets[j][2].t())))
+        assert_within(want[j], ref[0], err[0], shapes[j])

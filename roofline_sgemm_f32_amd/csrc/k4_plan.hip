@@ -524,14 +524,22 @@ static SplitPlan glu_plan(const GluArgs& g, const GemmArgs& p, bool may_split) {
 
 // Whether a gated call packs its unaligned operands: as its product would, but
 // wide unaligned weights are not copied for few rows, each of which pays for
-// the copy with M products per weight only.  F x K: up to 32 rows (32 x 22016 x
-// 4097: packed 495 us, not 255; 20 x 16384 x 2047: 197, 89), or one or two full
-// 64-row tiles, whose loads need no row checks (64 x 16384 x 2047: 220, 131; 128
-// rows: 247, 186; but 48 rows: 196, 245; 100 rows: 243, 255).  K x F: below 300
-// rows (64 x 16385 x 1023: 100, 66; 200 rows: 199, 188; 300 rows: 232, 215).
+// the copy with M products per weight only (us, packed and as stored).
+//  * F x K, up to 32 rows (32 x 22016 x 4097: 495, 255; 20 x 16384 x 2047: 197,
+//    89).
+//  * F x K, where every 64 x 32 tile is full: its 4-byte loads need no checks,
+//    which double their time (64 x 22016 x 4097: 559, 293, but 63 rows 580, 552
+//    and 65 rows 749, 665).  Up to 512 rows (192 x 16384 x 2047: 330, 249; 384 x
+//    11008 x 4097: 696, 639; 512 x 8192 x 2047: 296, 299; 640 rows 357, 381).
+//    From 512 columns of tiles on one partial column more leaves few rows ahead
+//    (64 x 22000 x 4097: 555, 489; 256 x 16390 x 2047: 386, 379; but 128 x 9000 x
+//    4097: 323, 408).
+//  * K x F, below 300 rows (64 x 16385 x 1023: 100, 66; 200 rows: 199, 188; 300
+//    rows: 232, 215).
 static bool glu_worth_packing(const GluArgs& g, const GemmArgs& p, size_t x_bytes, size_t w_bytes) {
     const bool wide = ceil_div(p.M, 64) * ceil_div(p.N, 64) >= 512;
-    const bool few = g.transw ? g.M <= 32 || g.M == 64 || g.M == 128 : g.M < 300;
+    const bool full = g.M % 64 == 0 && (g.F % 32 == 0 ? g.M <= 512 : g.F >= 512 * 32 && g.M <= 256);
+    const bool few = g.transw ? g.M <= 32 || full : g.M < 300;
     if (w_bytes > 0 && wide && few) return false;
     return worth_packing(p, double(x_bytes + 2 * w_bytes));
 }

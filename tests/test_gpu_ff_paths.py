@@ -214,3 +214,21 @@ def test_workspace_calls_of_two_streams_at_once():
     for j in (0, 2):
         ref, err = glu64("gelu", *(t.cpu().double() for t in (sets[j][0], sets[j][1].t(), sets[j][2].t())))
         assert_within(want[j], ref[0], err[0], shapes[j])
+
+
+@pytest.mark.parametrize("shape", [(64, 69, 16384), (64, 69, 16390), (192, 35, 6144), (512, 67, 2080),
+                                   (448, 130, 2400), (128, 33, 8201), (576, 37, 2048), (256, 21, 16391)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_gated_unaligned_full_tiles(shape):
+    """Unaligned F x K weights under rows that fill 64-row tiles: as stored
+    where the columns fill theirs, or are many, and otherwise as copies."""
+    M, K, F = shape
+    gen = torch.Generator().manual_seed(F)
+    X, W = torch.randn((M, K), generator=gen), torch.randn((2, F, K), generator=gen) / K ** 0.5
+    D = W.cuda()
+    H, G, Up = Guarded(M, F, gap=1), Guarded(M, F), Guarded(M, F)
+    rs.glu(X.cuda(), D[0], D[1], transw=True, out=H.view, save=(G.view, Up.view))
+    ref, err = glu64("silu", X.double(), W[0].double().t(), W[1].double().t())
+    for o, r, e, n in zip((H, G, Up), ref, err, "HGU"):
+        assert_within(o.view, r, e, n)
+        assert o.intact(), n

@@ -15,7 +15,6 @@ namespace sgemm {
 
 // sgemm_act_t
 enum Act { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2, ACT_RELU = 3, ACT_SIGMOID = 4 };
-constexpr int kActCount = 5;
 
 // 1 / (1 + exp(-v)) and its complement 1 / (1 + exp(v)).
 struct Logistic {

@@ -546,9 +546,8 @@ static bool glu_worth_packing(const GluArgs& g, const GemmArgs& p, size_t x_byte
 
 hipError_t launch_glu(const GluArgs& g, hipStream_t s) {
     if (glu_thin_ok(g)) return launch_glu_thin(g, s);
-    GemmArgs p = glu_product(g), one = p;
-    one.N = g.F;
-    if (!k4_supports(p) || !k4_supports(one)) return launch_glu_general(g, s);
+    GemmArgs p = glu_product(g);
+    if (!k4_supports(p)) return launch_glu_general(g, s);
     const bool x_vec = rows_vec(g.X, g.ldx, g.K);
     const int64_t w_rows = g.transw ? g.F : g.K, w_run = g.transw ? g.K : g.F;
     const bool w_vec = rows_vec(g.Wg, g.ldw, w_run) && rows_vec(g.Wu, g.ldw, w_run);

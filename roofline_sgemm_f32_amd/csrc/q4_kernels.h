@@ -17,6 +17,7 @@
 
 #include "activation.h"
 #include "kernels.h"
+#include "q4_elements.h"
 
 namespace sgemm {
 
@@ -29,31 +30,19 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kUnit = 128;      // K per step of a wave: 4 lane groups of 32 weights
-constexpr int64_t kRowsLds = 80 * 1024;  // LDS of a q4_rows workgroup: half a CU's
-constexpr int kRowsMax = 8;     // rows of X of one q4_rows workgroup
+// LDS of a q4_rows workgroup: half a CU's, unless one round of the waves takes
+// more (float X of 8 rows, groups of 32, gated: 112 KiB).
+constexpr int64_t kRowsLds = 80 * 1024;
+// Rows of X that q4_rows takes.  Up to 16 fit the instruction; sixteen of float X
+// do not fit the LDS (a round of the waves is 194 KiB), and of bfloat16 X they
+// take more LDS than two workgroups a CU have, which costs where there are two
+// (K = 4096, us, here and on tiles: 12 x 8192 25, 14; 16 x 8192 30, 14; gated 36,
+// 23) and gains where there are fewer (9 x 4096 9.4, 13.6; 16 x 4096 14.9, 13.6;
+// gated 15, 22 and 20, 22; 16 x 1024 x 2048 9.6, 10.4; gated 11, 16).
+constexpr int kRowsMax = 8;
 
 // bfloat16 parts of X for the matrix cores: 3 for float, 1 for 16-bit types.
 template <int XT> constexpr int parts() { return XT == T_F32 ? 3 : 1; }
-
-// An element as its bits, and these as a float.
-__device__ __forceinline__ uint32_t load_raw(int type, const void* p, int64_t i) {
-    if (type == T_F32) return static_cast<const uint32_t*>(p)[i];
-    return static_cast<const uint16_t*>(p)[i];
-}
-__device__ __forceinline__ float raw_to_float(int type, uint32_t v) {
-    const float half = float(__builtin_bit_cast(_Float16, uint16_t(v)));
-    return type == T_F32 ? __uint_as_float(v) : type == T_BF16 ? __uint_as_float(v << 16) : half;
-}
-__device__ __forceinline__ float load_float(int type, const void* p, int64_t i) {
-    return raw_to_float(type, load_raw(type, p, i));
-}
-
-template <int XT>
-__device__ __forceinline__ void store_as(void* p, int64_t i, float v) {
-    if constexpr (XT == T_F32) static_cast<float*>(p)[i] = v;
-    else if constexpr (XT == T_F16) static_cast<_Float16*>(p)[i] = _Float16(v);
-    else static_cast<__bf16*>(p)[i] = __bf16(v);
-}
 
 // 16 bytes from any address.
 __device__ __forceinline__ u32x4 load16(const void* p) {
@@ -266,17 +255,16 @@ __device__ __forceinline__ void transpose_groups(u32x4& v) {
 }
 }  // namespace
 
-// Up to 8 rows of X.  A workgroup owns 16 columns n of Y for rows m0 ..
-// m0 + 7; its waves deal the K units out among themselves and add their sums
-// through LDS in wave order.  The weights are the B operand of the 16 x 16 x 32
-// instruction (lane: column n = lane % 16, eight k of step j from lane group
-// lane / 16) and go from memory to registers in 16-byte loads, one pass, PF
-// units ahead.  X is the A operand, rows past M repeating the last one.  X,
-// the scales (as floats) and the zero points (as dequant's constants) are
-// staged in LDS chunk by chunk: a wave's X loads would otherwise take four
-// times the load instructions of its weights, float X would be split by every
-// wave, and loads as small as a scale's would hold up the weights' behind
-// them, since loads complete in order.
+// Up to 8 rows of X.  A workgroup owns 16 columns n of Y; its waves deal the K
+// units out among themselves and add their sums through LDS in wave order.  The
+// weights are the B operand of the 16 x 16 x 32 instruction (lane: column n =
+// lane % 16, eight k of step j from lane group lane / 16) and go from memory to
+// registers in 16-byte loads, one pass, PF units ahead.  X is the A operand,
+// rows past M repeating the last one.  X, the scales (as floats) and the zero
+// points (as dequant's constants) are staged in LDS chunk by chunk: a wave's X
+// loads would otherwise take four times the load instructions of its weights,
+// float X would be split by every wave, and loads as small as a scale's would
+// hold up the weights' behind them, since loads complete in order.
 // GS: steps of 32 that share a scale (4 for groups of 128 or more).
 struct ScaleZero {
     float s;
@@ -285,7 +273,7 @@ struct ScaleZero {
 
 template <int XT, int GS, int NWT, int PF, int NW>
 __global__ void __launch_bounds__(64 * NW, 4)
-q4_rows(Q4Args g, int chunk, int tiles_m, int tiles) {
+q4_rows(Q4Args g, int chunk, int tiles) {
     // 32-bit offsets within a tile: the host sends larger strides elsewhere.
     constexpr int P = parts<XT>(), NS = 4 / GS, XS = XT == T_F32 ? 4 : 2;
     extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -296,9 +284,8 @@ q4_rows(Q4Args g, int chunk, int tiles_m, int tiles) {
     // All units, and those wholly inside a row.
     const int units = (K + kUnit - 1) / kUnit, full = bytes / (kUnit / 2);
     for (int tile = blockIdx.x; tile < tiles; tile += int(gridDim.x)) {
-        const int tn = tiles_m == 1 ? tile : tile / tiles_m;
-        const int64_t n0 = int64_t(tn) * 16, m0 = int64_t(tile - tn * tiles_m) * kRowsMax;
-        const int rows = int(g.M - m0 < kRowsMax ? g.M - m0 : kRowsMax);
+        const int64_t n0 = int64_t(tile) * 16;
+        const int rows = int(g.M);
         const int cols = int(g.N - n0 < 16 ? g.N - n0 : 16);
         const int mr = r < rows ? r : rows - 1;
         const uint32_t woff = uint32_t(r < cols ? r : cols - 1) * uint32_t(g.ldw) + uint32_t(lg) * 16u;
@@ -388,8 +375,10 @@ q4_rows(Q4Args g, int chunk, int tiles_m, int tiles) {
                 const int xm0 = xm, xk0 = xk, st0 = st, sq0 = sq;
 #pragma unroll
                 for (int b = 0; b < BX; b++) {
-                    if (xm < rows && xk + tid < nk) load_x_checked<XT>(static_cast<const char*>(g.X) + ((m0 + xm) * g.ldx + (c0 * 16 + xk + tid) * 8) * XS,
-                                           K - (c0 * 16 + xk + tid) * 8, x[b]);
+                    // 32 bits: 64-bit products took 8 x 4096 x 4096 of floats 14.9 us, not 13.1.
+                    const uint32_t off = (uint32_t(xm) * uint32_t(g.ldx) + uint32_t(c0 * 16 + xk + tid) * 8u) * XS;
+                    if (xm < rows && xk + tid < nk)
+                        load_x_checked<XT>(static_cast<const char*>(g.X) + off, K - (c0 * 16 + xk + tid) * 8, x[b]);
                     xk += nt;
                     if (xk >= nk) xk = 0, xm++;
                 }
@@ -476,7 +465,7 @@ q4_rows(Q4Args g, int chunk, int tiles_m, int tiles) {
                 sum[t] = red[t * 256 + o];
                 for (int w = 1; w < nw; w++) sum[t] += red[(w * NWT + t) * 256 + o];
             }
-            const int64_t m = m0 + o / 16, nn = n0 + o % 16;
+            const int64_t m = o / 16, nn = n0 + o % 16;
             if (nn < g.N)
                 store_as<XT>(g.Y, m * g.ldy + nn, NWT == 2 ? act_value(g.act, sum[0]) * sum[NWT - 1] : sum[0]);
         }
@@ -488,22 +477,21 @@ q4_rows(Q4Args g, int chunk, int tiles_m, int tiles) {
 // PF units each.
 template <int XT, int GS, int NWT, int PF, int NW>
 static hipError_t launch_rows_cfg(const Q4Args& g, int64_t unit_bytes, hipStream_t s) {
-    const int64_t units = ceil_div(g.K, kUnit), rows = g.M < kRowsMax ? g.M : kRowsMax;
-    const int64_t fixed = 64 * rows, round = NW * PF;
+    const int64_t units = ceil_div(g.K, kUnit), fixed = 64 * g.M, round = NW * PF;
     int64_t chunk = (kRowsLds - fixed) / unit_bytes / round * round;
     if (chunk < round) chunk = round;
     if (chunk > units) chunk = units;
     size_t lds = size_t(NW) * NWT * 1024;
     if (size_t(chunk * unit_bytes + fixed) > lds) lds = size_t(chunk * unit_bytes + fixed);
-    const int64_t tm = ceil_div(g.M, kRowsMax), tiles = ceil_div(g.N, 16) * tm;
+    const int64_t tiles = ceil_div(g.N, 16);
     hipLaunchKernelGGL((q4_rows<XT, GS, NWT, PF, NW>), dim3(grid_for(tiles)), dim3(64 * NW), lds, s, g,
-                       int(chunk), int(tm), int(tiles));
+                       int(chunk), int(tiles));
     return hipGetLastError();
 }
 
 template <int XT, int GS, int NWT>
 static hipError_t launch_rows(const Q4Args& g, hipStream_t s) {
-    const int64_t units = ceil_div(g.K, kUnit), rows = g.M < kRowsMax ? g.M : kRowsMax;
+    const int64_t units = ceil_div(g.K, kUnit), rows = g.M;
     const int64_t unit_bytes = 4 * parts<XT>() * 4 * rows * 16 + NWT * (4 / GS) * 16 * int64_t(sizeof(ScaleZero));
     // Four units ahead in eight waves where that much of X leaves room for two
     // workgroups in a CU's LDS; more of it (float X of several rows) takes one

@@ -305,9 +305,9 @@ int sgemm_glu_f32(int act, int transw, int64_t M, int64_t F, int64_t K,
  * SGEMM_ERR_ARG).  beta == 0: dWg and dWu are not read; beta == 1 accumulates
  * over micro-batches.  M == 0 leaves dW = beta dW; F == 0 gives dX = 0.
  * act'(0) = 0 for relu.  Where dG, dU adjoin as [dG | dU] in one buffer
- * (dU == dG + F, lddgu >= 2 F) and so do the weights, or the weight
- * gradients, a pair of products runs as one.  Nothing is atomic: the result
- * of a call is the same from run to run.  Wg and Wu (X) are only read, and
+ * (dU == dG + F, lddgu >= 2 F) and so do the weight gradients, or for F up
+ * to 4096 the weights, a pair of products runs as one.  Nothing is atomic: the
+ * result of a call is the same from run to run.  Wg and Wu (X) are only read, and
  * may be NULL, when dX (dWg) is skipped. */
 int sgemm_glu_backward_f32(int act, int transw, int64_t M, int64_t F, int64_t K,
                            const float *X, int64_t ldx, const float *Wg, const float *Wu,
@@ -328,10 +328,13 @@ int sgemm_glu_backward_f32(int act, int transw, int64_t M, int64_t F, int64_t K,
  * every z is 8) N x G bytes, each 0..15, G = ceil(K / group) (lds, ldz >=
  * max(1, G); ldz is ignored without Z).  X (M x K) and Y (M x N) are of type
  * xtype.  Every pointer has the alignment of its element type.
- *   The product is exact to float: q - z and the sums' terms are not rounded
- * to the type of X, each group's sum is held in float and scaled once, and the
- * result is rounded to xtype at the end.  A group's sum is formed before its
- * scale is applied, so X has to leave it in float range.
+ *   Terms are not rounded: q - z and X count in full (float X in steps of
+ * 2^-133, so all of its bits from 2^-110 on), and sums are in float.  A group's
+ * products are added, in parts of 128 where it is longer, and each such sum is
+ * scaled once; the result is rounded to xtype at the end.  As a sum is formed
+ * before its scale is applied, X has to leave it in float range, and an
+ * infinite scale gives infinities of the sum's sign (NaN where the parts of a
+ * longer group differ in sign).
  *   Y must not overlap an input (SGEMM_ERR_ALIAS).  K == 0: Y is zero.  No
  * workspace, no synchronisation; every call can be captured. */
 typedef enum sgemm_type { SGEMM_TYPE_F32 = 0, SGEMM_TYPE_F16 = 1, SGEMM_TYPE_BF16 = 2 } sgemm_type_t;

@@ -7,11 +7,12 @@
 // bfloat16 and float16, so the products run on the matrix cores of the 16-bit
 // types without rounding a weight: float16 X on float16, bfloat16 X on
 // bfloat16, and float X as the sum of three bfloat16 parts of 8 bits each
-// (24 bits: the float exactly, down to 2^-110), one matrix instruction per
-// part.  That is 16 / 3 times the rate of the float matrix instructions, with
-// products that are exact.  Each group's sum is formed from zero in float
-// and joins the output's float sum through one multiply-add by its scale, so
-// a scale is never rounded either.
+// (24 bits: the float exactly, down to 2^-110; smaller ones in steps of
+// 2^-133), one matrix instruction per part.  That is 16 / 3 times the rate of
+// the float matrix instructions, with products that are exact.  The sum of a
+// group, or of 128 k of a longer one, is formed from zero in float and joins the
+// output's float sum through one multiply-add by its scale, so a scale is never
+// rounded either.
 #pragma once
 #include <type_traits>
 
@@ -861,10 +862,14 @@ static hipError_t launch_tile(const Q4Args& g, hipStream_t s) {
 // small tile shares out K instead), so the choice is the configuration with the
 // least rounds x time of a round.  Times measured on MI355X at K = 4096 (us; the
 // ratios at K = 2048 are alike): bfloat16 and float16 / float, of one product and
-// of the gated pair.  Over 9 to 1024 rows by 1024 to 8192 columns the choice is
-// the fastest of these, or within 15 % of it; always the 128 x 256 tile would
-// take 70 us for 9 rows where 14 do, always the 32 x 32 one 383 for 1024 rows
-// where 78 do.
+// of the gated pair, on rounds that leave some CUs idle (a full one of the 128 x
+// 256 tile takes 78 / 191, as the CUs then share the L2s and memory), and in
+// groups of 128 / 64.  Over 9 to 1024 rows by 1024 to 8192 columns the choice is
+// the fastest of these five, or within 15 % of it; always the 128 x 256 tile
+// would take 70 us for 9 rows where 14 do, always the 32 x 32 one 383 for 1024
+// rows where 78 do.  A sixth tile of the plain product, 64 x 256, would be faster
+// where it fills one round (512 x 8192 x 4096 52 us where the choice takes 60,
+// float 108 and 127; 1024 x 4096 x 4096 53 and 62).
 template <int XT, int GS, int NWT>
 static hipError_t launch_tiles(const Q4Args& g, hipStream_t s) {
     constexpr bool f = XT == T_F32, two = NWT == 2;

@@ -232,3 +232,23 @@ def test_gated_unaligned_full_tiles(shape):
     for o, r, e, n in zip((H, G, Up), ref, err, "HGU"):
         assert_within(o.view, r, e, n)
         assert o.intact(), n
+
+
+@pytest.mark.parametrize("M", [1, 20, 140])
+def test_4bit_smallest_floats(M):
+    """float X below 2^-110 counts in steps of 2^-133, cut towards zero, each
+    times q - z and the scale; bfloat16 X in full."""
+    gen = torch.Generator().manual_seed(M)
+    N, K, group = 64, 256, 64
+    w, s, z = q4_make(gen, N, K, group, torch.float32, True)
+    s.fill_(2.0 ** 100)
+    W = q4_int(w, z, K, group).abs().t() * 2.0 ** 100
+    for e in (-111, -118, -126, -140):
+        X = (torch.randint(1 << 23, 1 << 24, (M, K), generator=gen).double() * 2.0 ** (e - 23)).float()
+        Y = rs.q4_matmul(X.cuda(), w, s, z, group=group)
+        ref, err = q4_64(X, w, s, z, group)
+        assert_within(Y, ref, err + torch.full((M, K), 2.0 ** -133, dtype=torch.float64) @ W, e)
+    X = (torch.randint(-40, 41, (M, K), generator=gen).double() * 2.0 ** -133).to(torch.bfloat16)
+    Y = rs.q4_matmul(X.cuda(), w, s, z, group=group)
+    ref, _ = q4_64(X, w, s, z, group)
+    assert torch.equal(Y.cpu(), ref.to(torch.bfloat16))

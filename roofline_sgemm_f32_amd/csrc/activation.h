@@ -16,20 +16,37 @@ namespace sgemm {
 // sgemm_act_t
 enum Act { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2, ACT_RELU = 3, ACT_SIGMOID = 4 };
 
+// exp(x) for x <= 0: x / ln 2 in its nearest integer and a rest of at most a
+// half, from ln 2's inverse in two floats (Cody and Waite's reduction).  Off by
+// two units in the last place at most, the instruction's one and the rest's
+// rounding; expf's cases for large x are not needed here.
+__device__ __forceinline__ float exp_neg(float x) {
+    const float c = x < -110.0f ? -110.0f : x;  // 0 from -104 on; NaN stays NaN
+    const float n = rintf(c * 1.44269504f);
+    const float f = fmaf(c, 1.92596303e-8f, fmaf(c, 1.44269504f, -n));
+    return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f(f), int(n));
+}
+// 1 / d for d in 1 .. 2: one Newton step on the instruction's estimate, off by a
+// little over half a unit.  A quotient n (1 / d) rounds once more.
+__device__ __forceinline__ float rcp_1to2(float d) {
+    const float r = __builtin_amdgcn_rcpf(d);
+    return fmaf(fmaf(-d, r, 1.0f), r, r);
+}
+
 // 1 / (1 + exp(-v)) and its complement 1 / (1 + exp(v)).
 struct Logistic {
     float s, r;
 };
 __device__ __forceinline__ Logistic logistic2(float v) {
-    const float e = expf(-fabsf(v)), q = 1.0f / (1.0f + e);
+    const float e = exp_neg(-fabsf(v)), q = rcp_1to2(1.0f + e);
     return v < 0.0f ? Logistic{e * q, q} : Logistic{q, e * q};
 }
-// n / (1 + exp(-v)): the numerator selected, one division (4096 x 8192 x 4096
-// with G and U kept 3905 us; from logistic2's s 3926; with exp(-v) whatever its
-// sign, which overflows below -88.7, 3896).
+// n / (1 + exp(-v)), the numerator selected (4096 x 8192 x 4096 with G and U kept
+// 3850 us; with expf and the compiler's division 3905; of these with exp(-v)
+// whatever its sign, which overflows below -88.7, 3896).
 __device__ __forceinline__ float logistic_of(float n, float v) {
-    const float e = expf(-fabsf(v));
-    return (v < 0.0f ? n * e : n) / (1.0f + e);
+    const float e = exp_neg(-fabsf(v));
+    return (v < 0.0f ? n * e : n) * rcp_1to2(1.0f + e);
 }
 
 // 2 c (g + 0.044715 g^3), c = sqrt(2 / pi): twice the argument of tanh.

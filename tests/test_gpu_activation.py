@@ -106,3 +106,27 @@ def test_tails_of_the_forward_pass(act):
     one = torch.ones((1, 1), device="cuda")
     H = rs.glu(one, g[None].cuda(), torch.ones((1, g.numel()), device="cuda"), act=act)
     assert_tails(act, "forward", g, H[0].cpu(), val, err)
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_non_finite_and_extreme_values(act):
+    """NaN stays NaN, infinities go to their limits (where the formula has one
+    in floats: not 0 times infinity), and finite values up to the largest stay
+    finite."""
+    nan, inf, big = float("nan"), float("inf"), 3.4028234e38
+    g = torch.tensor([nan, inf, big, -big, 1e-45, -1e-45, 0.0, -0.0])
+    one = torch.ones((1, 1), device="cuda")
+    forward = rs.glu(one, g[None].cuda(), torch.ones((1, g.numel()), device="cuda"), act=act)[0].cpu()
+    da, back = derivative(act, g)
+    for a in (forward, back):
+        assert torch.isnan(a[0])
+        assert a[1] == (1.0 if act == "sigmoid" else inf)
+        assert a[2] == (1.0 if act == "sigmoid" else big) and a[3] == 0.0
+        at0 = 0.5 if act == "sigmoid" else 0.0
+        assert ((a[4:] - at0).abs() <= 2.0 ** -149).all()
+    assert torch.isfinite(da[2:]).all()
+    assert da[3] == 0.0 and da[2] == (0.0 if act == "sigmoid" else 1.0)
+    if act == "relu":  # compares with 0, which NaN does not exceed
+        assert da[0] == 0.0 and da[4:].tolist() == [1.0, 0.0, 0.0, 0.0]
+    else:
+        assert torch.isnan(da[0]) and (da[4:] == (0.25 if act == "sigmoid" else 0.5)).all()

@@ -58,7 +58,8 @@
  *   pack, K == 0, alpha == 0) allocates nothing and never synchronises.
  *   sgemm_glu_f32 (to pack unaligned operands and to split K) and the
  *   products of sgemm_glu_backward_f32 use the workspace in the same way;
- *   sgemm_q4 and sgemm_q4_glu never do.
+ *   sgemm_q4 and sgemm_q4_glu never do; sgemm_lora, sgemm_lora_backward and
+ *   sgemm_orthogonalize are given their scratch memory by the caller.
  *
  * Errors
  *   Arguments are validated on the host before any HIP call; a bad argument
@@ -127,7 +128,8 @@ typedef enum sgemm_status {
     SGEMM_ERR_UNSUPPORTED = 7, /* the explicit variant cannot index this shape (AUTO always can) */
     SGEMM_ERR_ARG = 8,         /* another invalid argument (copy probe: n < 0, bad block or grid) */
     SGEMM_ERR_SCRATCH = 9      /* sgemm_f32_ex_split_noalloc: the requested K split's partial
-                                  products need more than SGEMM_STATIC_SCRATCH_BYTES */
+                                  products need more than SGEMM_STATIC_SCRATCH_BYTES;
+                                  where the caller gives a workspace: it is too small */
 } sgemm_status_t;
 
 /* C = A * B with the variant chosen per shape.  Same as
@@ -351,6 +353,91 @@ int sgemm_q4_glu(int act, int xtype, int stype, int64_t M, int64_t F, int64_t K,
                  int64_t ldx, const uint8_t *Wg, const uint8_t *Wu, int64_t ldw, int64_t group,
                  const void *Sg, const void *Su, int64_t lds, const uint8_t *Zg, const uint8_t *Zu,
                  int64_t ldz, void *H, int64_t ldh, void *stream);
+
+/* ---- Low-rank adapters ----------------------------------------------------
+ *
+ *     Y[m] = base[m] + alpha s[l] (X[m] A_l^T) B_l^T,   l = ids[m]
+ *
+ * Each row of X has the adapter that its id names, or none: an id outside
+ * 0..L-1 (-1, say) gives Y[m] = base[m].  X is M x K, base and Y are M x N,
+ * A_l is R x K (row stride lda, A_l at A + l stride_a elements), B_l is N x R
+ * (ldb, stride_b), all of type `type`; strides between adapters are >= 0 and
+ * may be 0.  R is 1..SGEMM_LORA_MAX_RANK, L is 1..SGEMM_LORA_MAX_ADAPTERS, M, N
+ * and K are below 2^31.  ids: M int32 (id_bits 32) or int64 (id_bits 64); NULL:
+ * every row has adapter 0.  s: L floats (NULL: all 1).  base NULL: zero; base may
+ * be Y itself (ldbase == ldy).  H (may be NULL) receives X[m] A_l^T, M x R floats
+ * of row stride ldh, zero in rows without adapter.
+ *   X A^T is formed and kept in float, and so is the sum with base, which is
+ * rounded to `type` once.  Nothing is atomic: the result of a call is the same
+ * from run to run.  An adapter's zero rank columns change no result, so smaller
+ * ranks are padded with zeros.
+ *   Both entry points take scratch memory from the caller: `workspace`, of at
+ * least the bytes that sgemm_lora_workspace names for these sizes (0: NULL is
+ * fine), 16-byte aligned, which the call's kernels use until they end.  They
+ * allocate nothing and never synchronise; every call can be captured. */
+#define SGEMM_LORA_MAX_RANK 256
+#define SGEMM_LORA_MAX_ADAPTERS 32768
+
+/* Bytes of workspace of sgemm_lora (backward 0) or sgemm_lora_backward
+ * (backward 1) for these sizes, or minus a status code. */
+int64_t sgemm_lora_workspace(int backward, int type, int64_t M, int64_t N, int64_t K, int64_t R,
+                             int64_t L);
+
+int sgemm_lora(int type, int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, const void *X,
+               int64_t ldx, const void *A, int64_t lda, int64_t stride_a, const void *B, int64_t ldb,
+               int64_t stride_b, const void *ids, int id_bits, const float *s, float alpha,
+               const void *base, int64_t ldbase, void *Y, int64_t ldy, float *H, int64_t ldh,
+               void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Gradients of sgemm_lora from dY (M x N) and the H of the forward pass:
+ *
+ *     dH[m] = alpha s[l] dY[m] B_l      (float)
+ *     dX[m] = base[m] + dH[m] A_l       (M x K; base NULL: zero; base may be dX)
+ *     dA_l  = sum_{m: ids[m] = l} dH[m]^T X[m]
+ *     dB_l  = alpha s[l] sum_{m: ids[m] = l} dY[m]^T H[m]
+ *
+ * dX == NULL skips dX; dA == NULL and dB == NULL skip theirs.  dA and dB are
+ * written for every adapter (zero where no row has it), laid out like A and B
+ * with strides of their own, which must keep the adapters apart.  Sums are in
+ * float, in an order that depends on the sizes and ids alone. */
+int sgemm_lora_backward(int type, int64_t M, int64_t N, int64_t K, int64_t R, int64_t L,
+                        const void *dY, int64_t lddy, const void *X, int64_t ldx, const void *A,
+                        int64_t lda, int64_t stride_a, const void *B, int64_t ldb, int64_t stride_b,
+                        const float *H, int64_t ldh, const void *ids, int id_bits, const float *s,
+                        float alpha, const void *base, int64_t ldbase, void *dX, int64_t lddx,
+                        void *dA, int64_t ldda, int64_t stride_da, void *dB, int64_t lddb,
+                        int64_t stride_db, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* ---- Orthogonalised updates -----------------------------------------------
+ *
+ * For each of `batch` matrices G (M x N, row stride ldg, stride_g elements apart):
+ *
+ *     X = G / (|G| + eps)                 |G| the Frobenius norm
+ *     X = a X + (b S + c S^2) X, S = X X^T, for each of `steps` triples (a, b, c)
+ *
+ * and O = X (S = X^T X and the factor on the right where M > N, which is the
+ * same).  With singular values s of G / |G| those of O are p(..p(s)), p(s) = a s
+ * + b s^3 + c s^5: coefficients that drive them all to about one leave an update
+ * whose directions all count alike.  coefficients: 3 * steps doubles in host
+ * memory, read before the call returns; steps 1..SGEMM_ORTHO_MAX_STEPS.  G and O
+ * are of type `type`; O may be G itself (same strides), else they must not
+ * overlap; O's strides must keep the matrices apart.
+ *   The norm is summed in double.  Between the steps X and S are kept as two
+ * float16 parts each, 22 bits, times a power of two, and products are summed in
+ * float.  The power comes from a bound of X that follows from the coefficients
+ * alone (|X| <= 1 at the start); coefficients that are not finite or let it pass
+ * 64 are SGEMM_ERR_ARG.  A matrix of zeros gives zeros; an infinity or NaN in G
+ * makes its matrix's results NaN.
+ *   `workspace`: at least sgemm_orthogonalize_workspace bytes, 256-byte aligned.
+ * No allocation, no synchronisation, every call can be captured. */
+#define SGEMM_ORTHO_MAX_STEPS 64
+
+int64_t sgemm_orthogonalize_workspace(int64_t batch, int64_t M, int64_t N);
+
+int sgemm_orthogonalize(int type, int64_t batch, int64_t M, int64_t N, const void *G, int64_t ldg,
+                        int64_t stride_g, void *O, int64_t ldo, int64_t stride_o, int steps,
+                        const double *coefficients, double eps, void *workspace,
+                        int64_t workspace_bytes, void *stream);
 
 /* Device-to-device copy dst[i] = src[i], 0 <= i < n, with a grid-stride loop:
  * the HBM bandwidth probe of amittech.dev, "7.3 Bandwidths and peak rate -

@@ -7,6 +7,7 @@ has not been built, the first call raises; there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -41,7 +42,9 @@ EXPORTS = ["sgemm_f32", "sgemm_f32_variant", "sgemm_copy_f32", "sgemm_copy_f32_l
            "sgemm_last_hip_error", "sgemm_abi_version", "sgemm_probe_valu_f32",
            "sgemm_probe_mfma_f32", "sgemm_f32_ex", "sgemm_f32_colmajor", "sgemm_f32_ex_split",
            "sgemm_split_plan", "sgemm_plan_config", "sgemm_f32_ex_split_noalloc",
-           "sgemm_glu_f32", "sgemm_glu_backward_f32", "sgemm_q4", "sgemm_q4_glu"]
+           "sgemm_glu_f32", "sgemm_glu_backward_f32", "sgemm_q4", "sgemm_q4_glu",
+           "sgemm_lora_workspace", "sgemm_lora", "sgemm_lora_backward",
+           "sgemm_orthogonalize_workspace", "sgemm_orthogonalize"]
 
 MAX_SPLITS = 64
 STATIC_SCRATCH_BYTES = 64 * 1024 * 1024  # SGEMM_STATIC_SCRATCH_BYTES
@@ -115,6 +118,20 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.sgemm_q4_glu.argtypes = [cint, cint, cint, i64, i64, i64, vp, i64, vp, vp, i64, i64, vp, vp,
                                  i64, vp, vp, i64, vp, i64, vp]
     lib.sgemm_q4_glu.restype = cint
+    lib.sgemm_lora_workspace.argtypes = [cint, cint, i64, i64, i64, i64, i64]
+    lib.sgemm_lora_workspace.restype = i64
+    lib.sgemm_lora.argtypes = [cint, i64, i64, i64, i64, i64, vp, i64, vp, i64, i64, vp, i64, i64, vp,
+                               cint, vp, f32, vp, i64, vp, i64, vp, i64, vp, i64, vp]
+    lib.sgemm_lora.restype = cint
+    lib.sgemm_lora_backward.argtypes = [cint, i64, i64, i64, i64, i64, vp, i64, vp, i64, vp, i64, i64,
+                                        vp, i64, i64, vp, i64, vp, cint, vp, f32, vp, i64, vp, i64, vp,
+                                        i64, i64, vp, i64, i64, vp, i64, vp]
+    lib.sgemm_lora_backward.restype = cint
+    lib.sgemm_orthogonalize_workspace.argtypes = [i64, i64, i64]
+    lib.sgemm_orthogonalize_workspace.restype = i64
+    lib.sgemm_orthogonalize.argtypes = [cint, i64, i64, i64, vp, i64, i64, vp, i64, i64, cint, vp,
+                                        ctypes.c_double, vp, i64, vp]
+    lib.sgemm_orthogonalize.restype = cint
     lib.sgemm_copy_f32.argtypes = [vp, vp, i64, vp]
     lib.sgemm_copy_f32.restype = cint
     lib.sgemm_copy_f32_launch.argtypes = [vp, vp, i64, cint, i64, vp]
@@ -532,6 +549,203 @@ def q4_glu(X, gate_w, gate_scales, up_w, up_scales, gate_zeros=None, up_zeros=No
           gate_zeros.data_ptr() if gate_zeros is not None else None,
           up_zeros.data_ptr() if up_zeros is not None else None, ld[2], H.data_ptr(), ldh)
     return H
+
+
+def _stack(t, name, shape, dtype):
+    """(row stride, matrix stride) of a 3-D GPU tensor of row-major matrices,
+    checked."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype:
+        raise TypeError(f"{name} must be a tensor of {dtype}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be 3-D")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    (n, rows, cols), (stride, ld, step) = t.shape, t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{name} must have unit column stride (row-major)")
+    if rows > 1 and ld < cols:
+        raise ValueError(f"{name} must have a row stride of at least its row length")
+    return (ld if rows > 1 else max(cols, 1)), (stride if n > 1 else 0)
+
+
+def _lora_ids(ids, M, L):
+    """Bits of the ids' type (32 where there are none), checked."""
+    if ids is None:
+        if L != 1:
+            raise ValueError("ids are needed where there is more than one adapter")
+        return 32
+    if not isinstance(ids, torch.Tensor) or ids.dtype not in (torch.int32, torch.int64):
+        raise TypeError("ids must be a tensor of torch.int32 or torch.int64")
+    if ids.device.type != "cuda":
+        raise ValueError("ids must be a GPU tensor")
+    if tuple(ids.shape) != (M,) or (M > 1 and ids.stride(0) != 1):
+        raise ValueError(f"ids must be {M} contiguous numbers, one for each row")
+    return 32 if ids.dtype == torch.int32 else 64
+
+
+def _lora_scale(scale, L):
+    """(factor of all adapters, tensor of theirs or None), checked."""
+    if isinstance(scale, torch.Tensor):
+        if scale.dtype != torch.float32:
+            raise TypeError("scale must be a number or a tensor of torch.float32")
+        if scale.device.type != "cuda":
+            raise ValueError("scale must be a GPU tensor")
+        if tuple(scale.shape) != (L,) or (L > 1 and scale.stride(0) != 1):
+            raise ValueError(f"scale must be {L} contiguous numbers, one for each adapter")
+        return 1.0, scale
+    return float(scale), None
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(name, *sizes):
+    n = getattr(load(), name)(*sizes)
+    if n < 0:
+        raise SgemmError(-n, name)
+    return n
+
+
+def _workspace(like, name, *sizes):
+    """Scratch memory for one call, from torch's allocator: it belongs to the
+    current stream, or to the graph that is being captured."""
+    n = _workspace_bytes(name, *sizes)
+    return torch.empty(n, dtype=torch.uint8, device=like.device), n
+
+
+def lora(X, A, B, ids=None, scale=1.0, base=None, out=None, save=False):
+    """Low-rank adapters of many requests beside a shared projection, on the
+    current stream: Y[m] = base[m] + scale[l] (X[m] A[l]^T) B[l]^T with l =
+    ids[m].  X is M x K, A is L x R x K, B is L x N x R (R up to 256), ``base``
+    (the projection's result; None: zero) and Y are M x N, all float32, float16
+    or bfloat16.  ``ids`` (int32 or int64, M) names each row's adapter; an id
+    outside 0..L-1, -1 say, means none: Y[m] = base[m].  None: every row has the
+    only adapter.  ``scale`` is a number, or float32 numbers for the adapters.
+    ``out`` may be base itself.  Sums are kept in float32 and rounded once.
+    Returns Y, with ``save`` (Y, H): H[m] = X[m] A[l]^T (M x R, float32, zero for
+    a row without adapter), which lora_backward takes; ``save`` may also be the
+    tensor H to write."""
+    _FLOATS or _use_torch()
+    ldx = _rows(X, "X", None, _FLOATS)
+    (M, K), t = X.shape, X.dtype
+    lda, sa = _stack(A, "A", None, t)
+    L, R = A.shape[:2]
+    if A.shape[2] != K:
+        raise ValueError(f"A has shape {tuple(A.shape)}, expected {(L, R, K)}")
+    N = B.shape[1] if isinstance(B, torch.Tensor) and B.dim() == 3 else 0
+    ldb, sb = _stack(B, "B", (L, N, R), t)
+    bits = _lora_ids(ids, M, L)
+    alpha, scales = _lora_scale(scale, L)
+    ldbase = 1 if base is None else _rows(base, "base", (M, N), (t,))
+    if out is None:
+        Y, ldy = torch.empty((M, N), dtype=t, device=X.device), max(N, 1)
+    else:
+        Y, ldy = out, _rows(out, "out", (M, N), (t,))
+    H, ldh = None, 1
+    if isinstance(save, torch.Tensor):
+        H, ldh = save, _rows(save, "save", (M, R))
+    elif save:
+        H, ldh = torch.empty((M, R), dtype=torch.float32, device=X.device), R
+    sizes = (_FLOATS[t], M, N, K, R, L)
+    ws, n = _workspace(X, "sgemm_lora_workspace", 0, *sizes)
+    _call(load().sgemm_lora, "sgemm_lora", X, (A, B, ids, scales, base, Y, H), *sizes, X.data_ptr(), ldx,
+          A.data_ptr(), lda, sa, B.data_ptr(), ldb, sb, _ptr(ids), bits, _ptr(scales), alpha,
+          _ptr(base), ldbase, Y.data_ptr(), ldy, _ptr(H), ldh, ws.data_ptr(), n)
+    return Y if H is None else (Y, H)
+
+
+def lora_backward(dY, X, A, B, H, ids=None, scale=1.0, base=None, need_dx=True, need_dw=True, dX=None,
+                  dW=None):
+    """Gradients of lora: from dY (M x N) and the H of the forward pass,
+    (dX, dA, dB), None for those not asked for (``need_dx``, ``need_dw``).
+    ``base`` (M x K, None: zero) is the gradient of X through the projection, to
+    which dX adds the adapters'; ``dX`` may be base itself.  ``dX`` and ``dW`` =
+    (dA, dB) may be supplied; dA and dB are written for every adapter, zero
+    where no row has it.  Types are as in lora: the gradients have X's."""
+    _FLOATS or _use_torch()
+    ldx = _rows(X, "X", None, _FLOATS)
+    (M, K), t = X.shape, X.dtype
+    lda, sa = _stack(A, "A", None, t)
+    L, R = A.shape[:2]
+    if A.shape[2] != K:
+        raise ValueError(f"A has shape {tuple(A.shape)}, expected {(L, R, K)}")
+    N = _dim(dY, 1)
+    lddy = _rows(dY, "dY", (M, N), (t,))
+    ldb, sb = _stack(B, "B", (L, N, R), t)
+    ldh = _rows(H, "H", (M, R))
+    bits = _lora_ids(ids, M, L)
+    alpha, scales = _lora_scale(scale, L)
+    ldbase = 1 if base is None else _rows(base, "base", (M, K), (t,))
+    lddx = ldda = lddb = 1
+    sda = sdb = 0
+    if need_dx:
+        dX = torch.empty((M, K), dtype=t, device=X.device) if dX is None else dX
+        lddx = _rows(dX, "dX", (M, K), (t,))
+    else:
+        dX = None
+    dA = dB = None
+    if need_dw:
+        dA, dB = _two(dW, "dW") if dW is not None else (
+            torch.empty((L, R, K), dtype=t, device=X.device), torch.empty((L, N, R), dtype=t, device=X.device))
+        (ldda, sda), (lddb, sdb) = _stack(dA, "dA", (L, R, K), t), _stack(dB, "dB", (L, N, R), t)
+    sizes = (_FLOATS[t], M, N, K, R, L)
+    ws, n = _workspace(X, "sgemm_lora_workspace", 1, *sizes)
+    # Empty tensors have no address; the entry point takes null for "skip".
+    null = [None if g is None or g.numel() == 0 else g.data_ptr() for g in (dX, dA, dB)]
+    _call(load().sgemm_lora_backward, "sgemm_lora_backward", X,
+          (dY, A, B, H, ids, scales, base, dX, dA, dB), *sizes, dY.data_ptr(), lddy, X.data_ptr(), ldx,
+          A.data_ptr(), lda, sa, B.data_ptr(), ldb, sb, H.data_ptr(), ldh, _ptr(ids), bits,
+          _ptr(scales), alpha, _ptr(base), ldbase, null[0], lddx, null[1], ldda, sda, null[2], lddb, sdb,
+          ws.data_ptr(), n)
+    return dX, dA, dB
+
+
+MUON = (3.4445, -4.7750, 2.0315)
+
+
+def orthogonalize(G, steps=5, coefficients=MUON, eps=1e-7, out=None):
+    """The update G with all its singular values moved to about one, by
+    Newton-Schulz steps, on the current stream: X = G / (|G| + eps), |G| the
+    Frobenius norm, then for each step X = a X + (b S + c S S) X with S = X X^T
+    (X^T X on the right for a tall G).  G is a matrix or a stack of matrices
+    (3-D), float32, float16 or bfloat16, and so is the result (``out`` when
+    given; it may be G itself).  ``coefficients`` is one triple (a, b, c) for
+    all ``steps``, or a sequence of triples, one for each step (``steps`` is
+    then not used).  They are refused where they let X grow past 64."""
+    _FLOATS or _use_torch()
+    if not isinstance(G, torch.Tensor) or G.dtype not in _FLOATS:
+        raise TypeError(f"G must be a tensor of {' or '.join(str(d) for d in _FLOATS)}")
+    if G.dim() not in (2, 3):
+        raise ValueError("G must be a matrix or a stack of matrices")
+    coef = _triples(coefficients, steps)
+    g3 = G if G.dim() == 3 else G.unsqueeze(0)
+    ldg, sg = _stack(g3, "G", None, G.dtype)
+    if out is None:
+        out = torch.empty(G.shape, dtype=G.dtype, device=G.device)
+    elif not isinstance(out, torch.Tensor) or out.shape != G.shape:
+        raise ValueError("out has the wrong shape")
+    ldo, so = _stack(out if out.dim() == 3 else out.unsqueeze(0), "out", tuple(g3.shape), G.dtype)
+    batch, M, N = g3.shape
+    ws, n = _workspace(G, "sgemm_orthogonalize_workspace", batch, M, N)
+    _call(load().sgemm_orthogonalize, "sgemm_orthogonalize", G, (out,), _FLOATS[G.dtype], batch, M, N,
+          G.data_ptr(), ldg, sg, out.data_ptr(), ldo, so, len(coef) // 3, coef, float(eps),
+          ws.data_ptr(), n)
+    return out
+
+
+def _triples(coefficients, steps):
+    """The coefficients of every step as a C array of doubles."""
+    rows = list(coefficients)
+    if rows and not isinstance(rows[0], (tuple, list)):
+        rows = [rows] * int(steps)
+    if not rows or any(len(r) != 3 for r in rows):
+        raise ValueError("coefficients must be a triple (a, b, c), or one triple for each step")
+    flat = [float(v) for r in rows for v in r]
+    return (ctypes.c_double * len(flat))(*flat)
 
 
 def copy_f32(dst, src):

@@ -1,6 +1,9 @@
 // C ABI entry points: argument validation (host only, before any HIP call),
 // variant dispatch and launch-status reporting.  The interface contract is
 // documented in include/sgemm.h.
+#include <algorithm>
+#include <cmath>
+
 #include "../../include/sgemm.h"
 #include "kernels.h"
 
@@ -197,6 +200,70 @@ int run_q4(int act, int xtype, int stype, int64_t M, int64_t N, int64_t K, const
     return launch_status(sgemm::launch_q4(g, static_cast<hipStream_t>(stream)));
 }
 
+// A stack of `n` rows x cols matrices, `stride` elements apart; of more than
+// one, the one row of elements that they span.
+View stack_view(const void* p, int64_t n, int64_t stride, int64_t rows, int64_t cols, int64_t ld,
+                int64_t size) {
+    if (!p || n <= 0 || rows <= 0 || cols <= 0) return {nullptr, 0, 0, 1, size};
+    if (n == 1) return {p, rows, cols, ld, size};
+    const int64_t len = (n - 1) * stride + (rows - 1) * ld + cols;
+    return {p, 1, len, len, size};
+}
+
+// Whether a stack's strides keep every element inside 62 bits of offset (and,
+// for an output, its matrices apart).
+bool stack_ok(int64_t n, int64_t stride, int64_t rows, int64_t cols, int64_t ld, bool output) {
+    if (!ld_ok(ld, cols) || stride < 0 || stride > (int64_t(1) << 60)) return false;
+    typedef __int128 wide;
+    const wide one = rows > 0 ? wide(rows - 1) * ld + cols : 0;
+    if (wide(n > 0 ? n - 1 : 0) * stride + one > (wide(1) << 60)) return false;
+    // Apart: one after another, or rows of one matrix in the gaps of another's.
+    return !output || n <= 1 || stride >= one ||
+           (stride >= cols && (n - 1) * wide(stride) + cols <= ld);
+}
+
+constexpr int64_t kIndexLimit = (int64_t(1) << 31) - 1;
+constexpr int64_t kOrthoLimit = 65536, kOrthoBatch = 65535;
+
+int validate_lora_sizes(int type, int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
+    if (type < 0 || type > SGEMM_TYPE_BF16) return SGEMM_ERR_ARG;
+    if (M < 0 || N < 0 || K < 0 || M > kIndexLimit || N > kIndexLimit || K > kIndexLimit) return SGEMM_ERR_DIM;
+    if (R < 1 || R > SGEMM_LORA_MAX_RANK || L < 1 || L > SGEMM_LORA_MAX_ADAPTERS) return SGEMM_ERR_DIM;
+    return SGEMM_OK;
+}
+
+// Bound of the singular values after each step (bounds[i]: before step i), from
+// those of G / |G|, which are at most 1.  |a s + b s^3 + c s^5| over [0, r] is
+// largest at r or where a + 3 b q + 5 c q^2 = 0, q = s^2.
+bool ortho_bounds(int steps, const double* coef, double* bounds) {
+    double r = 1.0;
+    for (int i = 0; i < steps; i++) {
+        const double a = coef[3 * i], b = coef[3 * i + 1], c = coef[3 * i + 2];
+        if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
+        bounds[i] = r;
+        auto p = [&](double q) { return std::fabs(std::sqrt(q) * (a + q * (b + q * c))); };
+        double top = p(r * r);
+        const double disc = 9 * b * b - 20 * a * c;
+        double roots[2] = {-1, -1};
+        if (c != 0 && disc >= 0) {
+            roots[0] = (-3 * b + std::sqrt(disc)) / (10 * c);
+            roots[1] = (-3 * b - std::sqrt(disc)) / (10 * c);
+        } else if (c == 0 && b != 0) {
+            roots[0] = -a / (3 * b);
+        }
+        for (double q : roots)
+            if (q > 0 && q < r * r) top = std::max(top, p(q));
+        // Roundings of a step and of its result, counted generously.
+        r = top * 1.01;
+        if (!(r <= 64.0)) return false;
+        // The factor a + b s^2 + c s^4 is stored too.
+        if (!(std::fabs(a) + std::fabs(b) * bounds[i] * bounds[i] + std::fabs(c) * std::pow(bounds[i], 4) <= 1e9))
+            return false;
+    }
+    bounds[steps] = r;
+    return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -372,6 +439,106 @@ int sgemm_q4_glu(int act, int xtype, int stype, int64_t M, int64_t F, int64_t K,
                   ldz, H, ldh, stream);
 }
 
+int64_t sgemm_lora_workspace(int backward, int type, int64_t M, int64_t N, int64_t K, int64_t R,
+                             int64_t L) {
+    const int v = validate_lora_sizes(type, M, N, K, R, L);
+    if (v != SGEMM_OK) return -v;
+    return int64_t(sgemm::lora_workspace_bytes(backward != 0, type, M, N, K, int(R), int(L)));
+}
+
+int sgemm_lora(int type, int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, const void* X,
+               int64_t ldx, const void* A, int64_t lda, int64_t stride_a, const void* B, int64_t ldb,
+               int64_t stride_b, const void* ids, int id_bits, const float* s, float alpha,
+               const void* base, int64_t ldbase, void* Y, int64_t ldy, float* H, int64_t ldh,
+               void* workspace, int64_t workspace_bytes, void* stream) {
+    int v = validate_lora_sizes(type, M, N, K, R, L);
+    if (v != SGEMM_OK) return v;
+    if (id_bits != 32 && id_bits != 64) return SGEMM_ERR_ARG;
+    if (!ld_ok(ldx, K) || !ld_ok(ldy, N) || (base && !ld_ok(ldbase, N)) || (H && !ld_ok(ldh, R))) return SGEMM_ERR_LD;
+    if (!stack_ok(L, stride_a, R, K, lda, false) || !stack_ok(L, stride_b, N, R, ldb, false)) return SGEMM_ERR_LD;
+    if (M == 0 || (N == 0 && !H)) return SGEMM_OK;
+    if ((N > 0 && (!Y || !B)) || (K > 0 && (!X || !A))) return SGEMM_ERR_NULLPTR;
+    const int64_t es = type == SGEMM_TYPE_F32 ? 4 : 2;
+    const View in[] = {{base, M, N, ldbase, es}, {X, M, K, ldx, es}, stack_view(A, L, stride_a, R, K, lda, es),
+                       stack_view(B, L, stride_b, N, R, ldb, es), {ids, 1, M, M, id_bits / 8}, {s, 1, L, L, 4},
+                       {workspace, 1, workspace_bytes, workspace_bytes > 0 ? workspace_bytes : 1, 1}};
+    const View out[] = {{Y, M, N, ldy, es}, {H, M, R, ldh, 4}};
+    if ((v = check_alias(in, out, 1, 1)) != SGEMM_OK) return v;
+    if (workspace_bytes < int64_t(sgemm::lora_workspace_bytes(false, type, M, N, K, int(R), int(L))))
+        return SGEMM_ERR_SCRATCH;
+    if (workspace_bytes > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15))) return SGEMM_ERR_ARG;
+    const sgemm::LoraArgs g{type, M,  N,  K,  int(R), int(L),        X,  ldx,   A,    lda,    stride_a, B,
+                            ldb,  stride_b, ids, id_bits == 64, s, alpha, base, ldbase, Y, ldy, H, ldh, workspace};
+    return launch_status(sgemm::launch_lora(g, static_cast<hipStream_t>(stream)));
+}
+
+int sgemm_lora_backward(int type, int64_t M, int64_t N, int64_t K, int64_t R, int64_t L,
+                        const void* dY, int64_t lddy, const void* X, int64_t ldx, const void* A,
+                        int64_t lda, int64_t stride_a, const void* B, int64_t ldb, int64_t stride_b,
+                        const float* H, int64_t ldh, const void* ids, int id_bits, const float* s,
+                        float alpha, const void* base, int64_t ldbase, void* dX, int64_t lddx,
+                        void* dA, int64_t ldda, int64_t stride_da, void* dB, int64_t lddb,
+                        int64_t stride_db, void* workspace, int64_t workspace_bytes, void* stream) {
+    int v = validate_lora_sizes(type, M, N, K, R, L);
+    if (v != SGEMM_OK) return v;
+    if (id_bits != 32 && id_bits != 64) return SGEMM_ERR_ARG;
+    if (!ld_ok(lddy, N) || !ld_ok(ldx, K) || !ld_ok(ldh, R) || (base && !ld_ok(ldbase, K)) || (dX && !ld_ok(lddx, K)))
+        return SGEMM_ERR_LD;
+    if (!stack_ok(L, stride_a, R, K, lda, false) || !stack_ok(L, stride_b, N, R, ldb, false)) return SGEMM_ERR_LD;
+    if ((dA && !stack_ok(L, stride_da, R, K, ldda, true)) || (dB && !stack_ok(L, stride_db, N, R, lddb, true)))
+        return SGEMM_ERR_LD;
+    if (!dX && !dA && !dB) return SGEMM_OK;
+    const bool rows = M > 0;
+    if (rows && N > 0 && (!dY || ((dX || dA) && !B) || (dB && !H))) return SGEMM_ERR_NULLPTR;
+    if (rows && K > 0 && ((dX && !A) || (dA && !X))) return SGEMM_ERR_NULLPTR;
+    const int64_t es = type == SGEMM_TYPE_F32 ? 4 : 2;
+    const View in[] = {{base, M, K, ldbase, es}, {X, M, K, ldx, es}, {dY, M, N, lddy, es},
+                       stack_view(A, L, stride_a, R, K, lda, es), stack_view(B, L, stride_b, N, R, ldb, es),
+                       {H, M, R, ldh, 4}, {ids, 1, M, M > 0 ? M : 1, id_bits / 8}, {s, 1, L, L, 4},
+                       {workspace, 1, workspace_bytes, workspace_bytes > 0 ? workspace_bytes : 1, 1}};
+    const View out[] = {{dX, M, K, lddx, es}, stack_view(dA, L, stride_da, R, K, ldda, es),
+                        stack_view(dB, L, stride_db, N, R, lddb, es)};
+    if ((v = check_alias(in, out, 1, 1)) != SGEMM_OK) return v;
+    if (workspace_bytes < int64_t(sgemm::lora_workspace_bytes(true, type, M, N, K, int(R), int(L))))
+        return SGEMM_ERR_SCRATCH;
+    if (workspace_bytes > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15))) return SGEMM_ERR_ARG;
+    const sgemm::LoraGradArgs g{{type, M, N, K, int(R), int(L), X, ldx, A, lda, stride_a, B, ldb, stride_b, ids,
+                                 id_bits == 64, s, alpha, base, ldbase, const_cast<void*>(dY), lddy,
+                                 const_cast<float*>(H), ldh, workspace},
+                                dX, lddx, dA, ldda, stride_da, dB, lddb, stride_db};
+    return launch_status(sgemm::launch_lora_backward(g, static_cast<hipStream_t>(stream)));
+}
+
+int64_t sgemm_orthogonalize_workspace(int64_t batch, int64_t M, int64_t N) {
+    if (batch < 0 || M < 0 || N < 0 || M > kOrthoLimit || N > kOrthoLimit || batch > kOrthoBatch) return -SGEMM_ERR_DIM;
+    return int64_t(sgemm::ortho_workspace_bytes(batch, M, N));
+}
+
+int sgemm_orthogonalize(int type, int64_t batch, int64_t M, int64_t N, const void* G, int64_t ldg,
+                        int64_t stride_g, void* O, int64_t ldo, int64_t stride_o, int steps,
+                        const double* coefficients, double eps, void* workspace,
+                        int64_t workspace_bytes, void* stream) {
+    if (type < 0 || type > SGEMM_TYPE_BF16 || steps < 1 || steps > SGEMM_ORTHO_MAX_STEPS) return SGEMM_ERR_ARG;
+    if (!(eps >= 0) || !std::isfinite(eps)) return SGEMM_ERR_ARG;
+    if (batch < 0 || M < 0 || N < 0 || M > kOrthoLimit || N > kOrthoLimit || batch > kOrthoBatch) return SGEMM_ERR_DIM;
+    if (!stack_ok(batch, stride_g, M, N, ldg, false) || !stack_ok(batch, stride_o, M, N, ldo, true)) return SGEMM_ERR_LD;
+    if (!coefficients) return SGEMM_ERR_NULLPTR;
+    double bounds[SGEMM_ORTHO_MAX_STEPS + 1];
+    if (!ortho_bounds(steps, coefficients, bounds)) return SGEMM_ERR_ARG;
+    if (batch == 0 || M == 0 || N == 0) return SGEMM_OK;
+    if (!G || !O) return SGEMM_ERR_NULLPTR;
+    const int64_t es = type == SGEMM_TYPE_F32 ? 4 : 2;
+    const bool place = G == O && ldg == ldo && (batch == 1 || stride_g == stride_o);
+    const View w{workspace, 1, workspace_bytes, workspace_bytes > 0 ? workspace_bytes : 1, 1};
+    const View vg = stack_view(G, batch, stride_g, M, N, ldg, es), vo = stack_view(O, batch, stride_o, M, N, ldo, es);
+    if ((!place && share(vg, vo)) || share(vg, w) || share(vo, w)) return SGEMM_ERR_ALIAS;
+    if (workspace_bytes < int64_t(sgemm::ortho_workspace_bytes(batch, M, N))) return SGEMM_ERR_SCRATCH;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255)) return SGEMM_ERR_ARG;
+    const sgemm::OrthoArgs g{type, batch, M,     N,   G,      ldg, stride_g, O,
+                             ldo,  stride_o, steps, coefficients, bounds, eps, workspace};
+    return launch_status(sgemm::launch_orthogonalize(g, static_cast<hipStream_t>(stream)));
+}
+
 int sgemm_auto_variant(int64_t M, int64_t N, int64_t K, const float* A, int64_t lda,
                        const float* B, int64_t ldb, float* C, int64_t ldc) {
     const int v = validate(SGEMM_AUTO, M, N, K, A, lda, B, ldb, C, ldc);
@@ -464,7 +631,7 @@ const char* sgemm_status_string(int status) {
         case SGEMM_ERR_LAUNCH: return "kernel launch failed";
         case SGEMM_ERR_UNSUPPORTED: return "variant cannot address this shape";
         case SGEMM_ERR_ARG: return "invalid argument";
-        case SGEMM_ERR_SCRATCH: return "the requested split needs more than the static scratch holds";
+        case SGEMM_ERR_SCRATCH: return "scratch memory too small (the static scratch for a requested split, or the workspace given)";
         default: return "unknown status";
     }
 }

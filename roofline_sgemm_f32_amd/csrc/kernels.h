@@ -263,4 +263,58 @@ struct Q4Args {
 };
 hipError_t launch_q4(const Q4Args& g, hipStream_t s);
 
+// Low-rank adapters (lora.hip).  Sizes M, N, K below 2^31.
+struct LoraArgs {
+    int type;
+    int64_t M, N, K;
+    int R, L;
+    const void* X;
+    int64_t ldx;
+    const void* A;  // L x R x K
+    int64_t lda, sa;
+    const void* B;  // L x N x R
+    int64_t ldb, sb;
+    const void* ids;  // null: adapter 0
+    bool id64;
+    const float* scales;  // null: 1
+    float alpha;
+    const void* base;  // null: 0
+    int64_t ldbase;
+    void* Y;
+    int64_t ldy;
+    float* H;  // null: not kept
+    int64_t ldh;
+    void* ws;
+};
+// Backward: X and H are the forward pass's, Y is dY (read), base and dX M x K.
+struct LoraGradArgs {
+    LoraArgs f;
+    void* dX;  // null: skipped, as dA and dB
+    int64_t lddx;
+    void* dA;
+    int64_t ldda, sda;
+    void* dB;
+    int64_t lddb, sdb;
+};
+size_t lora_workspace_bytes(bool backward, int type, int64_t M, int64_t N, int64_t K, int R, int L);
+hipError_t launch_lora(const LoraArgs& g, hipStream_t s);
+hipError_t launch_lora_backward(const LoraGradArgs& g, hipStream_t s);
+
+// Orthogonalised updates (orthogonalize.hip).  bounds[i]: of |X| before step i.
+struct OrthoArgs {
+    int type;
+    int64_t batch, M, N;
+    const void* G;
+    int64_t ldg, sg;
+    void* O;
+    int64_t ldo, so;
+    int steps;
+    const double* coef;
+    const double* bounds;
+    double eps;
+    void* ws;
+};
+size_t ortho_workspace_bytes(int64_t batch, int64_t M, int64_t N);
+hipError_t launch_orthogonalize(const OrthoArgs& g, hipStream_t s);
+
 }  // namespace sgemm

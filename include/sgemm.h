@@ -376,7 +376,7 @@ int sgemm_q4_glu(int act, int xtype, int stype, int64_t M, int64_t F, int64_t K,
  * fine), 16-byte aligned, which the call's kernels use until they end.  They
  * allocate nothing and never synchronise; every call can be captured. */
 #define SGEMM_LORA_MAX_RANK 256
-#define SGEMM_LORA_MAX_ADAPTERS 32768
+#define SGEMM_LORA_MAX_ADAPTERS 4096
 
 /* Bytes of workspace of sgemm_lora (backward 0) or sgemm_lora_backward
  * (backward 1) for these sizes, or minus a status code. */

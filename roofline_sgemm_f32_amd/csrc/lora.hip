@@ -1,6 +1,7 @@
 // Low-rank adapters beside a projection, and their gradients: one output per
 // lane (or wave, for the sums along K and N).
-#include "kernels.h"
+#include "lora.h"
+#include "lora_kernels.h"
 
 namespace sgemm {
 namespace {
@@ -84,15 +85,101 @@ __global__ void __launch_bounds__(256) lora_weights(LoraArgs g, const float* V, 
 
 }  // namespace
 
-size_t lora_workspace_bytes(bool, int, int64_t M, int64_t, int64_t, int R, int) { return size_t(M) * R * sizeof(float); }
+namespace {
+
+// Sizes of a forward pass's launches and of its workspace.
+struct ForwardPlan {
+    RowPlan::Mode mode;
+    int tmb;                 // 16-row blocks of a tile
+    int64_t tiles;           // at most this many
+    int planes;
+    int64_t kshare, nshare;
+    size_t p_at, order_at, tiles_at, bytes;
+};
+
+size_t align_up(size_t n) { return (n + 255) / 256 * 256; }
+
+ForwardPlan forward_plan(int type, bool ids, int64_t M, int64_t N, int64_t K, int R, int L) {
+    ForwardPlan p{};
+    const int64_t adapters = L < M ? L : M;
+    p.mode = !ids ? RowPlan::UNIFORM : M <= 64 ? RowPlan::SINGLE : RowPlan::SORTED;
+    p.tmb = p.mode == RowPlan::SINGLE || M / (ids ? adapters : 1) < 32 ? 1 : 4;
+    const int tile = 16 * p.tmb;
+    p.tiles = p.mode == RowPlan::SINGLE ? M : ceil_div(M, tile) + (ids ? adapters + 1 : 0);
+    const int64_t busy = p.mode == RowPlan::SINGLE ? M : ceil_div(M, tile);
+    const int64_t kunit = type == T_F32 ? 128 : 256;  // four waves' double steps
+    int64_t planes = ceil_div(512, busy), most = ceil_div(K, kunit);
+    planes = planes > most ? most : planes;
+    planes = planes > 16 ? 16 : planes < 1 ? 1 : planes;
+    p.kshare = K > 0 ? ceil_div(ceil_div(K, planes), kunit) * kunit : 1;
+    p.planes = int(K > 0 ? ceil_div(K, p.kshare) : 1);
+    int64_t shares = ceil_div(1024, busy), top = ceil_div(N, 256);
+    shares = shares > top ? top : shares;
+    shares = shares < 1 ? 1 : shares > 4096 ? 4096 : shares;
+    p.nshare = N > 0 ? ceil_div(ceil_div(N, shares), 256) * 256 : 256;
+    p.p_at = 0;
+    p.order_at = align_up(size_t(p.planes) * M * R * sizeof(float));
+    p.tiles_at = p.order_at + align_up(size_t(M) * sizeof(int));
+    p.bytes = p.mode == RowPlan::SORTED ? p.tiles_at + align_up(size_t(4 + 4 * p.tiles) * sizeof(int)) : p.order_at;
+    return p;
+}
+
+template <int T, int TMB>
+void shrink(const ShrinkArgs& a, int64_t tiles, int planes, hipStream_t s) {
+    const dim3 block(64 * kShrinkWaves);
+    const unsigned x = grid_for(tiles);
+    if (a.R <= 16) hipLaunchKernelGGL((lora_shrink<T, 1, TMB>), dim3(x, planes, 1), block, 0, s, a);
+    else if (a.R <= 32) hipLaunchKernelGGL((lora_shrink<T, 2, TMB>), dim3(x, planes, 1), block, 0, s, a);
+    else hipLaunchKernelGGL((lora_shrink<T, 4, TMB>), dim3(x, planes, (a.R + 63) / 64), block, 0, s, a);
+}
+
+template <int T, int TMB>
+void expand(const ExpandArgs& a, int64_t tiles, hipStream_t s) {
+    const dim3 grid(grid_for(tiles), unsigned(ceil_div(a.N > 0 ? a.N : 1, a.nshare)));
+    const size_t lds = expand_lds<T>(a.R, 16 * TMB);
+    if constexpr (T != T_F32) {
+        if (a.R <= 16) {
+            hipLaunchKernelGGL((lora_expand<T, TMB, true>), grid, dim3(256), lds, s, a);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((lora_expand<T, TMB, false>), grid, dim3(256), lds, s, a);
+}
+
+template <int T>
+hipError_t forward(const LoraArgs& g, const ForwardPlan& p, hipStream_t s) {
+    char* const ws = static_cast<char*>(g.ws);
+    RowPlan rows{p.mode, g.ids, g.id64, int(g.M), g.L, reinterpret_cast<int*>(ws + p.order_at),
+                 reinterpret_cast<int*>(ws + p.tiles_at)};
+    if (p.mode == RowPlan::SORTED) {
+        GroupArgs a{g.ids, g.id64, int(g.M), g.L, 0, reinterpret_cast<int*>(ws + p.order_at), 16 * p.tmb,
+                    reinterpret_cast<int*>(ws + p.tiles_at), 0, nullptr, nullptr};
+        const hipError_t e = launch_lora_group(a, s);
+        if (e != hipSuccess) return e;
+    }
+    float* P = reinterpret_cast<float*>(ws + p.p_at);
+    const ShrinkArgs sh{g.X, g.ldx, g.A, g.lda, g.sa, g.K, g.R, nullptr, 1.0f, false, P, g.M * g.R, p.kshare, rows, p.tiles};
+    const ExpandArgs ex{P, g.M * g.R, p.planes, g.R, g.B, g.ldb, g.sb, g.N, g.scales, g.alpha, true,
+                        g.base, g.ldbase, g.Y, g.ldy, g.H, g.ldh, p.nshare, rows, p.tiles};
+    if (p.tmb == 1) shrink<T, 1>(sh, p.tiles, p.planes, s), expand<T, 1>(ex, p.tiles, s);
+    else shrink<T, 4>(sh, p.tiles, p.planes, s), expand<T, 4>(ex, p.tiles, s);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t lora_workspace_bytes(bool backward, int type, int64_t M, int64_t N, int64_t K, int R, int L) {
+    if (M == 0) return 0;
+    if (backward) return size_t(M) * R * sizeof(float);
+    const size_t a = forward_plan(type, false, M, N, K, R, L).bytes, b = forward_plan(type, true, M, N, K, R, L).bytes;
+    return a > b ? a : b;
+}
 
 hipError_t launch_lora(const LoraArgs& g, hipStream_t s) {
-    float* H = g.H ? g.H : static_cast<float*>(g.ws);
-    const int64_t ldh = g.H ? g.ldh : g.R;
-    hipLaunchKernelGGL(lora_reduce, dim3(grid_for(ceil_div(g.M * g.R, 4))), dim3(256), 0, s, g, H, ldh, false);
-    if (g.N > 0)
-        hipLaunchKernelGGL(lora_expand, dim3(grid_for(ceil_div(g.M * g.N, 256))), dim3(256), 0, s, g, H, ldh, g.Y, g.ldy, g.N, false);
-    return hipGetLastError();
+    const ForwardPlan p = forward_plan(g.type, g.ids != nullptr, g.M, g.N, g.K, g.R, g.L);
+    if (g.type == T_F32) return forward<T_F32>(g, p, s);
+    if (g.type == T_F16) return forward<T_F16>(g, p, s);
+    return forward<T_BF16>(g, p, s);
 }
 
 hipError_t launch_lora_backward(const LoraGradArgs& b, hipStream_t s) {

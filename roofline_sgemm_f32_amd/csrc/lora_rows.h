@@ -1,0 +1,113 @@
+// Which rows a workgroup of the adapter kernels takes, and element types.
+#pragma once
+#include <type_traits>
+
+#include "kernels.h"
+
+namespace sgemm {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+template <int T> struct Elem;
+template <> struct Elem<T_F32> { using type = float; };
+template <> struct Elem<T_F16> { using type = _Float16; };
+template <> struct Elem<T_BF16> { using type = __bf16; };
+// Elements in 16 bytes.
+template <int T> constexpr int kVec = T == T_F32 ? 4 : 8;
+
+// A run of rows with one adapter (-1: none): positions [start, start + count)
+// of the order.
+struct RowTile {
+    int adapter, start, count;
+};
+
+// How rows are dealt out in tiles.
+struct RowPlan {
+    enum Mode { SORTED, SINGLE, UNIFORM } mode;
+    const void* ids;   // SINGLE: a tile is one row, with the adapter of its id
+    bool id64;
+    int M, L;
+    const int* order;  // SORTED: row of each position, rows of one adapter together
+    const int* head;   // SORTED: number of tiles, then RowTile's fields of each
+};
+
+__device__ __forceinline__ int adapter_of(const void* ids, bool id64, int L, int64_t m) {
+    const int64_t id = id64 ? static_cast<const int64_t*>(ids)[m] : static_cast<const int32_t*>(ids)[m];
+    return id >= 0 && id < L ? int(id) : -1;
+}
+
+// Tile t of `size` rows; count 0 past the last.
+__device__ __forceinline__ RowTile row_tile(const RowPlan& p, int64_t t, int size) {
+    if (p.mode == RowPlan::SORTED) {
+        if (t >= p.head[0]) return {-1, 0, 0};
+        const int* at = p.head + 4 + 4 * t;
+        return {at[0], at[1], at[2]};
+    }
+    if (p.mode == RowPlan::SINGLE) return {adapter_of(p.ids, p.id64, p.L, t), int(t), 1};
+    const int64_t start = t * size;
+    return {0, int(start), int(p.M - start < size ? p.M - start : size)};
+}
+
+__device__ __forceinline__ int row_at(const RowPlan& p, int position) {
+    return p.mode == RowPlan::SORTED ? p.order[position] : position;
+}
+
+// 16 bytes from any address, and to any.
+__device__ __forceinline__ u32x4 load16(const void* p) {
+    u32x4 v;
+    __builtin_memcpy(&v, p, 16);
+    return v;
+}
+__device__ __forceinline__ void store16(void* p, u32x4 v) { __builtin_memcpy(p, &v, 16); }
+
+// The 16 bytes of elements [i, i + kVec) of a row of n elements, zero past its end.
+template <int T>
+__device__ __forceinline__ u32x4 load_chunk(const typename Elem<T>::type* row, int64_t i, int64_t n) {
+    if (i + kVec<T> <= n) return load16(row + i);
+    typename Elem<T>::type v[kVec<T>];
+#pragma unroll
+    for (int e = 0; e < kVec<T>; e++) v[e] = i + e < n ? row[i + e] : typename Elem<T>::type(0.0f);
+    u32x4 r;
+    __builtin_memcpy(&r, v, 16);
+    return r;
+}
+
+template <int T>
+__device__ __forceinline__ void unpack(u32x4 v, float (&f)[kVec<T>]) {
+    typename Elem<T>::type e[kVec<T>];
+    __builtin_memcpy(e, &v, 16);
+#pragma unroll
+    for (int i = 0; i < kVec<T>; i++) f[i] = float(e[i]);
+}
+template <int T>
+__device__ __forceinline__ u32x4 pack(const float (&f)[kVec<T>]) {
+    typename Elem<T>::type e[kVec<T>];
+#pragma unroll
+    for (int i = 0; i < kVec<T>; i++) e[i] = typename Elem<T>::type(f[i]);
+    u32x4 v;
+    __builtin_memcpy(&v, e, 16);
+    return v;
+}
+
+// One 16 x 16 block plus the products of two operands of 16 bytes a lane: lane
+// l has elements (l / 16) kVec .. of row l % 16 of either.
+template <int T>
+__device__ __forceinline__ v4f mma16(u32x4 a, u32x4 b, v4f c) {
+    if constexpr (T == T_F16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    else if constexpr (T == T_BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+    else {
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[e]), __uint_as_float(b[e]), c, 0, 0, 0);
+        return c;
+    }
+}
+
+}  // namespace
+}  // namespace sgemm

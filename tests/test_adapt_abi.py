@@ -33,7 +33,7 @@ def test_lora_refusals(lib):
     for name in ("M", "N", "K"):
         assert lora(lib, **{name: -1}) == DIM and lora(lib, **{name: 1 << 31}) == DIM, name
     assert lora(lib, R=0) == DIM and lora(lib, R=257) == DIM
-    assert lora(lib, L=0) == DIM and lora(lib, L=32769) == DIM
+    assert lora(lib, L=0) == DIM and lora(lib, L=4097) == DIM
     for name, least in (("ldx", 6), ("lda", 6), ("ldb", 2), ("ldbase", 8), ("ldy", 8), ("ldh", 2)):
         assert lora(lib, **{name: least - 1}) == LD, name
     assert lora(lib, sa=-1) == LD and lora(lib, sb=-1) == LD
@@ -115,10 +115,14 @@ def test_workspaces(lib):
     assert lib.sgemm_lora_workspace(0, 3, 1, 1, 1, 1, 1) == -ARG
     assert lib.sgemm_lora_workspace(1, 0, 1, 1, 1, 300, 1) == -DIM
     assert lib.sgemm_orthogonalize_workspace(1, -1, 1) == -DIM
+    for sizes in ((0, 1, 1), (1, 0, 1), (1, 1, 0), (0, 0, 0), (70, 0, 0), (5000, 0, 9)):
+        for backward in (0, 1):
+            assert lib.sgemm_lora_workspace(backward, 0, *sizes, 4, 3) >= 0, sizes
+        assert lib.sgemm_orthogonalize_workspace(*sizes) >= 0, sizes
     # Sizes stay in range at the largest arguments.
     big = (1 << 31) - 1
-    assert 0 < lib.sgemm_lora_workspace(0, 0, big, big, big, 256, 32768) < 1 << 60
-    assert 0 < lib.sgemm_lora_workspace(1, 0, big, big, big, 256, 32768) < 1 << 60
+    assert 0 < lib.sgemm_lora_workspace(0, 0, big, big, big, 256, 4096) < 1 << 60
+    assert 0 < lib.sgemm_lora_workspace(1, 0, big, big, big, 256, 4096) < 1 << 60
     assert 0 < lib.sgemm_orthogonalize_workspace(65535, 65536, 65536) < 1 << 60
 
 

@@ -113,14 +113,15 @@ ForwardPlan forward_plan(int type, bool ids, int64_t M, int64_t N, int64_t K, in
     planes = planes > 16 ? 16 : planes < 1 ? 1 : planes;
     p.kshare = K > 0 ? ceil_div(ceil_div(K, planes), kunit) * kunit : 1;
     p.planes = int(K > 0 ? ceil_div(K, p.kshare) : 1);
-    int64_t shares = ceil_div(1024, busy), top = ceil_div(N, 256);
+    const int64_t nunit = p.tmb == 1 ? 256 : 64;
+    int64_t shares = ceil_div(1024, busy), top = ceil_div(N, nunit);
     shares = shares > top ? top : shares;
     shares = shares < 1 ? 1 : shares > 4096 ? 4096 : shares;
-    p.nshare = N > 0 ? ceil_div(ceil_div(N, shares), 256) * 256 : 256;
+    p.nshare = N > 0 ? ceil_div(ceil_div(N, shares), nunit) * nunit : nunit;
     p.p_at = 0;
-    p.order_at = align_up(size_t(p.planes) * M * R * sizeof(float));
+    p.order_at = align_up(size_t(p.planes) * M * lora_pitch(R) * sizeof(float));
     p.tiles_at = p.order_at + align_up(size_t(M) * sizeof(int));
-    p.bytes = p.mode == RowPlan::SORTED ? p.tiles_at + align_up(size_t(4 + 4 * p.tiles) * sizeof(int)) : p.order_at;
+    p.bytes = p.mode == RowPlan::SORTED ? p.tiles_at + align_up(size_t(4 + 4 * (p.tiles + 1)) * sizeof(int)) : p.order_at;
     return p;
 }
 
@@ -136,14 +137,36 @@ void shrink(const ShrinkArgs& a, int64_t tiles, int planes, hipStream_t s) {
 template <int T, int TMB>
 void expand(const ExpandArgs& a, int64_t tiles, hipStream_t s) {
     const dim3 grid(grid_for(tiles), unsigned(ceil_div(a.N > 0 ? a.N : 1, a.nshare)));
-    const size_t lds = expand_lds<T>(a.R, 16 * TMB);
-    if constexpr (T != T_F32) {
-        if (a.R <= 16) {
-            hipLaunchKernelGGL((lora_expand<T, TMB, true>), grid, dim3(256), lds, s, a);
-            return;
+    const bool odd = a.R % kVec<T> != 0;
+    if constexpr (TMB == 1) {
+        const size_t lds = expand_lds<T>(a.R, 16 * TMB);
+        auto run = [&](auto kind) {
+            constexpr int KIND = decltype(kind)::value;
+            if (odd) hipLaunchKernelGGL((lora_expand<T, TMB, KIND, true>), grid, dim3(256), lds, s, a);
+            else hipLaunchKernelGGL((lora_expand<T, TMB, KIND, false>), grid, dim3(256), lds, s, a);
+        };
+        if (a.R > (T == T_F32 ? 32 : 64)) return run(std::integral_constant<int, EXPAND_LONG>{});
+        if constexpr (T != T_F32)
+            if (a.R <= 16) return run(std::integral_constant<int, EXPAND_PACKED>{});
+        run(std::integral_constant<int, EXPAND_HELD>{});
+    } else {
+        auto run = [&](auto kind, auto sums) {
+            constexpr int KIND = decltype(kind)::value, NS = decltype(sums)::value;
+            if (odd) hipLaunchKernelGGL((lora_expand_tiles<T, KIND, NS, true>), grid, dim3(256), 0, s, a);
+            else hipLaunchKernelGGL((lora_expand_tiles<T, KIND, NS, false>), grid, dim3(256), 0, s, a);
+        };
+        constexpr int PER = 4 * kVec<T>;  // ranks of a sum
+        using H = std::integral_constant<int, EXPAND_HELD>;
+        if constexpr (T != T_F32) {
+            if (a.R <= 16) return run(std::integral_constant<int, EXPAND_PACKED>{}, std::integral_constant<int, 1>{});
+        } else {
+            if (a.R <= 16) return run(H{}, std::integral_constant<int, 1>{});
         }
+        if (a.R <= 32) run(H{}, std::integral_constant<int, 32 / PER>{});
+        else if (a.R <= 64) run(H{}, std::integral_constant<int, 64 / PER>{});
+        else if (a.R <= 128) run(H{}, std::integral_constant<int, 128 / PER>{});
+        else run(H{}, std::integral_constant<int, 256 / PER>{});
     }
-    hipLaunchKernelGGL((lora_expand<T, TMB, false>), grid, dim3(256), lds, s, a);
 }
 
 template <int T>
@@ -158,8 +181,8 @@ hipError_t forward(const LoraArgs& g, const ForwardPlan& p, hipStream_t s) {
         if (e != hipSuccess) return e;
     }
     float* P = reinterpret_cast<float*>(ws + p.p_at);
-    const ShrinkArgs sh{g.X, g.ldx, g.A, g.lda, g.sa, g.K, g.R, nullptr, 1.0f, false, P, g.M * g.R, p.kshare, rows, p.tiles};
-    const ExpandArgs ex{P, g.M * g.R, p.planes, g.R, g.B, g.ldb, g.sb, g.N, g.scales, g.alpha, true,
+    const ShrinkArgs sh{g.X, g.ldx, g.A, g.lda, g.sa, g.K, g.R, nullptr, 1.0f, false, P, g.M * lora_pitch(g.R), p.kshare, rows, p.tiles};
+    const ExpandArgs ex{P, g.M * lora_pitch(g.R), p.planes, g.R, g.B, g.ldb, g.sb, g.N, g.scales, g.alpha, true,
                         g.base, g.ldbase, g.Y, g.ldy, g.H, g.ldh, p.nshare, rows, p.tiles};
     if (p.tmb == 1) shrink<T, 1>(sh, p.tiles, p.planes, s), expand<T, 1>(ex, p.tiles, s);
     else shrink<T, 4>(sh, p.tiles, p.planes, s), expand<T, 4>(ex, p.tiles, s);

@@ -12,6 +12,10 @@
 namespace sgemm {
 namespace {
 
+// Floats of a row of a plane of H: R rounded up so that rows are 64-byte pieces,
+// zero past R.
+__host__ __device__ constexpr int lora_pitch(int R) { return (R + 15) / 16 * 16; }
+
 // ---- H = X A^T ----------------------------------------------------------------
 
 struct ShrinkArgs {
@@ -24,7 +28,7 @@ struct ShrinkArgs {
     const float* scales;  // with scaled: the sums times alpha scales[l]
     float alpha;
     bool scaled;
-    float* P;           // planes of M x R, one for each K share
+    float* P;           // planes of M rows of lora_pitch(R) floats, in the order of positions, one for each K share
     int64_t plane;
     int64_t kshare;     // K per grid.y
     RowPlan rows;
@@ -36,7 +40,8 @@ constexpr int kShrinkWaves = 4;
 // A workgroup: a tile of 16 TMB rows, 16 RB of the R columns, a share of K split
 // again over its waves, whose sums are added through LDS.
 template <int T, int RB, int TMB>
-__global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink(ShrinkArgs a) {
+__global__ void __launch_bounds__(64 * kShrinkWaves) __attribute__((amdgpu_waves_per_eu(TMB * RB > 8 ? 2 : 3)))
+lora_shrink(ShrinkArgs a) {
     using E = typename Elem<T>::type;
     constexpr int V = kVec<T>, STEP = 4 * V;  // K of one mma16
     __shared__ float red[2][TMB * RB * 256];
@@ -44,8 +49,6 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink(ShrinkArgs a) {
     const int i = lane & 15, g = lane >> 4;
     const int r0 = blockIdx.z * 16 * RB;
     const int64_t kb = blockIdx.y * a.kshare, ke = kb + a.kshare < a.K ? kb + a.kshare : a.K;
-    // The wave's part: whole double steps, the last wave's shorter.
-    const int64_t part = ((ke - kb + kShrinkWaves - 1) / kShrinkWaves + 2 * STEP - 1) / (2 * STEP) * (2 * STEP);
     for (int64_t t = blockIdx.x; t < a.tiles; t += gridDim.x) {
         const RowTile tile = row_tile(a.rows, t, 16 * TMB);
         if (tile.count == 0) break;       // past the last tile
@@ -67,15 +70,16 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink(ShrinkArgs a) {
         for (int m = 0; m < TMB; m++)
 #pragma unroll
             for (int n = 0; n < RB; n++) acc[m][n] = v4f{0, 0, 0, 0};
-        int64_t k = kb + wave * part;
-        const int64_t end = k + part < ke ? k + part : ke;
         auto step = [&](const u32x4 (&xf)[TMB], const u32x4 (&wf)[RB]) {
 #pragma unroll
             for (int m = 0; m < TMB; m++)
 #pragma unroll
                 for (int n = 0; n < RB; n++) acc[m][n] = mma16<T>(xf[m], wf[n], acc[m][n]);
         };
-        for (; k + 2 * STEP <= end; k += 2 * STEP) {
+        // Double steps are dealt to the waves in turn: together they read 8 STEP
+        // neighbouring elements of each row.
+        int64_t k = kb + wave * 2 * STEP;
+        for (; k + 2 * STEP <= ke; k += kShrinkWaves * 2 * STEP) {
             u32x4 xf[2][TMB], wf[2][RB];
 #pragma unroll
             for (int u = 0; u < 2; u++) {
@@ -87,12 +91,13 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink(ShrinkArgs a) {
             step(xf[0], wf[0]);
             step(xf[1], wf[1]);
         }
-        for (; k < end; k += STEP) {
+        // The wave that the last, shorter double step falls to.
+        for (; k < ke; k += STEP) {
             u32x4 xf[TMB], wf[RB];
 #pragma unroll
-            for (int n = 0; n < RB; n++) wf[n] = load_chunk<T>(w[n], k + g * V, end);
+            for (int n = 0; n < RB; n++) wf[n] = load_chunk<T>(w[n], k + g * V, ke);
 #pragma unroll
-            for (int m = 0; m < TMB; m++) xf[m] = load_chunk<T>(x[m], k + g * V, end);
+            for (int m = 0; m < TMB; m++) xf[m] = load_chunk<T>(x[m], k + g * V, ke);
             step(xf, wf);
         }
         // Waves 2, 3 to 0, 1, then wave 1 to 0.
@@ -117,28 +122,31 @@ __global__ void __launch_bounds__(64 * kShrinkWaves) lora_shrink(ShrinkArgs a) {
         }
         if (wave == 0) {
             const float f = a.scaled ? a.alpha * (a.scales ? a.scales[tile.adapter] : 1.0f) : 1.0f;
-            float* P = a.P + blockIdx.y * a.plane;
+            const int pitch = lora_pitch(a.R);
+            float* P = a.P + blockIdx.y * a.plane + int64_t(tile.start) * pitch;
 #pragma unroll
             for (int m = 0; m < TMB; m++)
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
                     const int p = 16 * m + 4 * g + e;
                     if (p >= tile.count) continue;
-                    float* row = P + int64_t(row_at(a.rows, tile.start + p)) * a.R;
+                    float* row = P + p * pitch;
 #pragma unroll
                     for (int n = 0; n < RB; n++) {
                         const int r = r0 + 16 * n + i;
-                        if (r < a.R) row[r] = a.scaled ? acc[m][n][e] * f : acc[m][n][e];
+                        if (r < pitch) row[r] = r >= a.R ? 0.0f : a.scaled ? acc[m][n][e] * f : acc[m][n][e];
                     }
                 }
         }
     }
 }
 
+enum ExpandKind { EXPAND_PACKED, EXPAND_HELD, EXPAND_LONG };
+
 // ---- Y = base + s H B^T -------------------------------------------------------
 
 struct ExpandArgs {
-    const float* P;     // H: the sum of `planes` planes of rows of R floats
+    const float* P;     // H: the sum of `planes` planes, as ShrinkArgs
     int64_t plane;
     int planes, R;
     const void* W;      // L x N x R
@@ -153,36 +161,138 @@ struct ExpandArgs {
     int64_t ldy;
     float* H;           // also store H here
     int64_t ldh;
-    int64_t nshare;     // N per grid.y, a multiple of 256
+    int64_t nshare;     // N per grid.y, a multiple of 64
     RowPlan rows;
     int64_t tiles;
 };
 
 // LDS of a workgroup: H in the operands' form (two 16-bit parts, or floats) with
 // rows padded by 16 bytes, and a factor for each row.
+__host__ __device__ constexpr int expand_ranks(int R) { return R <= 16 ? 32 : (R + 63) / 64 * 64; }
 template <int T> inline size_t expand_lds(int R, int rows) {
-    const int rp = (R + 31) / 32 * 32;
+    const int rp = expand_ranks(R);
     return size_t(rows) * (T == T_F32 ? (rp + 4) * 4 : 2 * (rp + 8) * 2) + size_t(rows) * 4;
 }
 
-// A workgroup: a tile of 16 TMB rows and a share of N, 64 columns a wave at a
+// The largest of sixteen lanes' values.
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) v = fmaxf(v, __shfl_xor(v, d, 16));
+    return v;
+}
+// 2^(14 - exponent of top); 1 for zero.
+__device__ __forceinline__ float half_factor(float top) {
+    if (!(top > 0.0f)) return 1.0f;
+    int ex = int(__float_as_uint(top) >> 23) - 127;
+    ex = ex < -100 ? -100 : ex;
+    return __uint_as_float(uint32_t(14 - ex + 127) << 23);
+}
+// H in two parts of 16 bits, times up (float16).
+template <int T, int NE>
+__device__ __forceinline__ void split_elements(const float (&v)[NE], float up, uint16_t (&h)[NE], uint16_t (&l)[NE]) {
+#pragma unroll
+    for (int e = 0; e < NE; e++) {
+        if constexpr (T == T_F16) {
+            const float x = v[e] * up;
+            const _Float16 top = _Float16(x);
+            h[e] = __builtin_bit_cast(uint16_t, top);
+            l[e] = __builtin_bit_cast(uint16_t, _Float16(fabsf(x) <= 65504.0f ? x - float(top) : 0.0f));
+        } else {
+            const uint32_t cut = __float_as_uint(v[e]) & 0xFFFF0000u;
+            const bool finite = (cut & 0x7F800000u) != 0x7F800000u;
+            // A NaN whose payload is in the cut bits stays one.
+            h[e] = uint16_t(!finite && v[e] != v[e] ? 0x7FC0u : cut >> 16);
+            l[e] = __builtin_bit_cast(uint16_t, __bf16(finite ? v[e] - __uint_as_float(cut) : 0.0f));
+        }
+    }
+}
+template <int T>
+__device__ __forceinline__ void split_h(const float (&v)[8], float up, u32x4& h, u32x4& l) {
+    uint16_t a[8], b[8];
+    split_elements<T, 8>(v, up, a, b);
+    __builtin_memcpy(&h, a, 16);
+    __builtin_memcpy(&l, b, 16);
+}
+// Elements r .. r + 3 of a row of H in the operands' form.
+template <int T>
+__device__ __forceinline__ void store_h(char* hi, char* lo, int r, v4f v, float up) {
+    if constexpr (T == T_F32) {
+        *reinterpret_cast<v4f*>(hi + r * 4) = v;
+    } else {
+        uint16_t h[4], l[4];
+        const float f[4] = {v[0], v[1], v[2], v[3]};
+        split_elements<T, 4>(f, up, h, l);
+        __builtin_memcpy(hi + r * 2, h, 8);
+        __builtin_memcpy(lo + r * 2, l, 8);
+    }
+}
+
+// A lane's V sums d at columns c .. of a row of N, past whose end nothing is
+// stored; the loop is not unrolled, to keep this rare path small.
+template <int T>
+__device__ __forceinline__ void store_edge(const typename Elem<T>::type* base, typename Elem<T>::type* out, int64_t c,
+                                           int64_t N, bool has, bool add, const float (&d)[kVec<T>]) {
+#pragma unroll 1
+    for (int e = 0; e < kVec<T> && c + e < N; e++) {
+        float x = d[0];
+#pragma unroll
+        for (int z = 1; z < kVec<T>; z++) x = e == z ? d[z] : x;
+        const float b = add ? float(base[c + e]) : 0.0f;
+        out[c + e] = typename Elem<T>::type(!add ? x : has ? b + x : b);
+    }
+}
+
+// Elements r .. of a row of R, zero past its end, without a branch.  ODD: R is
+// no multiple of the 16 bytes' elements, which are then loaded one by one.
+template <int T, bool ODD>
+__device__ __forceinline__ u32x4 load_ranks(const typename Elem<T>::type* row, int r, int R) {
+    u32x4 v;
+    if constexpr (ODD) {
+        typename Elem<T>::type e[kVec<T>];
+#pragma unroll
+        for (int z = 0; z < kVec<T>; z++) e[z] = row[r + z < R ? r + z : 0];
+#pragma unroll
+        for (int z = 0; z < kVec<T>; z++) e[z] = r + z < R ? e[z] : typename Elem<T>::type(0.0f);
+        __builtin_memcpy(&v, e, 16);
+    } else {
+        v = load16(row + (r < R ? r : 0));
+#pragma unroll
+        for (int z = 0; z < 4; z++) v[z] = r < R ? v[z] : 0;
+    }
+    return v;
+}
+
+// A workgroup: 16 TMB rows of a tile and a share of N, 64 columns a wave at a
 // time.  H is rounded to no fewer than 16 bits: for 16-bit types it is the sum
 // of two parts, of bfloat16 cut off and rounded (2^-16 of an element), or of
 // float16 after a power of two for the row that brings its largest element
-// below 2^15 (2^-22, and 2^-39 of that element).  One matrix instruction sums
-// over 32: both parts of up to 16 columns (PACKED), or one part of 32.
-template <int T, int TMB, bool PACKED>
-__global__ void __launch_bounds__(256) lora_expand(ExpandArgs a) {
+// below 2^15 (2^-22, and 2^-39 of that element).  One matrix instruction of a
+// 16-bit type sums over 32: both parts of a rank of up to 16 (PACKED), else one
+// part of 32.  Ranks up to 64 (float: 32) are HELD in registers for all rows of
+// the tile; larger ones are read again, from the caches, for each 16 rows (LONG).
+template <int T, int TMB, int KIND, bool ODD>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TMB > 1 ? 2 : 3)))
+lora_expand(ExpandArgs a) {
     using E = typename Elem<T>::type;
     constexpr int V = kVec<T>, TM = 16 * TMB, STEP = 4 * V;
+    // Operands of the adapter held at a time, for all of the tile's rows unless LONG.
+    constexpr int HELD = KIND == EXPAND_PACKED ? 1 : 2;
+    constexpr int NG = 16 / V;  // groups of V results a lane and 16 rows
     extern __shared__ __attribute__((aligned(16))) char smem[];
-    const int rp = (a.R + 31) / 32 * 32;
+    const int rp = expand_ranks(a.R), steps = rp / STEP;
     const int pitch = T == T_F32 ? (rp + 4) * 4 : (rp + 8) * 2;  // bytes
     char* const hi = smem;
     char* const lo = smem + TM * pitch;  // 16-bit types
     float* const factor = reinterpret_cast<float*>(smem + TM * pitch * (T == T_F32 ? 1 : 2));
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i = lane & 15, g = lane >> 4;
+    const int64_t nb = blockIdx.y * a.nshare, ne = nb + a.nshare < a.N ? nb + a.nshare : a.N;
+    // Columns of a lane's results: group j starts at column n0 + col(j), so that
+    // four lanes' pieces adjoin; and the row of block q that becomes them.
+    auto col = [&](int j) { return T == T_F32 ? 16 * j + 4 * g : 32 * j + 8 * g; };
+    auto w_row = [&](int q) {
+        return T == T_F32 ? 16 * q + i : 32 * (q >> 1) + 8 * (i >> 2) + 4 * (q & 1) + (i & 3);
+    };
     for (int64_t t = blockIdx.x; t < a.tiles; t += gridDim.x) {
         const RowTile tile = row_tile(a.rows, t, TM);
         if (tile.count == 0) break;
@@ -190,154 +300,390 @@ __global__ void __launch_bounds__(256) lora_expand(ExpandArgs a) {
         const bool in_place = a.base == a.Y;
         if (!has && in_place && !a.H) continue;
         const float s = !has || !a.scaled ? 1.0f : a.alpha * (a.scales ? a.scales[tile.adapter] : 1.0f);
-        __syncthreads();
-        // Sixteen lanes a row.
-        for (int p = threadIdx.x >> 4; p < TM; p += 16) {
-            const bool in = p < tile.count;
-            const int64_t row = in ? row_at(a.rows, tile.start + p) : 0;
-            const int c = threadIdx.x & 15;
-            float v[16], top = 0.0f;
-#pragma unroll
-            for (int q = 0; q < 16; q++) {
-                const int r = c + 16 * q;
-                v[q] = 0.0f;
-                if (16 * q < rp) {
-                    if (in && has && r < a.R)
-                        for (int z = 0; z < a.planes; z++) v[q] += a.P[z * a.plane + row * a.R + r];
-                    if (in && r < a.R && a.H && blockIdx.y == 0) a.H[row * a.ldh + r] = v[q];
-                    if (fabsf(v[q]) <= 3.4e38f) top = fmaxf(top, fabsf(v[q]));
-                }
-            }
-            float f = s, up = 1.0f;
-            if constexpr (T == T_F16) {
-#pragma unroll
-                for (int d = 1; d < 16; d *= 2) top = fmaxf(top, __shfl_xor(top, d, 16));
-                // The power that brings the largest finite one into [2^14, 2^15).
-                if (top > 0.0f) {
-                    int ex = int(__float_as_uint(top) >> 23) - 127;
-                    ex = ex < -100 ? -100 : ex;
-                    up = __uint_as_float(uint32_t(14 - ex + 127) << 23);
-                    f = s * __uint_as_float(uint32_t(ex - 14 + 127) << 23);
-                }
-            }
-            if (c == 0) factor[p] = f;
-#pragma unroll
-            for (int q = 0; q < 16; q++) {
-                const int r = c + 16 * q;
-                if (16 * q >= rp) continue;
-                if constexpr (T == T_F32) {
-                    *reinterpret_cast<float*>(hi + p * pitch + r * 4) = v[q];
-                } else if constexpr (T == T_F16) {
-                    const float x = v[q] * up;
-                    const _Float16 h = _Float16(x);
-                    const float d = x - float(h);
-                    *reinterpret_cast<_Float16*>(hi + p * pitch + r * 2) = h;
-                    *reinterpret_cast<_Float16*>(lo + p * pitch + r * 2) = _Float16(fabsf(x) <= 65504.0f ? d : 0.0f);
-                } else {
-                    const uint32_t cut = __float_as_uint(v[q]) & 0xFFFF0000u;
-                    const bool finite = (cut & 0x7F800000u) != 0x7F800000u;
-                    // A NaN whose payload is in the cut bits stays one.
-                    const uint32_t top16 = !finite && v[q] != v[q] ? 0x7FC0u : cut >> 16;
-                    *reinterpret_cast<uint16_t*>(hi + p * pitch + r * 2) = uint16_t(top16);
-                    *reinterpret_cast<__bf16*>(lo + p * pitch + r * 2) = __bf16(finite ? v[q] - __uint_as_float(cut) : 0.0f);
-                }
-            }
-        }
-        __syncthreads();
         const E* const w = static_cast<const E*>(a.W) + (has ? tile.adapter : 0) * a.sw;
-        const int64_t nb = blockIdx.y * a.nshare, ne = nb + a.nshare < a.N ? nb + a.nshare : a.N;
         const E* base[TMB];
         E* out[TMB];
-        float f[TMB];
-        bool in[TMB];
+        bool own[TMB];
 #pragma unroll
         for (int m = 0; m < TMB; m++) {
-            in[m] = 16 * m + i < tile.count;
-            const int64_t row = row_at(a.rows, tile.start + (in[m] ? 16 * m + i : 0));
-            base[m] = a.base ? static_cast<const E*>(a.base) + row * a.ldbase : nullptr;
-            out[m] = static_cast<E*>(a.Y) + row * a.ldy;
-            f[m] = factor[16 * m + i];
+            own[m] = 16 * m + i < tile.count;
+            const int64_t at = row_at(a.rows, tile.start + (own[m] ? 16 * m + i : 0));
+            base[m] = static_cast<const E*>(a.base) + at * a.ldbase;
+            out[m] = static_cast<E*>(a.Y) + at * a.ldy;
         }
-        // Columns of a lane's results: group j of V neighbours starts at column
-        // n0 + col(j), so that four lanes' pieces adjoin.
-        constexpr int NG = 16 / V;  // groups: 4 of 4, or 2 of 8
-        auto col = [&](int j) { return T == T_F32 ? 16 * j + 4 * g : 32 * j + 8 * g; };
-        for (int64_t n0 = nb + wave * 64; n0 < ne; n0 += 256) {
-            u32x4 bq[TMB][NG];
-            const bool whole = n0 + 64 <= a.N;
-            if (whole && a.base) {
+        // What 64 columns take from memory, fetched one turn ahead.
+        struct Turn {
+            u32x4 b[TMB][NG], w[HELD][4];
+        };
+        auto load_w = [&](int64_t n0, int u, Turn& v) {
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const int64_t n = n0 + w_row(q) < a.N ? n0 + w_row(q) : a.N - 1;
+#pragma unroll
+                for (int h = 0; h < HELD; h++) {
+                    const int r = KIND == EXPAND_PACKED ? 8 * (g & 1) : (u + h) * STEP + g * V;
+                    v.w[h][q] = load_ranks<T, ODD>(w + n * a.ldw, r, a.R);
+                }
+            }
+        };
+        auto fetch = [&](int64_t n0, Turn& v) {
+            if (n0 >= ne) return;
+            if (n0 + 64 <= a.N && a.base) {
 #pragma unroll
                 for (int m = 0; m < TMB; m++)
 #pragma unroll
-                    for (int j = 0; j < NG; j++)
-                        if (in[m]) bq[m][j] = load16(base[m] + n0 + col(j));
+                    for (int j = 0; j < NG; j++) v.b[m][j] = load16(base[m] + n0 + col(j));
             }
-            v4f acc[4][TMB];
+            if (has && KIND != EXPAND_LONG) load_w(n0, 0, v);
+        };
+        Turn cur;
+        fetch(nb + wave * 64, cur);
+        __syncthreads();
+        // Sixteen lanes a row, four neighbours of each 64 columns a lane; the loads
+        // of the planes in flight together.
+        const int c = threadIdx.x & 15, hp = lora_pitch(a.R);
+        const float* const P = a.P + int64_t(tile.start) * hp;
+        bool in[TMB];
 #pragma unroll
-            for (int q = 0; q < 4; q++)
+        for (int m = 0; m < TMB; m++) in[m] = 16 * m + int(threadIdx.x >> 4) < tile.count;
+        float top[TMB] = {};
+        for (int pass = 0; pass < (T == T_F16 && rp > 64 ? 2 : 1); pass++) {
+            for (int q0 = 0; q0 < rp; q0 += 64) {
+                const int rq = q0 + 4 * c;
+                v4f v[TMB];
 #pragma unroll
-                for (int m = 0; m < TMB; m++) acc[q][m] = v4f{0, 0, 0, 0};
-            if (has) {
-                const E* wr[4];
+                for (int m = 0; m < TMB; m++) v[m] = v4f{0, 0, 0, 0};
+                if (has && rq < hp) {
+                    // Rows past the tile's repeat its first.
+                    int at[TMB];
 #pragma unroll
-                for (int q = 0; q < 4; q++) {
-                    // Row of block q that becomes the lane's columns above.
-                    const int at = T == T_F32 ? 16 * q + i : 32 * (q >> 1) + 8 * (i >> 2) + 4 * (q & 1) + (i & 3);
-                    const int64_t n = n0 + at < a.N ? n0 + at : a.N - 1;
-                    wr[q] = w + n * a.ldw;
+                    for (int m = 0; m < TMB; m++) at[m] = in[m] ? (16 * m + int(threadIdx.x >> 4)) * hp + rq : rq;
+                    int z = 0;
+                    for (; z + 4 <= a.planes; z += 4) {
+                        v4f q[4][TMB];
+#pragma unroll
+                        for (int y = 0; y < 4; y++)
+#pragma unroll
+                            for (int m = 0; m < TMB; m++)
+                                q[y][m] = *reinterpret_cast<const v4f*>(P + (z + y) * a.plane + at[m]);
+#pragma unroll
+                        for (int y = 0; y < 4; y++)
+#pragma unroll
+                            for (int m = 0; m < TMB; m++) v[m] += q[y][m];
+                    }
+                    for (; z < a.planes; z++)
+#pragma unroll
+                        for (int m = 0; m < TMB; m++)
+                            v[m] += *reinterpret_cast<const v4f*>(P + z * a.plane + at[m]);
                 }
-                const int steps = (a.R + STEP - 1) / STEP;
-                for (int u = 0; u < (PACKED ? 1 : steps); u++) {
-                    u32x4 wf[4];
-                    const int r = PACKED ? 8 * (g & 1) : u * STEP + g * V;
 #pragma unroll
-                    for (int q = 0; q < 4; q++) wf[q] = load_chunk<T>(wr[q], r, a.R);
+                for (int m = 0; m < TMB; m++) {
+                    const int p = 16 * m + (threadIdx.x >> 4);
+                    if (!in[m]) v[m] = v4f{0, 0, 0, 0};
+                    float up = 1.0f;
+                    if constexpr (T == T_F16) {
+                        // The power that brings the row's largest finite element into [2^14, 2^15).
+                        if (pass == 0) {
 #pragma unroll
-                    for (int m = 0; m < TMB; m++) {
-                        const int at = (16 * m + i) * pitch;
-                        if constexpr (PACKED) {
-                            const u32x4 h = *reinterpret_cast<const u32x4*>((g < 2 ? hi : lo) + at + r * 2);
+                            for (int e = 0; e < 4; e++)
+                                if (fabsf(v[m][e]) <= 3.4e38f) top[m] = fmaxf(top[m], fabsf(v[m][e]));
+                            if (rp > 64) continue;
+                        }
+                        // Every lane of the row's sixteen is here.
+                        up = half_factor(group_max(top[m]));
+                    }
+                    if (rq < rp) store_h<T>(hi + p * pitch, lo + p * pitch, rq, v[m], up);
+                    if (a.H && blockIdx.y == 0 && in[m]) {
+                        float* const h = a.H + row_at(a.rows, tile.start + p) * a.ldh;
 #pragma unroll
-                            for (int q = 0; q < 4; q++) acc[q][m] = mma16<T>(wf[q], h, acc[q][m]);
-                        } else {
-                            const u32x4 h = *reinterpret_cast<const u32x4*>(hi + at + r * int(sizeof(E)));
+                        for (int e = 0; e < 4; e++)
+                            if (rq + e < a.R) h[rq + e] = v[m][e];
+                    }
+                }
+            }
+        }
+        if (c == 0)
 #pragma unroll
-                            for (int q = 0; q < 4; q++) acc[q][m] = mma16<T>(wf[q], h, acc[q][m]);
-                            if constexpr (T != T_F32) {
-                                const u32x4 l = *reinterpret_cast<const u32x4*>(lo + at + r * 2);
+            for (int m = 0; m < TMB; m++) factor[16 * m + (threadIdx.x >> 4)] = s;
+        if constexpr (T == T_F16) {
 #pragma unroll
-                                for (int q = 0; q < 4; q++) acc[q][m] = mma16<T>(wf[q], l, acc[q][m]);
+            for (int m = 0; m < TMB; m++) {
+                const float up = half_factor(group_max(top[m]));
+                if (c == 0) factor[16 * m + (threadIdx.x >> 4)] = s / up;
+            }
+        }
+        __syncthreads();
+        float f[TMB];
+#pragma unroll
+        for (int m = 0; m < TMB; m++) f[m] = factor[16 * m + i];
+        for (int64_t n0 = nb + wave * 64; n0 < ne; n0 += 256) {
+            Turn next;
+            fetch(n0 + 256, next);
+            const bool whole = n0 + 64 <= a.N;
+#pragma unroll
+            for (int m = 0; m < TMB; m++) {
+                v4f acc[4];
+#pragma unroll
+                for (int q = 0; q < 4; q++) acc[q] = v4f{0, 0, 0, 0};
+                if (has) {
+                    const int at = (16 * m + i) * pitch;
+                    for (int u = 0; u < (KIND == EXPAND_LONG ? steps : 1); u += HELD) {
+                        if constexpr (KIND == EXPAND_LONG) load_w(n0, u, cur);
+#pragma unroll
+                        for (int h = 0; h < HELD; h++) {
+                            const int r = KIND == EXPAND_PACKED ? 8 * (g & 1) : (u + h) * STEP + g * V;
+                            const char* const from = KIND == EXPAND_PACKED && g >= 2 ? lo : hi;
+                            const u32x4 x = *reinterpret_cast<const u32x4*>(from + at + r * int(sizeof(E)));
+#pragma unroll
+                            for (int q = 0; q < 4; q++) acc[q] = mma16<T>(cur.w[h][q], x, acc[q]);
+                            if constexpr (T != T_F32 && KIND != EXPAND_PACKED) {
+                                const u32x4 y = *reinterpret_cast<const u32x4*>(lo + at + r * 2);
+#pragma unroll
+                                for (int q = 0; q < 4; q++) acc[q] = mma16<T>(cur.w[h][q], y, acc[q]);
                             }
                         }
                     }
                 }
-            }
-#pragma unroll
-            for (int m = 0; m < TMB; m++) {
-                if (!in[m]) continue;
+                if (!own[m]) continue;
 #pragma unroll
                 for (int j = 0; j < NG; j++) {
                     float d[V], b[V];
 #pragma unroll
-                    for (int e = 0; e < V; e++) d[e] = f[m] * acc[j * V / 4 + e / 4][m][e % 4];
+                    for (int e = 0; e < V; e++) d[e] = f[m] * acc[j * V / 4 + e / 4][e % 4];
                     const int64_t c = n0 + col(j);
                     if (whole) {
                         if (a.base) {
-                            unpack<T>(bq[m][j], b);
+                            unpack<T>(cur.b[m][j], b);
 #pragma unroll
                             for (int e = 0; e < V; e++) d[e] = has ? b[e] + d[e] : b[e];
                         }
                         store16(out[m] + c, pack<T>(d));
                     } else {
-#pragma unroll
-                        for (int e = 0; e < V; e++)
-                            if (c + e < a.N) {
-                                const float b1 = a.base ? float(base[m][c + e]) : 0.0f;
-                                out[m][c + e] = E(!a.base ? d[e] : has ? b1 + d[e] : b1);
-                            }
+                        store_edge<T>(base[m], out[m], c, a.N, has, a.base != nullptr, d);
                     }
                 }
             }
+            cur = next;
+        }
+    }
+}
+
+// The same for tiles of many rows: a workgroup takes 64 rows and a share of N,
+// each wave 16 of the rows, with their H in registers (in two parts, as above)
+// for the whole of it.  64 columns of the adapter are staged in LDS for the four
+// waves, up to 64 ranks at a time, while the ones before are multiplied: read
+// from memory by each wave for itself (into registers), they passed through the L1
+// four times and took as long as base and Y (8192 x 8192 of rank 64: 97 us).
+// NS: matrix instructions' sums of one part that R takes.
+template <int T, int KIND, int NS, bool ODD>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(NS * kVec<T> <= 16 ? 4 : NS * kVec<T> <= 32 ? 2 : 1)))
+lora_expand_tiles(ExpandArgs a) {
+    using E = typename Elem<T>::type;
+    constexpr bool PACKED = KIND == EXPAND_PACKED;
+    constexpr int V = kVec<T>, STEP = 4 * V, NG = 16 / V;
+    constexpr int CHUNK = PACKED ? 1 : NS < 64 / STEP ? NS : 64 / STEP;  // sums staged at a time
+    constexpr int ROW = PACKED ? 16 : CHUNK * STEP;                      // ranks of those
+    constexpr int PITCH = ROW * int(sizeof(E)) + 16;                     // bytes of a staged row
+    constexpr int PIECES = ROW / V * 64 / 256 > 0 ? ROW / V * 64 / 256 : 1;
+    constexpr int CHUNKS = PACKED ? 1 : NS / CHUNK;
+    constexpr int AHEAD = 2;
+    __shared__ __attribute__((aligned(16))) char stage[2][64 * PITCH];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int i = lane & 15, g = lane >> 4;
+    const int64_t nb = blockIdx.y * a.nshare, ne = nb + a.nshare < a.N ? nb + a.nshare : a.N;
+    auto col = [&](int j) { return T == T_F32 ? 16 * j + 4 * g : 32 * j + 8 * g; };
+    auto w_row = [&](int q) {
+        return T == T_F32 ? 16 * q + i : 32 * (q >> 1) + 8 * (i >> 2) + 4 * (q & 1) + (i & 3);
+    };
+    for (int64_t t = blockIdx.x; t < a.tiles; t += gridDim.x) {
+        const RowTile tile = row_tile(a.rows, t, 64);
+        if (tile.count == 0) break;
+        const bool has = tile.adapter >= 0;
+        if (!has && a.base == a.Y && !a.H) continue;
+        const float s = !has || !a.scaled ? 1.0f : a.alpha * (a.scales ? a.scales[tile.adapter] : 1.0f);
+        const E* const w = static_cast<const E*>(a.W) + (has ? tile.adapter : 0) * a.sw;
+        const int p = 16 * wave + i;
+        const bool own = p < tile.count;
+        const int64_t row = row_at(a.rows, tile.start + (own ? p : 0));
+        const E* const base = static_cast<const E*>(a.base) + row * a.ldbase;
+        E* const out = static_cast<E*>(a.Y) + row * a.ldy;
+        const int turns = int((ne - nb + 63) / 64);
+        // Sixteen bytes of the adapter's columns n0 .., chunk ch, for LDS; past R they
+        // are zeroed only when they are put there, as that waits for them.
+        u32x4 piece[PIECES];
+        auto fetch_w = [&](int64_t n0, int ch) {
+#pragma unroll
+            for (int q = 0; q < PIECES; q++) {
+                const int e = threadIdx.x + 256 * q, n = e / (ROW / V) & 63, r = ch * ROW + e % (ROW / V) * V;
+                const int64_t at = n0 + n < a.N ? n0 + n : a.N - 1;
+                if constexpr (ODD) piece[q] = load_ranks<T, true>(w + at * a.ldw, r, a.R);
+                else piece[q] = load16(w + at * a.ldw + (r < a.R ? r : 0));
+            }
+        };
+        auto put_w = [&](char* to, int ch) {
+#pragma unroll
+            for (int q = 0; q < PIECES; q++) {
+                const int e = threadIdx.x + 256 * q, n = e / (ROW / V), c = e % (ROW / V);
+                u32x4 v = piece[q];
+#pragma unroll
+                for (int z = 0; z < 4; z++) v[z] = ODD || ch * ROW + c * V < a.R ? v[z] : 0;
+                if (64 * (ROW / V) >= 256 || n < 64) *reinterpret_cast<u32x4*>(to + n * PITCH + 16 * c) = v;
+            }
+        };
+        // base, AHEAD turns of 64 columns in flight.  Where there is less to fetch the
+        // last columns are fetched again: a wait can then be for all but so many loads.
+        const bool wide = a.base != nullptr && a.N >= 64;
+        u32x4 b[AHEAD][NG];
+        auto fetch_base = [&](int turn, int slot) {
+            const int64_t n0 = nb + 64 * int64_t(turn);
+            const E* const from = base + (n0 + 64 <= a.N ? n0 : a.N - 64);
+#pragma unroll
+            for (int j = 0; j < NG; j++) b[slot][j] = load16(from + col(j));
+        };
+        if (has && turns > 0) fetch_w(nb, 0);
+        if (wide && turns > 0)
+#pragma unroll
+            for (int slot = 0; slot < AHEAD; slot++) fetch_base(slot, slot);
+        // H: the lane's V ranks of each sum, all planes.
+        const int hp = lora_pitch(a.R);
+        u32x4 hi[NS], lo[T == T_F32 || PACKED ? 1 : NS];
+        float f = s;
+        {
+            const float* const P = a.P + int64_t(tile.start + (own ? p : 0)) * hp;
+            float v[NS][V];
+#pragma unroll
+            for (int u = 0; u < NS; u++) {
+#pragma unroll
+                for (int e = 0; e < V; e++) v[u][e] = 0.0f;
+            }
+            if (has)
+                for (int z = 0; z < a.planes; z++) {
+                    v4f x[NS][V / 4];
+#pragma unroll
+                    for (int u = 0; u < NS; u++) {
+                        const int r = PACKED ? 8 * (g & 1) : u * STEP + g * V;
+#pragma unroll
+                        for (int e = 0; e < V; e += 4)
+                            x[u][e / 4] = *reinterpret_cast<const v4f*>(P + z * a.plane + (r + e < hp ? r + e : 0));
+                    }
+#pragma unroll
+                    for (int u = 0; u < NS; u++)
+#pragma unroll
+                        for (int e = 0; e < V; e++) v[u][e] += x[u][e / 4][e % 4];
+                }
+#pragma unroll
+            for (int u = 0; u < NS; u++) {
+                const int r = PACKED ? 8 * (g & 1) : u * STEP + g * V;
+#pragma unroll
+                for (int e = 0; e < V; e++)
+                    if (!own || r + e >= a.R) v[u][e] = 0.0f;
+                if (a.H && blockIdx.y == 0 && own && (!PACKED || g < 2))
+#pragma unroll
+                    for (int e = 0; e < V; e++)
+                        if (r + e < a.R) a.H[row * a.ldh + r + e] = v[u][e];
+            }
+            float up = 1.0f;
+            if constexpr (T == T_F16) {
+                float top = 0.0f;
+#pragma unroll
+                for (int u = 0; u < NS; u++)
+#pragma unroll
+                    for (int e = 0; e < V; e++)
+                        if (fabsf(v[u][e]) <= 3.4e38f) top = fmaxf(top, fabsf(v[u][e]));
+                top = fmaxf(top, __shfl_xor(top, 16));
+                up = half_factor(fmaxf(top, __shfl_xor(top, 32)));
+                f = s / up;
+            }
+#pragma unroll
+            for (int u = 0; u < NS; u++) {
+                u32x4 h, l = {0, 0, 0, 0};
+                if constexpr (T == T_F32) h = pack<T>(v[u]);
+                else split_h<T>(v[u], up, h, l);
+                if constexpr (PACKED) {
+#pragma unroll
+                    for (int y = 0; y < 4; y++) hi[u][y] = g < 2 ? h[y] : l[y];
+                } else {
+                    hi[u] = h;
+                    if constexpr (T != T_F32) lo[u] = l;
+                }
+            }
+        }
+        int half = 0;
+        __syncthreads();  // the tile before is done with LDS
+        // One turn's sums, for the lane's row.
+        auto multiply = [&](int64_t n0, v4f (&acc)[4]) {
+#pragma unroll
+            for (int q = 0; q < 4; q++) acc[q] = v4f{0, 0, 0, 0};
+#pragma unroll
+            for (int ch = 0; ch < CHUNKS; ch++) {
+                char* const st = stage[half];
+                half ^= 1;
+                put_w(st, ch);
+                __syncthreads();
+                if (ch + 1 < CHUNKS) fetch_w(n0, ch + 1);
+                else fetch_w(n0 + 64, 0);
+#pragma unroll
+                for (int u = 0; u < CHUNK; u++) {
+                    const int c = PACKED ? 16 * (g & 1) : (u * 4 + g) * 16;
+#pragma unroll
+                    for (int q = 0; q < 4; q++) {
+                        const u32x4 x = *reinterpret_cast<const u32x4*>(st + w_row(q) * PITCH + c);
+                        acc[q] = mma16<T>(x, hi[ch * CHUNK + u], acc[q]);
+                        if constexpr (T != T_F32 && !PACKED) acc[q] = mma16<T>(x, lo[ch * CHUNK + u], acc[q]);
+                    }
+                }
+            }
+        };
+        const int full = int(((ne < a.N ? ne : a.N) - nb) / 64);  // turns of whole 64 columns
+        auto columns = [&](auto with_h, auto with_base) {
+            constexpr bool HAS = decltype(with_h)::value, WIDE = decltype(with_base)::value;
+            for (int turn4 = 0; turn4 < full; turn4 += AHEAD)
+#pragma unroll
+                for (int slot = 0; slot < AHEAD; slot++) {
+                    const int turn = turn4 + slot;
+                    if (turn >= full) break;
+                    const int64_t n0 = nb + 64 * int64_t(turn);
+                    v4f acc[4];
+                    if constexpr (HAS) multiply(n0, acc);
+                    u32x4 y[NG];
+#pragma unroll
+                    for (int j = 0; j < NG; j++) {
+                        float d[V], x[V];
+#pragma unroll
+                        for (int e = 0; e < V; e++) d[e] = HAS ? f * acc[j * V / 4 + e / 4][e % 4] : 0.0f;
+                        if constexpr (WIDE) {
+                            unpack<T>(b[slot][j], x);
+#pragma unroll
+                            for (int e = 0; e < V; e++) d[e] = HAS ? x[e] + d[e] : x[e];
+                        }
+                        y[j] = pack<T>(d);
+                    }
+                    // Before the stores: the wait for these then does not wait for those.
+                    if constexpr (WIDE) fetch_base(turn + AHEAD, slot);
+                    asm volatile("" ::: "memory");
+                    if (own)
+#pragma unroll
+                        for (int j = 0; j < NG; j++) store16(out + n0 + col(j), y[j]);
+                }
+        };
+        if (has && wide) columns(std::true_type{}, std::true_type{});
+        else if (has) columns(std::true_type{}, std::false_type{});
+        else if (wide) columns(std::false_type{}, std::true_type{});
+        else columns(std::false_type{}, std::false_type{});
+        if (full < turns) {  // columns up to N
+            const int64_t n0 = nb + 64 * int64_t(full);
+            v4f acc[4] = {};
+            if (has) multiply(n0, acc);
+            if (own)
+#pragma unroll
+                for (int j = 0; j < NG; j++)
+#pragma unroll
+                    for (int e = 0; e < V; e++) {
+                        const int64_t c = n0 + col(j) + e;
+                        if (c >= a.N) continue;
+                        const float d = f * acc[j * V / 4 + e / 4][e % 4];
+                        out[c] = E(!a.base ? (has ? d : 0.0f) : has ? float(base[c]) + d : float(base[c]));
+                    }
         }
     }
 }

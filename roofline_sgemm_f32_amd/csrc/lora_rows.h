@@ -36,16 +36,19 @@ struct RowPlan {
 };
 
 __device__ __forceinline__ int adapter_of(const void* ids, bool id64, int L, int64_t m) {
-    const int64_t id = id64 ? static_cast<const int64_t*>(ids)[m] : static_cast<const int32_t*>(ids)[m];
-    return id >= 0 && id < L ? int(id) : -1;
+    // An int64 as its two halves, so that both types are loads without a branch.
+    const uint32_t* const p = static_cast<const uint32_t*>(ids) + (id64 ? 2 * m : m);
+    const uint32_t lo = p[0], hi = p[id64 ? 1 : 0];
+    return lo < uint32_t(L) && (!id64 || hi == 0) ? int(lo) : -1;
 }
 
 // Tile t of `size` rows; count 0 past the last.
 __device__ __forceinline__ RowTile row_tile(const RowPlan& p, int64_t t, int size) {
     if (p.mode == RowPlan::SORTED) {
-        if (t >= p.head[0]) return {-1, 0, 0};
-        const int* at = p.head + 4 + 4 * t;
-        return {at[0], at[1], at[2]};
+        const int n = p.head[0];
+        const int4 at = reinterpret_cast<const int4*>(p.head)[1 + t];  // in bounds, of no meaning past the last
+        return {__builtin_amdgcn_readfirstlane(at.x), __builtin_amdgcn_readfirstlane(at.y),
+                t < n ? __builtin_amdgcn_readfirstlane(at.z) : 0};
     }
     if (p.mode == RowPlan::SINGLE) return {adapter_of(p.ids, p.id64, p.L, t), int(t), 1};
     const int64_t start = t * size;
@@ -68,11 +71,19 @@ __device__ __forceinline__ void store16(void* p, u32x4 v) { __builtin_memcpy(p, 
 template <int T>
 __device__ __forceinline__ u32x4 load_chunk(const typename Elem<T>::type* row, int64_t i, int64_t n) {
     if (i + kVec<T> <= n) return load16(row + i);
-    typename Elem<T>::type v[kVec<T>];
+    u32x4 r = {0, 0, 0, 0};
+#pragma unroll 1
+    for (int e = 0; i + e < n; e++) {
+        if constexpr (T == T_F32) {
+            const uint32_t w = __float_as_uint(row[i + e]);
 #pragma unroll
-    for (int e = 0; e < kVec<T>; e++) v[e] = i + e < n ? row[i + e] : typename Elem<T>::type(0.0f);
-    u32x4 r;
-    __builtin_memcpy(&r, v, 16);
+            for (int q = 0; q < 4; q++) r[q] = q == e ? w : r[q];
+        } else {
+            const uint32_t w = uint32_t(__builtin_bit_cast(uint16_t, row[i + e])) << (16 * (e & 1));
+#pragma unroll
+            for (int q = 0; q < 4; q++) r[q] = q == e / 2 ? r[q] | w : r[q];
+        }
+    }
     return r;
 }
 

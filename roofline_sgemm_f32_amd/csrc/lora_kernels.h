@@ -476,7 +476,7 @@ lora_expand(ExpandArgs a) {
 // four times and took as long as base and Y (8192 x 8192 of rank 64: 97 us).
 // NS: matrix instructions' sums of one part that R takes.
 template <int T, int KIND, int NS, bool ODD>
-__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(NS * kVec<T> <= 16 ? 4 : NS * kVec<T> <= 32 ? 2 : 1)))
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(T == T_F32 ? (NS <= 2 ? 3 : NS <= 8 ? 2 : 1) : (NS <= 2 ? 4 : NS <= 4 ? 2 : 1))))
 lora_expand_tiles(ExpandArgs a) {
     using E = typename Elem<T>::type;
     constexpr bool PACKED = KIND == EXPAND_PACKED;

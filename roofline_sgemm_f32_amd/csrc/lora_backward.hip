@@ -1,0 +1,438 @@
+// Gradients of low-rank adapters:
+//   dH[m] = s_l dY[m] B_l,  dX[m] = base[m] + dH[m] A_l      (l = ids[m])
+//   dA_l = sum dH[m]^T X[m],  dB_l = s_l sum dY[m]^T H[m]     (over l's rows m)
+// The first two are the forward pass's products with the adapters transposed
+// (a copy of them, small beside the rows).  The others are sums over rows: each
+// chunk of an adapter's rows gives a partial sum, and these are added in order.
+#include "lora.h"
+
+namespace sgemm {
+namespace {
+
+// ---- transposed adapters --------------------------------------------------------
+
+struct TurnArgs {
+    const void* W;  // L matrices of rows x cols
+    int64_t ldw, sw;
+    int64_t rows, cols;
+    void* out;      // L matrices of cols x pitch, zero past `rows`
+    int64_t pitch;
+    int64_t tiles_r, tiles_c;
+};
+
+// A 64 x 64 tile a workgroup.
+template <typename E>
+__device__ void turn_tile(const TurnArgs& a, int64_t t) {
+    __shared__ E tile[64][64 + 4 / sizeof(E)];
+    const int64_t l = t / (a.tiles_r * a.tiles_c), q = t % (a.tiles_r * a.tiles_c);
+    const int64_t r0 = q / a.tiles_c * 64, c0 = q % a.tiles_c * 64;
+    const E* const w = static_cast<const E*>(a.W) + l * a.sw;
+    for (int e = threadIdx.x; e < 4096; e += 256) {
+        const int64_t r = r0 + e / 64, c = c0 + e % 64;
+        tile[e / 64][e % 64] = r < a.rows && c < a.cols ? w[r * a.ldw + c] : E(0);
+    }
+    __syncthreads();
+    E* const out = static_cast<E*>(a.out) + l * a.cols * a.pitch;
+    for (int e = threadIdx.x; e < 4096; e += 256) {
+        const int64_t c = c0 + e / 64, r = r0 + e % 64;
+        if (c < a.cols && r < a.pitch) out[c * a.pitch + r] = tile[e % 64][e / 64];
+    }
+    __syncthreads();
+}
+
+template <typename E>
+__global__ void __launch_bounds__(256) lora_turn(TurnArgs a, TurnArgs b, int64_t tiles_a, int64_t tiles) {
+    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+        if (t < tiles_a) turn_tile<E>(a, t);
+        else turn_tile<E>(b, t - tiles_a);
+    }
+}
+
+// ---- sums over rows ----------------------------------------------------------------
+
+// One of the two gradients: W[r, c] = sum over rows m of V[m, r] Z[m, c].
+struct SideArgs {
+    const void* Z;        // M rows of C elements
+    int64_t ldz, C;
+    const float* V;       // by_position: planes in the order of positions, else rows
+    int64_t ldv, plane;
+    int planes;
+    bool by_position;
+    float* partial;       // slots of R x C
+    void* out;            // an adapter's only chunk: R x C, or C x R (turned), times the scale
+    int64_t ldo, so;
+    bool turned;
+    const float* scales;  // with scaled
+    float alpha;
+    bool scaled;
+    int64_t groups;       // column groups
+};
+
+struct WeightArgs {
+    SideArgs side[2];
+    int R, chunk;
+    RowPlan rows;         // of chunks
+    int64_t chunks;       // at most
+    const int* slot_start;  // SORTED; else: chunks, if more than one
+    const int* chunk_start;
+};
+
+constexpr int kWeightRows = 64;  // of V in LDS at a time
+
+template <int T> constexpr int kGroupCols = T == T_F32 ? 64 : 128;  // columns of a wave
+
+// The slot of a chunk's partial sum, or -1: it is the adapter's only one.
+__device__ __forceinline__ int64_t slot_of(const WeightArgs& a, const RowTile& t) {
+    if (a.rows.mode != RowPlan::SORTED) return a.rows.M > a.chunk ? t.place : -1;
+    const int first = a.slot_start[t.adapter];
+    return a.slot_start[t.adapter + 1] > first ? first + t.place : -1;
+}
+
+// 2^(14 - exponent of top); 1 for zero.
+__device__ __forceinline__ float half_power(float top) {
+    if (!(top > 0.0f)) return 1.0f;
+    int ex = int(__float_as_uint(top) >> 23) - 127;
+    ex = ex < -100 ? -100 : ex;
+    return __uint_as_float(uint32_t(14 - ex + 127) << 23);
+}
+
+// A workgroup: a chunk of an adapter's rows, four waves' column groups, 16 RB of
+// the ranks.  The sum of a matrix instruction runs over rows, so its operands
+// hold 8 rows of one column (16-bit types: a lane's 8 rows x 8 columns, 16 bytes a
+// row, are turned in registers, two rows by one byte permutation), or one row
+// (float).  V is in two 16-bit parts, as in the forward pass; for float16 after a
+// power of two for each rank that brings the chunk's largest into [2^14, 2^15).
+// NARROW: fewer columns than a lane's on either side.
+template <int T, int RB, bool NARROW>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) lora_weights(WeightArgs a) {
+    using E = typename Elem<T>::type;
+    constexpr int V = kVec<T>, COLS = kGroupCols<T>, RN = 16 * RB;
+    constexpr int VP = kWeightRows + 8;  // 16-bit: rows of a rank, padded
+    __shared__ __attribute__((aligned(16))) char vs[T == T_F32 ? kWeightRows * RN * 4 : 2 * RN * VP * 2];
+    __shared__ int row_of[kWeightRows];
+    __shared__ uint32_t top[RN];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int i = lane & 15, g = lane >> 4;
+    const int r0 = blockIdx.z * RN;
+    const int64_t groups = a.side[0].groups + a.side[1].groups;
+    for (int64_t t = blockIdx.x; t < a.chunks * groups; t += gridDim.x) {
+        const RowTile tile = row_tile(a.rows, t / groups, a.chunk);
+        if (tile.count == 0) break;
+        const bool second = t % groups >= a.side[0].groups;
+        const SideArgs& sd = a.side[second];
+        const int64_t c0 = ((second ? t % groups - a.side[0].groups : t % groups) * 4 + wave) * COLS;
+        // The lane's columns.  Past the last they are the last ones again, so that the
+        // loads need no check: two lanes then find, and store, the same sums.
+        const int64_t c = NARROW || c0 + i * V + V <= sd.C ? c0 + i * V : sd.C - V;
+        const float s = sd.scaled ? sd.alpha * (sd.scales ? sd.scales[tile.adapter] : 1.0f) : 1.0f;
+        // Element (position p, rank r0 + r) of V.
+        auto v_at = [&](int p, int r) {
+            if (r0 + r >= a.R || p >= tile.count) return 0.0f;
+            if (!sd.by_position) return sd.V[int64_t(row_at(a.rows, tile.start + p)) * sd.ldv + r0 + r];
+            float v = 0.0f;
+            for (int z = 0; z < sd.planes; z++) v += sd.V[z * sd.plane + int64_t(tile.start + p) * sd.ldv + r0 + r];
+            return v;
+        };
+        if constexpr (T == T_F16) {
+            __syncthreads();
+            if (threadIdx.x < RN) top[threadIdx.x] = 0;
+            __syncthreads();
+            for (int e = threadIdx.x; e < tile.count * RN; e += 256) {
+                const float v = fabsf(v_at(e / RN, e % RN));
+                if (v <= 3.4e38f) atomicMax(&top[e % RN], __float_as_uint(v));  // a maximum has no order
+            }
+        }
+        v4f acc[V][RB];
+#pragma unroll
+        for (int e = 0; e < V; e++)
+#pragma unroll
+            for (int n = 0; n < RB; n++) acc[e][n] = v4f{0, 0, 0, 0};
+        for (int p0 = 0; p0 < tile.count; p0 += kWeightRows) {
+            __syncthreads();
+            for (int e = threadIdx.x; e < kWeightRows * RN; e += 256) {
+                const int p = e / RN, r = e % RN;
+                const float v = v_at(p0 + p, r);
+                if constexpr (T == T_F32) {
+                    reinterpret_cast<float*>(vs)[p * RN + r] = v;
+                } else {
+                    uint16_t* const at = reinterpret_cast<uint16_t*>(vs) + r * VP + p;
+                    if constexpr (T == T_F16) {
+                        const float x = v * half_power(__uint_as_float(top[r]));
+                        const _Float16 h = _Float16(x);
+                        at[0] = __builtin_bit_cast(uint16_t, h);
+                        at[RN * VP] = __builtin_bit_cast(uint16_t, _Float16(fabsf(x) <= 65504.0f ? x - float(h) : 0.0f));
+                    } else {
+                        const uint32_t cut = __float_as_uint(v) & 0xFFFF0000u;
+                        const bool finite = (cut & 0x7F800000u) != 0x7F800000u;
+                        at[0] = uint16_t(!finite && v != v ? 0x7FC0u : cut >> 16);
+                        at[RN * VP] = __builtin_bit_cast(uint16_t, __bf16(finite ? v - __uint_as_float(cut) : 0.0f));
+                    }
+                }
+            }
+            if (threadIdx.x < kWeightRows) {
+                const int p = p0 + threadIdx.x;
+                row_of[threadIdx.x] = row_at(a.rows, tile.start + (p < tile.count ? p : 0));
+            }
+            __syncthreads();
+            if (c0 >= sd.C) continue;
+            const int left = tile.count - p0 < kWeightRows ? tile.count - p0 : kWeightRows;
+            // Rows past the chunk repeat its first, and are zeroed: what other adapters'
+            // rows hold must not meet a zero of V.
+            auto load_z = [&](int p) {
+                const E* const row = static_cast<const E*>(sd.Z) + int64_t(row_of[p]) * sd.ldz;
+                u32x4 z;
+                if constexpr (NARROW) z = load_chunk<T>(row, c, sd.C);
+                else z = load16(row + c);
+                if (p >= left) z = u32x4{0, 0, 0, 0};
+                return z;
+            };
+            if constexpr (T == T_F32) {
+#pragma unroll 4
+                for (int q = 0; q < kWeightRows / 4; q++) {
+                    if (4 * q >= left) break;
+                    const u32x4 z = load_z(4 * q + g);
+#pragma unroll
+                    for (int n = 0; n < RB; n++) {
+                        const float v = reinterpret_cast<const float*>(vs)[(4 * q + g) * RN + 16 * n + i];
+#pragma unroll
+                        for (int e = 0; e < V; e++)
+                            acc[e][n] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, __uint_as_float(z[e]), acc[e][n], 0, 0, 0);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < kWeightRows / 32; q++) {
+                    if (32 * q >= left) break;
+                    u32x4 z[8];
+#pragma unroll
+                    for (int y = 0; y < 8; y++) z[y] = load_z(32 * q + 8 * g + y);
+                    u32x4 hi[RB], lo[RB];
+#pragma unroll
+                    for (int n = 0; n < RB; n++) {
+                        const char* const at = vs + ((16 * n + i) * VP + 32 * q + 8 * g) * 2;
+                        hi[n] = *reinterpret_cast<const u32x4*>(at);
+                        lo[n] = *reinterpret_cast<const u32x4*>(at + RN * VP * 2);
+                    }
+#pragma unroll
+                    for (int e = 0; e < V; e++) {
+                        u32x4 x;  // column e of the lane's 8 x 8
+#pragma unroll
+                        for (int y = 0; y < 4; y++)
+                            x[y] = __builtin_amdgcn_perm(z[2 * y + 1][e / 2], z[2 * y][e / 2], e % 2 ? 0x07060302u : 0x05040100u);
+#pragma unroll
+                        for (int n = 0; n < RB; n++) {
+                            acc[e][n] = mma16<T>(hi[n], x, acc[e][n]);
+                            acc[e][n] = mma16<T>(lo[n], x, acc[e][n]);
+                        }
+                    }
+                }
+            }
+        }
+        if (c0 >= sd.C) continue;
+        // The lane has ranks 4 g .. 4 g + 3 of each 16 at its V columns.
+        const int64_t slot = slot_of(a, tile);
+#pragma unroll
+        for (int n = 0; n < RB; n++)
+#pragma unroll
+            for (int y = 0; y < 4; y++) {
+                const int r = 16 * n + 4 * g + y;
+                if (r0 + r >= a.R) continue;
+                float f = s;
+                if constexpr (T == T_F16) f = s / half_power(__uint_as_float(top[r]));
+                if (slot >= 0) {
+                    float* const at = sd.partial + (slot * a.R + r0 + r) * sd.C + c;
+#pragma unroll
+                    for (int e = 0; e < V; e += 4) {
+                        const v4f w = {acc[e][n][y] * f, acc[e + 1][n][y] * f, acc[e + 2][n][y] * f, acc[e + 3][n][y] * f};
+                        if constexpr (!NARROW) __builtin_memcpy(at + e, &w, 16);
+                        else
+#pragma unroll
+                            for (int q = 0; q < 4; q++)
+                                if (c + e + q < sd.C) at[e + q] = w[q];
+                    }
+                } else {
+                    E* const out = static_cast<E*>(sd.out) + tile.adapter * sd.so;
+#pragma unroll
+                    for (int e = 0; e < V; e++)
+                        if (!NARROW || c + e < sd.C)
+                            out[sd.turned ? (c + e) * sd.ldo + r0 + r : (r0 + r) * sd.ldo + c + e] = E(acc[e][n][y] * f);
+                }
+            }
+    }
+}
+
+// The partial sums of an adapter added, in order, and zeros where no row has it: 64
+// x 64 of (rank, column) a workgroup.
+template <int T>
+__global__ void __launch_bounds__(256) lora_weights_sum(WeightArgs a, int64_t tiles0, int64_t tiles) {
+    using E = typename Elem<T>::type;
+    __shared__ float part[64][65];
+    const int rt = (a.R + 63) / 64;
+    for (int64_t t0 = blockIdx.x; t0 < tiles; t0 += gridDim.x) {
+        const bool second = t0 >= tiles0;
+        const SideArgs& sd = a.side[second];
+        const int64_t t = second ? t0 - tiles0 : t0, ct = (sd.C + 63) / 64;
+        const int l = int(t / (rt * ct));
+        const int r0 = int(t / ct % rt) * 64;
+        const int64_t c0 = t % ct * 64;
+        int64_t first, last;
+        bool some;
+        if (a.rows.mode == RowPlan::SORTED) {
+            first = a.slot_start[l], last = a.slot_start[l + 1];
+            some = a.chunk_start[l + 1] > a.chunk_start[l];
+        } else {
+            some = a.rows.M > 0 && l == 0;
+            first = 0, last = some && a.rows.M > a.chunk ? (a.rows.M + a.chunk - 1) / a.chunk : 0;
+        }
+        if (some && first == last) continue;  // written by its only chunk
+        __syncthreads();
+#pragma unroll 4
+        for (int e = threadIdx.x; e < 4096; e += 256) {
+            const int r = e / 64, cc = e % 64;
+            if (r0 + r >= a.R || c0 + cc >= sd.C) continue;
+            float v = 0.0f;
+            const float* at = sd.partial + (first * a.R + r0 + r) * sd.C + c0 + cc;
+#pragma unroll 4
+            for (int64_t q = first; q < last; q++, at += int64_t(a.R) * sd.C) v += *at;
+            if (sd.turned) part[cc][r] = v;
+            else (static_cast<E*>(sd.out) + l * sd.so)[(r0 + r) * sd.ldo + c0 + cc] = E(v);
+        }
+        if (!sd.turned) continue;
+        __syncthreads();
+        for (int e = threadIdx.x; e < 4096; e += 256) {
+            const int cc = e / 64, r = e % 64;
+            if (r0 + r < a.R && c0 + cc < sd.C)
+                (static_cast<E*>(sd.out) + l * sd.so)[(c0 + cc) * sd.ldo + r0 + r] = E(part[cc][r]);
+        }
+    }
+}
+
+struct BackwardPlan {
+    PassPlan pass;  // dH and dX: rows of N sums, K results
+    int chunk;
+    int64_t chunks, slots;
+    int64_t pitch_a, pitch_b;
+    size_t chunks_at, chunk_start_at, slot_start_at, a_at, b_at, pa_at, pb_at, bytes;
+};
+
+BackwardPlan backward_plan(int type, bool ids, int64_t M, int64_t N, int64_t K, int R, int L) {
+    BackwardPlan p{};
+    p.pass = pass_plan(type, ids, false, M, K, N, R, L);
+    p.chunk = M > 2048 ? 256 : M > 512 ? 128 : 64;
+    p.chunks = ceil_div(M, p.chunk) + (ids ? (L < M ? L : M) : 0);
+    // Adapters with more than one chunk have at most two for each `chunk` rows.
+    p.slots = 2 * ceil_div(M, p.chunk);
+    p.pitch_a = (R + 7) / 8 * 8;
+    p.pitch_b = (N + 7) / 8 * 8;
+    size_t at = align_up(p.pass.bytes);
+    auto take = [&](size_t n) {
+        const size_t here = at;
+        at += align_up(n);
+        return here;
+    };
+    const size_t es = type == T_F32 ? 4 : 2;
+    p.chunks_at = take(size_t(4 + 4 * (p.chunks + 1)) * sizeof(int));
+    p.chunk_start_at = take(size_t(L + 1) * sizeof(int));
+    p.slot_start_at = take(size_t(L + 1) * sizeof(int));
+    p.a_at = take(size_t(L) * K * p.pitch_a * es);
+    p.b_at = take(size_t(L) * R * p.pitch_b * es);
+    p.pa_at = take(size_t(p.slots) * R * K * sizeof(float));
+    p.pb_at = take(size_t(p.slots) * R * N * sizeof(float));
+    p.bytes = at;
+    return p;
+}
+
+template <int T>
+hipError_t weights(const LoraGradArgs& b, const BackwardPlan& p, const RowPlan& rows, const float* dH, hipStream_t s) {
+    const LoraArgs& g = b.f;
+    char* const ws = static_cast<char*>(g.ws);
+    WeightArgs a{};
+    a.R = g.R;
+    a.chunk = p.chunk;
+    a.rows = rows;
+    a.chunks = p.chunks;
+    a.slot_start = reinterpret_cast<const int*>(ws + p.slot_start_at);
+    a.chunk_start = reinterpret_cast<const int*>(ws + p.chunk_start_at);
+    const int64_t wide = 4 * kGroupCols<T>;
+    SideArgs& x = a.side[0];
+    x = {g.X, g.ldx, b.dA ? g.K : 0, dH, lora_pitch(g.R), g.M * lora_pitch(g.R), p.pass.planes, true,
+         reinterpret_cast<float*>(ws + p.pa_at), b.dA, b.ldda, b.sda, false, nullptr, 1.0f, false, 0};
+    SideArgs& y = a.side[1];
+    y = {g.Y, g.ldy, b.dB ? g.N : 0, g.H, g.ldh, 0, 1, false,
+         reinterpret_cast<float*>(ws + p.pb_at), b.dB, b.lddb, b.sdb, true, g.scales, g.alpha, true, 0};
+    x.groups = ceil_div(x.C, wide);
+    y.groups = ceil_div(y.C, wide);
+    if (x.groups + y.groups == 0) return hipSuccess;
+    const bool narrow = (x.C > 0 && x.C < kVec<T>) || (y.C > 0 && y.C < kVec<T>);
+    auto run = [&](auto rb) {
+        constexpr int RB = decltype(rb)::value;
+        const dim3 grid(grid_for(p.chunks * (x.groups + y.groups)), 1, (g.R + 16 * RB - 1) / (16 * RB));
+        if (narrow) hipLaunchKernelGGL((lora_weights<T, RB, true>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((lora_weights<T, RB, false>), grid, dim3(256), 0, s, a);
+    };
+    if (g.M > 0) {
+        if (g.R <= 16) run(std::integral_constant<int, 1>{});
+        else if (g.R <= 32) run(std::integral_constant<int, 2>{});
+        else run(std::integral_constant<int, 4>{});
+    }
+    const int64_t rt = (g.R + 63) / 64, t0 = g.L * rt * ceil_div(x.C, 64), t1 = g.L * rt * ceil_div(y.C, 64);
+    hipLaunchKernelGGL(lora_weights_sum<T>, dim3(grid_for(t0 + t1)), dim3(256), 0, s, a, t0, t0 + t1);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t lora_backward_bytes(int type, bool ids, int64_t M, int64_t N, int64_t K, int R, int L) {
+    return backward_plan(type, ids, M, N, K, R, L).bytes;
+}
+
+hipError_t launch_lora_backward(const LoraGradArgs& b, hipStream_t s) {
+    const LoraArgs& g = b.f;
+    hipError_t e = hipSuccess;
+    BackwardPlan p{};
+    RowPlan rows{RowPlan::UNIFORM, nullptr, false, int(g.M), g.L, nullptr, nullptr}, chunks = rows;
+    char* const ws = static_cast<char*>(g.ws);
+    float* dH = nullptr;
+    if (g.M > 0) {
+        p = backward_plan(g.type, g.ids != nullptr, g.M, g.N, g.K, g.R, g.L);
+        dH = reinterpret_cast<float*>(ws + p.pass.p_at);
+        if (g.ids) {
+            int* const order = reinterpret_cast<int*>(ws + p.pass.order_at);
+            int* const head = reinterpret_cast<int*>(ws + p.pass.tiles_at);
+            int* const ch = reinterpret_cast<int*>(ws + p.chunks_at);
+            const GroupArgs a{g.ids, g.id64, int(g.M), g.L, 0, order, 16 * p.pass.tmb, head, p.chunk, ch,
+                              reinterpret_cast<int*>(ws + p.chunk_start_at), reinterpret_cast<int*>(ws + p.slot_start_at)};
+            if ((e = launch_lora_group(a, s)) != hipSuccess) return e;
+            rows = {RowPlan::SORTED, g.ids, g.id64, int(g.M), g.L, order, head};
+            chunks = rows;
+            chunks.head = ch;
+        }
+        // The adapters transposed: A for dX, B for dH.
+        TurnArgs ta{g.A, g.lda, g.sa, g.R, b.dX ? g.K : 0, ws + p.a_at, p.pitch_a, ceil_div(p.pitch_a, 64), 0};
+        TurnArgs tb{g.B, g.ldb, g.sb, g.N, b.dX || b.dA ? g.R : 0, ws + p.b_at, p.pitch_b, ceil_div(p.pitch_b, 64), 0};
+        ta.tiles_c = ceil_div(ta.cols, 64);
+        tb.tiles_c = ceil_div(tb.cols, 64);
+        const int64_t na = g.L * ta.tiles_r * ta.tiles_c, nt = na + g.L * tb.tiles_r * tb.tiles_c;
+        if (nt > 0) {
+            if (g.type == T_F32) hipLaunchKernelGGL(lora_turn<uint32_t>, dim3(grid_for(nt)), dim3(256), 0, s, ta, tb, na, nt);
+            else hipLaunchKernelGGL(lora_turn<uint16_t>, dim3(grid_for(nt)), dim3(256), 0, s, ta, tb, na, nt);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
+        const int64_t plane = g.M * lora_pitch(g.R);
+        if (b.dX || b.dA) {
+            const ShrinkArgs sh{g.Y, g.ldy, ws + p.b_at, p.pitch_b, g.R * p.pitch_b, g.N, g.R, g.scales, g.alpha, true,
+                                dH, plane, p.pass.kshare, rows, p.pass.tiles};
+            if ((e = launch_shrink(g.type, sh, p.pass, s)) != hipSuccess) return e;
+        }
+        if (b.dX && g.K > 0) {
+            const ExpandArgs ex{dH, plane, p.pass.planes, g.R, ws + p.a_at, p.pitch_a, g.K * p.pitch_a, g.K, nullptr,
+                                1.0f, false, g.base, g.ldbase, b.dX, b.lddx, nullptr, 0, p.pass.nshare, rows, p.pass.tiles};
+            if ((e = launch_expand(g.type, ex, p.pass, s)) != hipSuccess) return e;
+        }
+    }
+    if (g.type == T_F32) return weights<T_F32>(b, p, chunks, dH, s);
+    if (g.type == T_F16) return weights<T_F16>(b, p, chunks, dH, s);
+    return weights<T_BF16>(b, p, chunks, dH, s);
+}
+
+}  // namespace sgemm

@@ -101,19 +101,25 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group(GroupArgs a) {
         scan(a.waves * groups, [&](int e) -> int& { return table[e % a.waves * groups + e / a.waves]; });
         // table[l] is now where adapter l's rows start.
         auto start_of = [&](int l) { return l < groups ? table[l] : a.M; };
+        // Tiles, chunks, and the chunks of adapters that have more than one.
 #pragma unroll 1
-        for (int kind = 0; kind < 2; kind++) {
+        for (int kind = 0; kind < 3; kind++) {
             const int size = kind ? a.chunk : a.tile;
             int* const head = kind ? a.chunks : a.tiles;
             if (!head) continue;
             const int last = kind ? a.L : groups;  // chunks are of adapters only
 #pragma unroll 1
-            for (int l = threadIdx.x; l < last; l += kGroupThreads)
-                first[l] = (start_of(l + 1) - start_of(l) + size - 1) / size;
+            for (int l = threadIdx.x; l < last; l += kGroupThreads) {
+                const int n = (start_of(l + 1) - start_of(l) + size - 1) / size;
+                first[l] = kind == 2 && n == 1 ? 0 : n;
+            }
             __syncthreads();
             const int total = scan(last, [&](int e) -> int& { return first[e]; });
+            int* const starts = kind == 1 ? a.chunk_start : kind == 2 ? a.slot_start : nullptr;
+            if (starts)
+                for (int l = threadIdx.x; l <= last; l += kGroupThreads) starts[l] = l < last ? first[l] : total;
 #pragma unroll 1
-            for (int t = threadIdx.x; t < total; t += kGroupThreads) {
+            for (int t = threadIdx.x; kind < 2 && t < total; t += kGroupThreads) {
                 int lo = 0, hi = last - 1;  // the last l with first[l] <= t
 #pragma unroll 1
                 while (lo < hi) {
@@ -122,11 +128,10 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group(GroupArgs a) {
                     else hi = mid - 1;
                 }
                 const int s = start_of(lo) + (t - first[lo]) * size, n = start_of(lo + 1) - s;
-                reinterpret_cast<int4*>(head)[1 + int64_t(t)] = int4{lo < a.L ? lo : -1, s, n < size ? n : size, 0};
+                reinterpret_cast<int4*>(head)[1 + int64_t(t)] =
+                    int4{lo < a.L ? lo : -1, s, n < size ? n : size, t - first[lo]};
             }
-            if (threadIdx.x == 0) head[0] = total;
-            if (kind)
-                for (int l = threadIdx.x; l <= last; l += kGroupThreads) a.chunk_start[l] = l < last ? first[l] : total;
+            if (threadIdx.x == 0 && kind < 2) head[0] = total;
             __syncthreads();
         }
     }

@@ -7,33 +7,12 @@
 // for up to 64 rows.  Nothing is staged: the matrix instructions' operands are
 // 16 bytes along K (or R) of one row, which is how memory holds them.
 #pragma once
-#include "lora_rows.h"
+#include "lora.h"
 
 namespace sgemm {
 namespace {
 
-// Floats of a row of a plane of H: R rounded up so that rows are 64-byte pieces,
-// zero past R.
-__host__ __device__ constexpr int lora_pitch(int R) { return (R + 15) / 16 * 16; }
-
 // ---- H = X A^T ----------------------------------------------------------------
-
-struct ShrinkArgs {
-    const void* X;      // rows of K elements
-    int64_t ldx;
-    const void* W;      // L x R x K
-    int64_t ldw, sw;
-    int64_t K;
-    int R;
-    const float* scales;  // with scaled: the sums times alpha scales[l]
-    float alpha;
-    bool scaled;
-    float* P;           // planes of M rows of lora_pitch(R) floats, in the order of positions, one for each K share
-    int64_t plane;
-    int64_t kshare;     // K per grid.y
-    RowPlan rows;
-    int64_t tiles;
-};
 
 constexpr int kShrinkWaves = 4;
 
@@ -144,27 +123,6 @@ lora_shrink(ShrinkArgs a) {
 enum ExpandKind { EXPAND_PACKED, EXPAND_HELD, EXPAND_LONG };
 
 // ---- Y = base + s H B^T -------------------------------------------------------
-
-struct ExpandArgs {
-    const float* P;     // H: the sum of `planes` planes, as ShrinkArgs
-    int64_t plane;
-    int planes, R;
-    const void* W;      // L x N x R
-    int64_t ldw, sw;
-    int64_t N;
-    const float* scales;
-    float alpha;
-    bool scaled;
-    const void* base;
-    int64_t ldbase;
-    void* Y;
-    int64_t ldy;
-    float* H;           // also store H here
-    int64_t ldh;
-    int64_t nshare;     // N per grid.y, a multiple of 64
-    RowPlan rows;
-    int64_t tiles;
-};
 
 // LDS of a workgroup: H in the operands' form (two 16-bit parts, or floats) with
 // rows padded by 16 bytes, and a factor for each row.

@@ -5,6 +5,17 @@
 #include "kernels.h"
 
 namespace sgemm {
+
+// How rows are dealt out in tiles.
+struct RowPlan {
+    enum Mode { SORTED, SINGLE, UNIFORM } mode;
+    const void* ids;   // SINGLE: a tile is one row, with the adapter of its id
+    bool id64;
+    int M, L;
+    const int* order;  // SORTED: row of each position, rows of one adapter together
+    const int* head;   // SORTED: number of tiles, 3 unused, then RowTile's fields of each
+};
+
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -20,19 +31,9 @@ template <> struct Elem<T_BF16> { using type = __bf16; };
 template <int T> constexpr int kVec = T == T_F32 ? 4 : 8;
 
 // A run of rows with one adapter (-1: none): positions [start, start + count)
-// of the order.
+// of the order; the place-th such run of its adapter.
 struct RowTile {
-    int adapter, start, count;
-};
-
-// How rows are dealt out in tiles.
-struct RowPlan {
-    enum Mode { SORTED, SINGLE, UNIFORM } mode;
-    const void* ids;   // SINGLE: a tile is one row, with the adapter of its id
-    bool id64;
-    int M, L;
-    const int* order;  // SORTED: row of each position, rows of one adapter together
-    const int* head;   // SORTED: number of tiles, then RowTile's fields of each
+    int adapter, start, count, place;
 };
 
 __device__ __forceinline__ int adapter_of(const void* ids, bool id64, int L, int64_t m) {
@@ -48,11 +49,12 @@ __device__ __forceinline__ RowTile row_tile(const RowPlan& p, int64_t t, int siz
         const int n = p.head[0];
         const int4 at = reinterpret_cast<const int4*>(p.head)[1 + t];  // in bounds, of no meaning past the last
         return {__builtin_amdgcn_readfirstlane(at.x), __builtin_amdgcn_readfirstlane(at.y),
-                t < n ? __builtin_amdgcn_readfirstlane(at.z) : 0};
+                t < n ? __builtin_amdgcn_readfirstlane(at.z) : 0, __builtin_amdgcn_readfirstlane(at.w)};
     }
-    if (p.mode == RowPlan::SINGLE) return {adapter_of(p.ids, p.id64, p.L, t), int(t), 1};
+    if (p.mode == RowPlan::SINGLE) return {adapter_of(p.ids, p.id64, p.L, t), int(t), 1, 0};
     const int64_t start = t * size;
-    return {0, int(start), int(p.M - start < size ? p.M - start : size)};
+    if (start >= p.M) return {0, 0, 0, 0};
+    return {0, int(start), int(p.M - start < size ? p.M - start : size), int(t)};
 }
 
 __device__ __forceinline__ int row_at(const RowPlan& p, int position) {

@@ -266,6 +266,27 @@ using Tile128 = Tile<2, 2, 2, 2, 2, 2>;
 using Tile192 = Tile<2, 2, 3, 3, 3, 1>;
 using Tile256 = Tile<2, 4, 4, 2, 2, 2>;
 
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const char* base) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(base), (short)0, int(0x80000000u), 0x00020000);
+}
+
+// One buffer load that writes LDS directly: lane L's bytes go to lds + BYTES L.  (A
+// template, as the host pass does not know the builtin.)
+template <int BYTES>
+__device__ __forceinline__ void load_lds(__amdgpu_buffer_rsrc_t r, char* lds, unsigned off, int at) {
+    static_assert(BYTES == 16, "the one width used");
+    if constexpr (BYTES == 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, LDS_PTR(lds), 16, off, at, 0, 0);
+}
+
+// Every load of this wave but the latest N has landed and its LDS reads are done,
+// then the same of every wave.  (__syncthreads would wait for all loads.)
+template <int N>
+__device__ __forceinline__ void step_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // A workgroup: one tile.  Steps of 32 of the sum go through the LDS stages, written
 // by loads that bypass the registers, STAGES - 1 ahead; a row's eight 16-byte
 // pieces are turned by (row / 2) % 8 places, so that sixteen lanes that read the
@@ -290,22 +311,19 @@ ortho_product(ProductArgs a) {
     // A wave's loads: each 8 rows, lane L the piece that lies at L.
     constexpr int LOADS = SIDE / 8 / CF::WAVES;
     static_assert(SIDE % (8 * CF::WAVES) == 0, "whole loads");
-    int64_t off[LOADS];
+    unsigned off[LOADS];  // below 256 rows of 256 KiB
 #pragma unroll
     for (int u = 0; u < LOADS; u++) {
         const int r = (wave * LOADS + u) * 8 + (lane >> 3);
-        off[u] = int64_t(r) * a.K * 4 + (((lane & 7) ^ (r >> 1 & 7)) * 16);
+        off[u] = unsigned(r) * unsigned(a.K) * 4u + (((lane & 7) ^ (r >> 1 & 7)) * 16);
     }
     auto issue = [&](int s) {
+        const __amdgpu_buffer_rsrc_t ra = make_rsrc(ga), rb = make_rsrc(gb);
         char* const to = smem + s % NS * STAGE + wave * LOADS * 1024;
 #pragma unroll
         for (int u = 0; u < LOADS; u++) {
-            __builtin_amdgcn_global_load_lds(
-                reinterpret_cast<const __attribute__((address_space(1))) void*>(reinterpret_cast<uintptr_t>(ga + off[u] + int64_t(s) * 128)),
-                LDS_PTR(to + u * 1024), 16, 0, 0);
-            __builtin_amdgcn_global_load_lds(
-                reinterpret_cast<const __attribute__((address_space(1))) void*>(reinterpret_cast<uintptr_t>(gb + off[u] + int64_t(s) * 128)),
-                LDS_PTR(to + CF::BYTES + u * 1024), 16, 0, 0);
+            load_lds<16>(ra, to + u * 1024, off[u], s * 128);
+            load_lds<16>(rb, to + CF::BYTES + u * 1024, off[u], s * 128);
         }
     };
     v16f acc[MBM][MBN];
@@ -370,13 +388,11 @@ ortho_product(ProductArgs a) {
     // stage that is written next.
     int s = 0;
     for (; s + NS - 1 < steps; s++) {
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((NS - 2) * 2 * LOADS) : "memory");
-        __syncthreads();
+        step_barrier<(NS - 2) * 2 * LOADS>();
         step(s, std::true_type{});
     }
     for (; s < steps; s++) {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
+        step_barrier<0>();
         step(s, std::false_type{});
     }
     __syncthreads();

@@ -422,9 +422,9 @@ int sgemm_lora_backward(int type, int64_t M, int64_t N, int64_t K, int64_t R, in
  * memory, read before the call returns; steps 1..SGEMM_ORTHO_MAX_STEPS.  G and O
  * are of type `type`; O may be G itself (same strides), else they must not
  * overlap; O's strides must keep the matrices apart.
- *   The norm is summed in double.  Between the steps X and S are kept as two
- * float16 parts each, 22 bits, times a power of two, and products are summed in
- * float.  The power comes from a bound of X that follows from the coefficients
+ *   The norm is summed in double.  Matrices with a side of up to 64 are computed
+ * in double.  For others X and S are kept between the steps as two float16 parts
+ * each, 22 bits, times a power of two, and products are summed in float.  The power comes from a bound of X that follows from the coefficients
  * alone (|X| <= 1 at the start); coefficients that are not finite or let it pass
  * 64 are SGEMM_ERR_ARG.  A matrix of zeros gives zeros; an infinity or NaN in G
  * makes its matrix's results NaN.

@@ -20,7 +20,7 @@
 #include <cmath>
 #include <type_traits>
 
-#include "kernels.h"
+#include "orthogonalize.h"
 
 namespace sgemm {
 namespace {
@@ -54,7 +54,7 @@ __device__ __forceinline__ void split(float v, _Float16& hi, _Float16& lo) {
 
 // ---- the norm and the first X ---------------------------------------------------
 
-constexpr int kNormBlocks = 1024;  // partial sums of a matrix
+constexpr int kNormBlocks = 512;  // partial sums of a matrix
 
 // Partial sums of squares in double, block x of matrix y; 16 bytes a lane at a
 // time, four in flight, where the matrix has no gaps.
@@ -101,7 +101,8 @@ __global__ void __launch_bounds__(256) ortho_squares(const void* G, int64_t M, i
 
 // X and X^T in parts, times `scale`, from G: a 64 x 64 tile of X (m x n) a
 // workgroup, turned in LDS.  Rows have kn and km columns.
-__global__ void __launch_bounds__(256) ortho_split(int type, const void* G, bool tall, int64_t m, int64_t n, int64_t ldg,
+template <int TYPE>
+__global__ void __launch_bounds__(256) ortho_split(const void* G, bool tall, int64_t m, int64_t n, int64_t ldg,
                                                    int64_t sg, const double* squares, int parts, double eps,
                                                    float scale, _Float16* X, _Float16* Xt, int64_t km, int64_t kn,
                                                    int64_t sx, int64_t st) {
@@ -119,17 +120,22 @@ __global__ void __launch_bounds__(256) ortho_split(int type, const void* G, bool
     const double f = double(scale) / (sqrt(total) + eps);
     X += b * sx;
     Xt += b * st;
-    // Rows of G as they lie: X's rows, or its columns.
-    for (int e = threadIdx.x; e < 4096; e += 256) {
-        const int y = e / 64, x = e % 64;
+    // Rows of G as they lie: X's rows, or its columns; the loads first.
+    float v[16];
+#pragma unroll
+    for (int u = 0; u < 16; u++) {
+        const int y = u * 4 + int(threadIdx.x) / 64, x = threadIdx.x % 64;
         const int64_t r = tall ? r0 + x : r0 + y, c = tall ? c0 + y : c0 + x;
-        float v = 0.0f;
-        if (r < m && c < n) {
-            const double g = load_as(type, G, b * sg + (tall ? c * ldg + r : r * ldg + c));
-            v = g == 0 ? 0.0f : float(g * f);  // zeros stay so whatever f
-        }
-        if (tall) tile[x][y] = v;
-        else tile[y][x] = v;
+        const bool in = r < m && c < n;
+        v[u] = load_as(TYPE, G, b * sg + (in ? (tall ? c * ldg + r : r * ldg + c) : 0));
+        if (!in) v[u] = 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < 16; u++) {
+        const int y = u * 4 + int(threadIdx.x) / 64, x = threadIdx.x % 64;
+        const float w = v[u] == 0 ? 0.0f : float(double(v[u]) * f);  // zeros stay so whatever f
+        if (tall) tile[x][y] = w;
+        else tile[y][x] = w;
     }
     __syncthreads();
     for (int e = threadIdx.x; e < 512; e += 256) {
@@ -262,7 +268,7 @@ struct Tile {
     static constexpr int BYTES = SIDE * 128;  // of one operand's stage
 };
 using Tile64 = Tile<2, 2, 1, 1, 4, 2>;
-using Tile128 = Tile<2, 2, 2, 2, 2, 2>;
+using Tile128 = Tile<2, 4, 2, 1, 4, 2>;
 using Tile192 = Tile<2, 2, 3, 3, 3, 1>;
 using Tile256 = Tile<2, 4, 4, 2, 2, 2>;
 
@@ -687,10 +693,13 @@ hipError_t run_steps(const OrthoArgs& g, const OrthoPlan& p, hipStream_t s) {
 }  // namespace
 
 size_t ortho_workspace_bytes(int64_t batch, int64_t M, int64_t N) {
-    return batch && M && N ? ortho_plan(batch, M, N).bytes : 0;
+    if (!batch || !M || !N) return 0;
+    if (std::min(M, N) <= kOrthoSmall) return ortho_small_bytes(batch, M, N);
+    return ortho_plan(batch, M, N).bytes;
 }
 
 hipError_t launch_orthogonalize(const OrthoArgs& g, hipStream_t s) {
+    if (std::min(g.M, g.N) <= kOrthoSmall) return launch_ortho_small(g, s);
     const OrthoPlan p = ortho_plan(g.batch, g.M, g.N);
     char* const ws = static_cast<char*>(g.ws);
     double* const squares = reinterpret_cast<double*>(ws + p.squares_at);
@@ -699,10 +708,16 @@ hipError_t launch_orthogonalize(const OrthoArgs& g, hipStream_t s) {
     if (g.type == T_F32) hipLaunchKernelGGL(ortho_squares<T_F32>, grid, dim3(256), 0, s, g.G, g.M, g.N, g.ldg, g.sg, squares);
     else if (g.type == T_F16) hipLaunchKernelGGL(ortho_squares<T_F16>, grid, dim3(256), 0, s, g.G, g.M, g.N, g.ldg, g.sg, squares);
     else hipLaunchKernelGGL(ortho_squares<T_BF16>, grid, dim3(256), 0, s, g.G, g.M, g.N, g.ldg, g.sg, squares);
-    hipLaunchKernelGGL(ortho_split, dim3(unsigned(ceil_div(p.kn, 64)), unsigned(ceil_div(p.km, 64)), unsigned(g.batch)),
-                       dim3(256), 0, s, g.type, g.G, p.tall, p.m, p.n, g.ldg, g.sg, squares, blocks, g.eps,
-                       float(std::ldexp(1.0, power_for(g.bounds[0]))), reinterpret_cast<_Float16*>(ws + p.x_at),
-                       reinterpret_cast<_Float16*>(ws + p.xt_at[0]), p.km, p.kn, p.am * p.kn * 2, p.an * p.km * 2);
+    const dim3 tiles(unsigned(ceil_div(p.kn, 64)), unsigned(ceil_div(p.km, 64)), unsigned(g.batch));
+    auto start = [&](auto type) {
+        hipLaunchKernelGGL(ortho_split<decltype(type)::value>, tiles, dim3(256), 0, s, g.G, p.tall, p.m, p.n, g.ldg, g.sg,
+                           squares, blocks, g.eps, float(std::ldexp(1.0, power_for(g.bounds[0]))),
+                           reinterpret_cast<_Float16*>(ws + p.x_at), reinterpret_cast<_Float16*>(ws + p.xt_at[0]), p.km,
+                           p.kn, p.am * p.kn * 2, p.an * p.km * 2);
+    };
+    if (g.type == T_F32) start(std::integral_constant<int, T_F32>{});
+    else if (g.type == T_F16) start(std::integral_constant<int, T_F16>{});
+    else start(std::integral_constant<int, T_BF16>{});
     return run_steps(g, p, s);
 }
 

@@ -79,6 +79,8 @@ struct ExpandArgs {
 // The two products (lora.hip), of element type T.
 hipError_t launch_shrink(int type, const ShrinkArgs& a, const PassPlan& p, hipStream_t s);
 hipError_t launch_expand(int type, const ExpandArgs& a, const PassPlan& p, hipStream_t s);
+// The planes of H added into the first.
+hipError_t launch_join(float* P, int64_t plane, int planes, hipStream_t s);
 size_t lora_backward_bytes(int type, bool ids, int64_t M, int64_t N, int64_t K, int R, int L);
 
 }  // namespace sgemm

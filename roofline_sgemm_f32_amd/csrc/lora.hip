@@ -61,7 +61,21 @@ hipError_t by_type(int type, F f) {
     return hipGetLastError();
 }
 
+__global__ void __launch_bounds__(256) lora_join(float* P, int64_t plane, int planes) {
+    for (int64_t e = (int64_t(blockIdx.x) * 256 + threadIdx.x) * 4; e < plane; e += int64_t(gridDim.x) * 1024) {
+        v4f v = *reinterpret_cast<const v4f*>(P + e);
+#pragma unroll 4
+        for (int z = 1; z < planes; z++) v += *reinterpret_cast<const v4f*>(P + z * plane + e);
+        *reinterpret_cast<v4f*>(P + e) = v;
+    }
+}
+
 }  // namespace
+
+hipError_t launch_join(float* P, int64_t plane, int planes, hipStream_t s) {
+    hipLaunchKernelGGL(lora_join, dim3(grid_for(ceil_div(plane, 1024))), dim3(256), 0, s, P, plane, planes);
+    return hipGetLastError();
+}
 
 PassPlan pass_plan(int type, bool ids, bool single, int64_t M, int64_t N, int64_t K, int R, int L) {
     PassPlan p{};
@@ -130,7 +144,11 @@ hipError_t launch_lora(const LoraArgs& g, hipStream_t s) {
     const int64_t plane = g.M * lora_pitch(g.R);
     const ShrinkArgs sh{g.X, g.ldx, g.A, g.lda, g.sa, g.K, g.R, nullptr, 1.0f, false, P, plane, p.kshare, rows, p.tiles};
     if ((e = launch_shrink(g.type, sh, p, s)) != hipSuccess) return e;
-    const ExpandArgs ex{P, plane, p.planes, g.R, g.B, g.ldb, g.sb, g.N, g.scales, g.alpha, true,
+    // Tiles of 64 rows read the planes once for each share of N: more than a few
+    // planes are worth a launch that adds them first.
+    const bool join = p.tmb == 4 && p.planes > 2;
+    if (join && (e = launch_join(P, plane, p.planes, s)) != hipSuccess) return e;
+    const ExpandArgs ex{P, plane, join ? 1 : p.planes, g.R, g.B, g.ldb, g.sb, g.N, g.scales, g.alpha, true,
                         g.base, g.ldbase, g.Y, g.ldy, g.H, g.ldh, p.nshare, rows, p.tiles};
     return launch_expand(g.type, ex, p, s);
 }

@@ -54,9 +54,8 @@ __global__ void __launch_bounds__(256) lora_turn(TurnArgs a, TurnArgs b, int64_t
 struct SideArgs {
     const void* Z;        // M rows of C elements
     int64_t ldz, C;
-    const float* V;       // by_position: planes in the order of positions, else rows
-    int64_t ldv, plane;
-    int planes;
+    const float* V;       // by_position: in the order of positions, else by rows
+    int64_t ldv;
     bool by_position;
     float* partial;       // slots of R x C
     void* out;            // an adapter's only chunk: R x C, or C x R (turned), times the scale
@@ -125,21 +124,32 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) l
         // loads need no check: two lanes then find, and store, the same sums.
         const int64_t c = NARROW || c0 + i * V + V <= sd.C ? c0 + i * V : sd.C - V;
         const float s = sd.scaled ? sd.alpha * (sd.scales ? sd.scales[tile.adapter] : 1.0f) : 1.0f;
-        // Element (position p, rank r0 + r) of V.
+        // Ranks r0 + r .. + 3 of V at position p.
         auto v_at = [&](int p, int r) {
-            if (r0 + r >= a.R || p >= tile.count) return 0.0f;
-            if (!sd.by_position) return sd.V[int64_t(row_at(a.rows, tile.start + p)) * sd.ldv + r0 + r];
-            float v = 0.0f;
-            for (int z = 0; z < sd.planes; z++) v += sd.V[z * sd.plane + int64_t(tile.start + p) * sd.ldv + r0 + r];
+            v4f v = {0, 0, 0, 0};
+            if (p >= tile.count || r0 + r >= a.R) return v;
+            const float* const at = sd.by_position ? sd.V + int64_t(tile.start + p) * sd.ldv + r0 + r
+                                                   : sd.V + int64_t(row_at(a.rows, tile.start + p)) * sd.ldv + r0 + r;
+            if (r0 + r + 4 <= a.R) {
+                __builtin_memcpy(&v, at, 16);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 3; e++)
+                    if (r0 + r + e < a.R) v[e] = at[e];
+            }
             return v;
         };
         if constexpr (T == T_F16) {
             __syncthreads();
             if (threadIdx.x < RN) top[threadIdx.x] = 0;
             __syncthreads();
-            for (int e = threadIdx.x; e < tile.count * RN; e += 256) {
-                const float v = fabsf(v_at(e / RN, e % RN));
-                if (v <= 3.4e38f) atomicMax(&top[e % RN], __float_as_uint(v));  // a maximum has no order
+#pragma unroll 2
+            for (int e = threadIdx.x; e < tile.count * (RN / 4); e += 256) {
+                const int r = e % (RN / 4) * 4;
+                const v4f v = v_at(e / (RN / 4), r);
+#pragma unroll
+                for (int y = 0; y < 4; y++)  // a maximum has no order
+                    if (fabsf(v[y]) <= 3.4e38f) atomicMax(&top[r + y], __float_as_uint(fabsf(v[y])));
             }
         }
         v4f acc[V][RB];
@@ -147,33 +157,48 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) l
         for (int e = 0; e < V; e++)
 #pragma unroll
             for (int n = 0; n < RB; n++) acc[e][n] = v4f{0, 0, 0, 0};
+        // The next rows' V and numbers, fetched while the ones before are multiplied.
+        v4f next[RB];
+        int next_row = 0;
+        auto fetch = [&](int p0) {
+#pragma unroll
+            for (int u = 0; u < RB; u++) {
+                const int e = threadIdx.x + 256 * u;
+                next[u] = v_at(p0 + e / (RN / 4), e % (RN / 4) * 4);
+            }
+            const int p = p0 + int(threadIdx.x);
+            if (threadIdx.x < kWeightRows) next_row = row_at(a.rows, tile.start + (p < tile.count ? p : 0));
+        };
+        fetch(0);
         for (int p0 = 0; p0 < tile.count; p0 += kWeightRows) {
             __syncthreads();
-            for (int e = threadIdx.x; e < kWeightRows * RN; e += 256) {
-                const int p = e / RN, r = e % RN;
-                const float v = v_at(p0 + p, r);
+#pragma unroll
+            for (int u = 0; u < RB; u++) {
+                const int e = threadIdx.x + 256 * u, p = e / (RN / 4), r = e % (RN / 4) * 4;
+                const v4f v = next[u];
                 if constexpr (T == T_F32) {
-                    reinterpret_cast<float*>(vs)[p * RN + r] = v;
+                    *reinterpret_cast<v4f*>(vs + (p * RN + r) * 4) = v;
                 } else {
-                    uint16_t* const at = reinterpret_cast<uint16_t*>(vs) + r * VP + p;
-                    if constexpr (T == T_F16) {
-                        const float x = v * half_power(__uint_as_float(top[r]));
-                        const _Float16 h = _Float16(x);
-                        at[0] = __builtin_bit_cast(uint16_t, h);
-                        at[RN * VP] = __builtin_bit_cast(uint16_t, _Float16(fabsf(x) <= 65504.0f ? x - float(h) : 0.0f));
-                    } else {
-                        const uint32_t cut = __float_as_uint(v) & 0xFFFF0000u;
-                        const bool finite = (cut & 0x7F800000u) != 0x7F800000u;
-                        at[0] = uint16_t(!finite && v != v ? 0x7FC0u : cut >> 16);
-                        at[RN * VP] = __builtin_bit_cast(uint16_t, __bf16(finite ? v - __uint_as_float(cut) : 0.0f));
+#pragma unroll
+                    for (int y = 0; y < 4; y++) {
+                        uint16_t* const at = reinterpret_cast<uint16_t*>(vs) + (r + y) * VP + p;
+                        if constexpr (T == T_F16) {
+                            const float x = v[y] * half_power(__uint_as_float(top[r + y]));
+                            const _Float16 h = _Float16(x);
+                            at[0] = __builtin_bit_cast(uint16_t, h);
+                            at[RN * VP] = __builtin_bit_cast(uint16_t, _Float16(fabsf(x) <= 65504.0f ? x - float(h) : 0.0f));
+                        } else {
+                            const uint32_t cut = __float_as_uint(v[y]) & 0xFFFF0000u;
+                            const bool finite = (cut & 0x7F800000u) != 0x7F800000u;
+                            at[0] = uint16_t(!finite && v[y] != v[y] ? 0x7FC0u : cut >> 16);
+                            at[RN * VP] = __builtin_bit_cast(uint16_t, __bf16(finite ? v[y] - __uint_as_float(cut) : 0.0f));
+                        }
                     }
                 }
             }
-            if (threadIdx.x < kWeightRows) {
-                const int p = p0 + threadIdx.x;
-                row_of[threadIdx.x] = row_at(a.rows, tile.start + (p < tile.count ? p : 0));
-            }
+            if (threadIdx.x < kWeightRows) row_of[threadIdx.x] = next_row;
             __syncthreads();
+            if (p0 + kWeightRows < tile.count) fetch(p0 + kWeightRows);
             if (c0 >= sd.C) continue;
             const int left = tile.count - p0 < kWeightRows ? tile.count - p0 : kWeightRows;
             // Rows past the chunk repeat its first, and are zeroed: what other adapters'
@@ -355,10 +380,10 @@ hipError_t weights(const LoraGradArgs& b, const BackwardPlan& p, const RowPlan& 
     a.chunk_start = reinterpret_cast<const int*>(ws + p.chunk_start_at);
     const int64_t wide = 4 * kGroupCols<T>;
     SideArgs& x = a.side[0];
-    x = {g.X, g.ldx, b.dA ? g.K : 0, dH, lora_pitch(g.R), g.M * lora_pitch(g.R), p.pass.planes, true,
+    x = {g.X, g.ldx, b.dA ? g.K : 0, dH, lora_pitch(g.R), true,
          reinterpret_cast<float*>(ws + p.pa_at), b.dA, b.ldda, b.sda, false, nullptr, 1.0f, false, 0};
     SideArgs& y = a.side[1];
-    y = {g.Y, g.ldy, b.dB ? g.N : 0, g.H, g.ldh, 0, 1, false,
+    y = {g.Y, g.ldy, b.dB ? g.N : 0, g.H, g.ldh, false,
          reinterpret_cast<float*>(ws + p.pb_at), b.dB, b.lddb, b.sdb, true, g.scales, g.alpha, true, 0};
     x.groups = ceil_div(x.C, wide);
     y.groups = ceil_div(y.C, wide);
@@ -423,9 +448,10 @@ hipError_t launch_lora_backward(const LoraGradArgs& b, hipStream_t s) {
             const ShrinkArgs sh{g.Y, g.ldy, ws + p.b_at, p.pitch_b, g.R * p.pitch_b, g.N, g.R, g.scales, g.alpha, true,
                                 dH, plane, p.pass.kshare, rows, p.pass.tiles};
             if ((e = launch_shrink(g.type, sh, p.pass, s)) != hipSuccess) return e;
+            if (p.pass.planes > 1 && (e = launch_join(dH, plane, p.pass.planes, s)) != hipSuccess) return e;
         }
         if (b.dX && g.K > 0) {
-            const ExpandArgs ex{dH, plane, p.pass.planes, g.R, ws + p.a_at, p.pitch_a, g.K * p.pitch_a, g.K, nullptr,
+            const ExpandArgs ex{dH, plane, 1, g.R, ws + p.a_at, p.pitch_a, g.K * p.pitch_a, g.K, nullptr,
                                 1.0f, false, g.base, g.ldbase, b.dX, b.lddx, nullptr, 0, p.pass.nshare, rows, p.pass.tiles};
             if ((e = launch_expand(g.type, ex, p.pass, s)) != hipSuccess) return e;
         }

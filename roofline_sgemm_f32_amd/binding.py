@@ -554,6 +554,13 @@ def q4_glu(X, gate_w, gate_scales, up_w, up_scales, gate_zeros=None, up_zeros=No
 def _stack(t, name, shape, dtype):
     """(row stride, matrix stride) of a 3-D GPU tensor of row-major matrices,
     checked."""
+    try:  # the usual case in few steps
+        (n, rows, cols), (stride, ld, step) = t.shape, t.stride()
+        if (t.dtype is dtype and t.is_cuda and step == 1 and rows > 1 and ld >= cols > 0
+                and (shape is None or (n, rows, cols) == shape)):
+            return ld, (stride if n > 1 else 0)
+    except (AttributeError, ValueError):
+        pass
     if not isinstance(t, torch.Tensor) or t.dtype != dtype:
         raise TypeError(f"{name} must be a tensor of {dtype}")
     if t.device.type != "cuda":
@@ -576,6 +583,9 @@ def _lora_ids(ids, M, L):
         if L != 1:
             raise ValueError("ids are needed where there is more than one adapter")
         return 32
+    if isinstance(ids, torch.Tensor) and ids.is_cuda and ids.shape == (M,) and ids.is_contiguous():
+        if ids.dtype is torch.int32 or ids.dtype is torch.int64:
+            return 32 if ids.dtype is torch.int32 else 64
     if not isinstance(ids, torch.Tensor) or ids.dtype not in (torch.int32, torch.int64):
         raise TypeError("ids must be a tensor of torch.int32 or torch.int64")
     if ids.device.type != "cuda":
@@ -588,6 +598,8 @@ def _lora_ids(ids, M, L):
 def _lora_scale(scale, L):
     """(factor of all adapters, tensor of theirs or None), checked."""
     if isinstance(scale, torch.Tensor):
+        if scale.dtype is torch.float32 and scale.is_cuda and scale.shape == (L,) and scale.is_contiguous():
+            return 1.0, scale
         if scale.dtype != torch.float32:
             raise TypeError("scale must be a number or a tensor of torch.float32")
         if scale.device.type != "cuda":
@@ -611,10 +623,11 @@ def _workspace_bytes(name, *sizes):
 
 
 def _workspace(like, name, *sizes):
-    """Scratch memory for one call, from torch's allocator: it belongs to the
-    current stream, or to the graph that is being captured."""
+    """Scratch memory for one call (tensor, address, bytes), from torch's allocator:
+    it belongs to the current stream, or to the graph that is being captured."""
     n = _workspace_bytes(name, *sizes)
-    return torch.empty(n, dtype=torch.uint8, device=like.device), n
+    ws = like.new_empty(n, dtype=torch.uint8) if n else None
+    return ws, (ws.data_ptr() if n else None), n
 
 
 def lora(X, A, B, ids=None, scale=1.0, base=None, out=None, save=False):
@@ -642,7 +655,7 @@ def lora(X, A, B, ids=None, scale=1.0, base=None, out=None, save=False):
     alpha, scales = _lora_scale(scale, L)
     ldbase = 1 if base is None else _rows(base, "base", (M, N), (t,))
     if out is None:
-        Y, ldy = torch.empty((M, N), dtype=t, device=X.device), max(N, 1)
+        Y, ldy = X.new_empty((M, N)), max(N, 1)
     else:
         Y, ldy = out, _rows(out, "out", (M, N), (t,))
     H, ldh = None, 1
@@ -651,10 +664,10 @@ def lora(X, A, B, ids=None, scale=1.0, base=None, out=None, save=False):
     elif save:
         H, ldh = torch.empty((M, R), dtype=torch.float32, device=X.device), R
     sizes = (_FLOATS[t], M, N, K, R, L)
-    ws, n = _workspace(X, "sgemm_lora_workspace", 0, *sizes)
+    ws, at, n = _workspace(X, "sgemm_lora_workspace", 0, *sizes)
     _call(load().sgemm_lora, "sgemm_lora", X, (A, B, ids, scales, base, Y, H), *sizes, X.data_ptr(), ldx,
           A.data_ptr(), lda, sa, B.data_ptr(), ldb, sb, _ptr(ids), bits, _ptr(scales), alpha,
-          _ptr(base), ldbase, Y.data_ptr(), ldy, _ptr(H), ldh, ws.data_ptr(), n)
+          _ptr(base), ldbase, Y.data_ptr(), ldy, _ptr(H), ldh, at, n)
     return Y if H is None else (Y, H)
 
 
@@ -693,14 +706,14 @@ def lora_backward(dY, X, A, B, H, ids=None, scale=1.0, base=None, need_dx=True, 
             torch.empty((L, R, K), dtype=t, device=X.device), torch.empty((L, N, R), dtype=t, device=X.device))
         (ldda, sda), (lddb, sdb) = _stack(dA, "dA", (L, R, K), t), _stack(dB, "dB", (L, N, R), t)
     sizes = (_FLOATS[t], M, N, K, R, L)
-    ws, n = _workspace(X, "sgemm_lora_workspace", 1, *sizes)
+    ws, at, n = _workspace(X, "sgemm_lora_workspace", 1, *sizes)
     # Empty tensors have no address; the entry point takes null for "skip".
     null = [None if g is None or g.numel() == 0 else g.data_ptr() for g in (dX, dA, dB)]
     _call(load().sgemm_lora_backward, "sgemm_lora_backward", X,
           (dY, A, B, H, ids, scales, base, dX, dA, dB), *sizes, dY.data_ptr(), lddy, X.data_ptr(), ldx,
           A.data_ptr(), lda, sa, B.data_ptr(), ldb, sb, H.data_ptr(), ldh, _ptr(ids), bits,
           _ptr(scales), alpha, _ptr(base), ldbase, null[0], lddx, null[1], ldda, sda, null[2], lddb, sdb,
-          ws.data_ptr(), n)
+          at, n)
     return dX, dA, dB
 
 
@@ -730,10 +743,10 @@ def orthogonalize(G, steps=5, coefficients=MUON, eps=1e-7, out=None):
         raise ValueError("out has the wrong shape")
     ldo, so = _stack(out if out.dim() == 3 else out.unsqueeze(0), "out", tuple(g3.shape), G.dtype)
     batch, M, N = g3.shape
-    ws, n = _workspace(G, "sgemm_orthogonalize_workspace", batch, M, N)
+    ws, at, n = _workspace(G, "sgemm_orthogonalize_workspace", batch, M, N)
     _call(load().sgemm_orthogonalize, "sgemm_orthogonalize", G, (out,), _FLOATS[G.dtype], batch, M, N,
           G.data_ptr(), ldg, sg, out.data_ptr(), ldo, so, len(coef) // 3, coef, float(eps),
-          ws.data_ptr(), n)
+          at, n)
     return out
 
 

@@ -21,6 +21,19 @@ struct GroupArgs {
 };
 hipError_t launch_lora_group(const GroupArgs& a, hipStream_t s);
 
+// Adapters transposed.
+struct TurnArgs {
+    const void* W;  // L matrices of rows x cols
+    int64_t ldw, sw;
+    int64_t rows, cols;
+    void* out;      // L matrices of cols x pitch, zero past `rows`
+    int64_t pitch;
+    int64_t tiles_r, tiles_c;
+};
+
+// The sort (unless group.order is null) and two stacks transposed, in one launch.
+hipError_t launch_lora_prepare(int type, const GroupArgs& group, const TurnArgs& a, const TurnArgs& b, hipStream_t s);
+
 // Sizes of a pass's launches (rows of K sums, N results a row) and of its
 // workspace.
 struct PassPlan {

@@ -88,11 +88,16 @@ PassPlan pass_plan(int type, bool ids, bool single, int64_t M, int64_t N, int64_
     const int64_t kunit = type == T_F32 ? 128 : 256;  // four waves' double steps
     int64_t planes = ceil_div(512, busy), most = ceil_div(K, kunit);
     planes = planes > most ? most : planes;
-    planes = planes > 16 ? 16 : planes < 1 ? 1 : planes;
+    const int64_t cap = p.mode == RowPlan::SINGLE ? 8 : 16;
+    planes = planes > cap ? cap : planes < 1 ? 1 : planes;
     p.kshare = K > 0 ? ceil_div(ceil_div(K, planes), kunit) * kunit : 1;
     p.planes = int(K > 0 ? ceil_div(K, p.kshare) : 1);
     const int64_t nunit = p.tmb == 1 ? 256 : 64;
-    int64_t shares = ceil_div(1024, busy), top = ceil_div(N, nunit);
+    // As many workgroups as are resident at a time (lora_expand_tiles by its registers;
+    // 8192 x 8192 bfloat16 of rank 64 78 us, with half as many 98; float 2048 x 4096
+    // of rank 64 24 us, with twice as many 30).
+    const int64_t resident = p.tmb == 1 || R <= 32 || (type != T_F32 && R <= 64) ? 1024 : 512;
+    int64_t shares = ceil_div(resident, busy), top = ceil_div(N, nunit);
     shares = shares > top ? top : shares;
     shares = shares < 1 ? 1 : shares > 4096 ? 4096 : shares;
     p.nshare = N > 0 ? ceil_div(ceil_div(N, shares), nunit) * nunit : nunit;
@@ -118,8 +123,17 @@ hipError_t launch_expand(int type, const ExpandArgs& a, const PassPlan& p, hipSt
     });
 }
 
+// Whether one launch (lora_few) is better than two: at most 16 workgroups, which each
+// read an adapter's A of at most 128 KiB.  us on the GPU, and with what the host takes
+// to call it from Python (11 against 15 at least): A of 16 KiB 3.8 against 6.8, 64 KiB
+// 5.3 against 6.8, 128 KiB 7.3 against 7.0, 256 KiB 10.9 against 7.9, 512 KiB 19.9
+// against 9.6.
+bool few_rows(int type, int64_t M, int64_t N, int64_t K, int64_t R) {
+    return M * ceil_div(N > 0 ? N : 1, kFewCols) <= 16 && R * K * (type == T_F32 ? 4 : 2) <= 128 * 1024;
+}
+
 size_t lora_workspace_bytes(bool backward, int type, int64_t M, int64_t N, int64_t K, int R, int L) {
-    if (M == 0) return 0;
+    if (M == 0 || (!backward && few_rows(type, M, N, K, R))) return 0;
     size_t most = 0;
     for (bool ids : {false, true}) {
         const size_t n = backward ? lora_backward_bytes(type, ids, M, N, K, R, L)
@@ -130,6 +144,14 @@ size_t lora_workspace_bytes(bool backward, int type, int64_t M, int64_t N, int64
 }
 
 hipError_t launch_lora(const LoraArgs& g, hipStream_t s) {
+    if (few_rows(g.type, g.M, g.N, g.K, g.R)) {
+        const dim3 grid(unsigned(ceil_div(g.N > 0 ? g.N : 1, kFewCols)), unsigned(g.M));
+        return by_type(g.type, [&](auto t) {
+            constexpr int T = decltype(t)::value;
+            if (g.R % kVec<T> != 0) hipLaunchKernelGGL((lora_few<T, true>), grid, dim3(512), 0, s, g);
+            else hipLaunchKernelGGL((lora_few<T, false>), grid, dim3(512), 0, s, g);
+        });
+    }
     const PassPlan p = pass_plan(g.type, g.ids != nullptr, true, g.M, g.N, g.K, g.R, g.L);
     char* const ws = static_cast<char*>(g.ws);
     int* const order = reinterpret_cast<int*>(ws + p.order_at);

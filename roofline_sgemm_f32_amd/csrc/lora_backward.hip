@@ -9,45 +9,6 @@
 namespace sgemm {
 namespace {
 
-// ---- transposed adapters --------------------------------------------------------
-
-struct TurnArgs {
-    const void* W;  // L matrices of rows x cols
-    int64_t ldw, sw;
-    int64_t rows, cols;
-    void* out;      // L matrices of cols x pitch, zero past `rows`
-    int64_t pitch;
-    int64_t tiles_r, tiles_c;
-};
-
-// A 64 x 64 tile a workgroup.
-template <typename E>
-__device__ void turn_tile(const TurnArgs& a, int64_t t) {
-    __shared__ E tile[64][64 + 4 / sizeof(E)];
-    const int64_t l = t / (a.tiles_r * a.tiles_c), q = t % (a.tiles_r * a.tiles_c);
-    const int64_t r0 = q / a.tiles_c * 64, c0 = q % a.tiles_c * 64;
-    const E* const w = static_cast<const E*>(a.W) + l * a.sw;
-    for (int e = threadIdx.x; e < 4096; e += 256) {
-        const int64_t r = r0 + e / 64, c = c0 + e % 64;
-        tile[e / 64][e % 64] = r < a.rows && c < a.cols ? w[r * a.ldw + c] : E(0);
-    }
-    __syncthreads();
-    E* const out = static_cast<E*>(a.out) + l * a.cols * a.pitch;
-    for (int e = threadIdx.x; e < 4096; e += 256) {
-        const int64_t c = c0 + e / 64, r = r0 + e % 64;
-        if (c < a.cols && r < a.pitch) out[c * a.pitch + r] = tile[e % 64][e / 64];
-    }
-    __syncthreads();
-}
-
-template <typename E>
-__global__ void __launch_bounds__(256) lora_turn(TurnArgs a, TurnArgs b, int64_t tiles_a, int64_t tiles) {
-    for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-        if (t < tiles_a) turn_tile<E>(a, t);
-        else turn_tile<E>(b, t - tiles_a);
-    }
-}
-
 // ---- sums over rows ----------------------------------------------------------------
 
 // One of the two gradients: W[r, c] = sum over rows m of V[m, r] Z[m, c].
@@ -286,19 +247,19 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) l
     }
 }
 
-// The partial sums of an adapter added, in order, and zeros where no row has it: 64
-// x 64 of (rank, column) a workgroup.
+// The partial sums of an adapter added, in order, and zeros where no row has it:
+// 16 ranks x 64 columns a workgroup, four neighbours a lane.
 template <int T>
 __global__ void __launch_bounds__(256) lora_weights_sum(WeightArgs a, int64_t tiles0, int64_t tiles) {
     using E = typename Elem<T>::type;
-    __shared__ float part[64][65];
-    const int rt = (a.R + 63) / 64;
+    __shared__ float part[64][17];
+    const int rt = (a.R + 15) / 16;
     for (int64_t t0 = blockIdx.x; t0 < tiles; t0 += gridDim.x) {
         const bool second = t0 >= tiles0;
         const SideArgs& sd = a.side[second];
         const int64_t t = second ? t0 - tiles0 : t0, ct = (sd.C + 63) / 64;
         const int l = int(t / (rt * ct));
-        const int r0 = int(t / ct % rt) * 64;
+        const int r0 = int(t / ct % rt) * 16;
         const int64_t c0 = t % ct * 64;
         int64_t first, last;
         bool some;
@@ -311,23 +272,41 @@ __global__ void __launch_bounds__(256) lora_weights_sum(WeightArgs a, int64_t ti
         }
         if (some && first == last) continue;  // written by its only chunk
         __syncthreads();
+        const int r = threadIdx.x / 16, x = threadIdx.x % 16 * 4;
+        const int64_t c = c0 + x;
+        const bool in = r0 + r < a.R && c < sd.C;
+        v4f v = {0, 0, 0, 0};
+        if (in) {
+            const float* at = sd.partial + (first * a.R + r0 + r) * sd.C + c;
+            if (c + 4 <= sd.C) {
 #pragma unroll 4
-        for (int e = threadIdx.x; e < 4096; e += 256) {
-            const int r = e / 64, cc = e % 64;
-            if (r0 + r >= a.R || c0 + cc >= sd.C) continue;
-            float v = 0.0f;
-            const float* at = sd.partial + (first * a.R + r0 + r) * sd.C + c0 + cc;
-#pragma unroll 4
-            for (int64_t q = first; q < last; q++, at += int64_t(a.R) * sd.C) v += *at;
-            if (sd.turned) part[cc][r] = v;
-            else (static_cast<E*>(sd.out) + l * sd.so)[(r0 + r) * sd.ldo + c0 + cc] = E(v);
+                for (int64_t q = first; q < last; q++, at += int64_t(a.R) * sd.C) {
+                    v4f w;
+                    __builtin_memcpy(&w, at, 16);
+                    v += w;
+                }
+            } else {
+                for (int64_t q = first; q < last; q++, at += int64_t(a.R) * sd.C)
+#pragma unroll
+                    for (int e = 0; e < 3; e++)
+                        if (c + e < sd.C) v[e] += at[e];
+            }
         }
-        if (!sd.turned) continue;
+        E* const out = static_cast<E*>(sd.out) + l * sd.so;
+        if (!sd.turned) {
+            if (in)
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    if (c + e < sd.C) out[(r0 + r) * sd.ldo + c + e] = E(v[e]);
+            continue;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; e++) part[x + e][r] = v[e];
         __syncthreads();
-        for (int e = threadIdx.x; e < 4096; e += 256) {
-            const int cc = e / 64, r = e % 64;
-            if (r0 + r < a.R && c0 + cc < sd.C)
-                (static_cast<E*>(sd.out) + l * sd.so)[(c0 + cc) * sd.ldo + r0 + r] = E(part[cc][r]);
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            const int y = u * 16 + int(threadIdx.x) / 16, q = threadIdx.x % 16;
+            if (r0 + q < a.R && c0 + y < sd.C) out[(c0 + y) * sd.ldo + r0 + q] = E(part[y][q]);
         }
     }
 }
@@ -343,7 +322,7 @@ struct BackwardPlan {
 BackwardPlan backward_plan(int type, bool ids, int64_t M, int64_t N, int64_t K, int R, int L) {
     BackwardPlan p{};
     p.pass = pass_plan(type, ids, false, M, K, N, R, L);
-    p.chunk = M > 2048 ? 256 : M > 512 ? 128 : 64;
+    p.chunk = M > 4096 ? 512 : M > 2048 ? 256 : M > 512 ? 128 : 64;
     p.chunks = ceil_div(M, p.chunk) + (ids ? (L < M ? L : M) : 0);
     // Adapters with more than one chunk have at most two for each `chunk` rows.
     p.slots = 2 * ceil_div(M, p.chunk);
@@ -400,7 +379,7 @@ hipError_t weights(const LoraGradArgs& b, const BackwardPlan& p, const RowPlan& 
         else if (g.R <= 32) run(std::integral_constant<int, 2>{});
         else run(std::integral_constant<int, 4>{});
     }
-    const int64_t rt = (g.R + 63) / 64, t0 = g.L * rt * ceil_div(x.C, 64), t1 = g.L * rt * ceil_div(y.C, 64);
+    const int64_t rt = (g.R + 15) / 16, t0 = g.L * rt * ceil_div(x.C, 64), t1 = g.L * rt * ceil_div(y.C, 64);
     hipLaunchKernelGGL(lora_weights_sum<T>, dim3(grid_for(t0 + t1)), dim3(256), 0, s, a, t0, t0 + t1);
     return hipGetLastError();
 }
@@ -421,13 +400,14 @@ hipError_t launch_lora_backward(const LoraGradArgs& b, hipStream_t s) {
     if (g.M > 0) {
         p = backward_plan(g.type, g.ids != nullptr, g.M, g.N, g.K, g.R, g.L);
         dH = reinterpret_cast<float*>(ws + p.pass.p_at);
+        GroupArgs group{};
+        group.L = g.L;
         if (g.ids) {
             int* const order = reinterpret_cast<int*>(ws + p.pass.order_at);
             int* const head = reinterpret_cast<int*>(ws + p.pass.tiles_at);
             int* const ch = reinterpret_cast<int*>(ws + p.chunks_at);
-            const GroupArgs a{g.ids, g.id64, int(g.M), g.L, 0, order, 16 * p.pass.tmb, head, p.chunk, ch,
-                              reinterpret_cast<int*>(ws + p.chunk_start_at), reinterpret_cast<int*>(ws + p.slot_start_at)};
-            if ((e = launch_lora_group(a, s)) != hipSuccess) return e;
+            group = {g.ids, g.id64, int(g.M), g.L, 0, order, 16 * p.pass.tmb, head, p.chunk, ch,
+                     reinterpret_cast<int*>(ws + p.chunk_start_at), reinterpret_cast<int*>(ws + p.slot_start_at)};
             rows = {RowPlan::SORTED, g.ids, g.id64, int(g.M), g.L, order, head};
             chunks = rows;
             chunks.head = ch;
@@ -437,12 +417,7 @@ hipError_t launch_lora_backward(const LoraGradArgs& b, hipStream_t s) {
         TurnArgs tb{g.B, g.ldb, g.sb, g.N, b.dX || b.dA ? g.R : 0, ws + p.b_at, p.pitch_b, ceil_div(p.pitch_b, 64), 0};
         ta.tiles_c = ceil_div(ta.cols, 64);
         tb.tiles_c = ceil_div(tb.cols, 64);
-        const int64_t na = g.L * ta.tiles_r * ta.tiles_c, nt = na + g.L * tb.tiles_r * tb.tiles_c;
-        if (nt > 0) {
-            if (g.type == T_F32) hipLaunchKernelGGL(lora_turn<uint32_t>, dim3(grid_for(nt)), dim3(256), 0, s, ta, tb, na, nt);
-            else hipLaunchKernelGGL(lora_turn<uint16_t>, dim3(grid_for(nt)), dim3(256), 0, s, ta, tb, na, nt);
-            if ((e = hipGetLastError()) != hipSuccess) return e;
-        }
+        if ((e = launch_lora_prepare(g.type, group, ta, tb, s)) != hipSuccess) return e;
         const int64_t plane = g.M * lora_pitch(g.R);
         if (b.dX || b.dA) {
             const ShrinkArgs sh{g.Y, g.ldy, ws + p.b_at, p.pitch_b, g.R * p.pitch_b, g.N, g.R, g.scales, g.alpha, true,

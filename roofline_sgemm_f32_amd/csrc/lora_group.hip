@@ -46,13 +46,11 @@ __device__ int scan(int n, At at) {
 // One workgroup.  Each of `waves` waves has a run of rows of its own: it counts
 // its ids in a table of its own, the tables' prefix sums over (adapter, wave)
 // are where its rows of an adapter go, and it deals them out in order, 64 rows
-// at a time, a row's place among equal ids of the 64 from one ballot per bit of
-// the id; the last of the equals counts for all (LDS atomics on one address take
+// at a time, a row's place among equal ids of the 64 from ballots; the last of the equals counts for all (LDS atomics on one address take
 // their turns).  Rows without adapter come last.  Up to kHeld rows' groups and
 // places stay in LDS between the two passes.  The loops are not unrolled: the code runs
 // once, on one CU, and fetching it takes longer than running it.
-__global__ void __launch_bounds__(kGroupThreads) lora_group(GroupArgs a) {
-    extern __shared__ int lds[];
+__device__ __forceinline__ void group_rows(const GroupArgs& a, int* lds) {
     const int groups = a.L + 1;                  // the last: no adapter
     int* const first = lds;                      // groups + 1: tiles before a group's
     int* const table = lds + groups + 1;         // waves x groups
@@ -68,7 +66,10 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group(GroupArgs a) {
     for (int m = threadIdx.x; m < (a.M < kHeld ? a.M : kHeld); m += kGroupThreads) held[m] = uint16_t(group_of(m));
 #pragma unroll 1
     for (int e = threadIdx.x; e < a.waves * groups; e += kGroupThreads) table[e] = 0;
-    volatile int* const mine = table + wave * groups;  // this wave's, written by any lane of it
+    // The wave's own counts, written by any lane of it: a barrier to the compiler
+    // orders the accesses (volatile ones would leave the LDS instructions: they took
+    // 1.4 us for each 1024 rows).
+    int* const mine = table + wave * groups;
     // Pass 0 counts, pass 1 deals out (without counting again where all
     // places are held).
 #pragma unroll 1
@@ -83,18 +84,29 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group(GroupArgs a) {
                 if (in) a.order[mine[l] + place[m]] = int(m);
                 continue;
             }
-            uint64_t same = __ballot(in);
+            // Lanes with the same id: of up to three ids one by one (runs of rows), else
+            // from the ids' bits.
+            uint64_t same = 0, todo = __ballot(in);
 #pragma unroll 1
-            for (int b = 0; (groups - 1) >> b; b++) {
-                const uint64_t set = __ballot(l >> b & 1);
-                same &= l >> b & 1 ? set : ~set;
+            for (int q = 0; todo && q < 3; q++) {
+                const uint64_t m = __ballot(in && l == __builtin_amdgcn_readlane(l, __builtin_ctzll(todo)));
+                same = m >> lane & 1 ? m : same;
+                todo &= ~m;
+            }
+            if (todo) {
+                same = __ballot(in);
+#pragma unroll 1
+                for (int b = 0; (groups - 1) >> b; b++) {
+                    const uint64_t set = __ballot(l >> b & 1);
+                    same &= l >> b & 1 ? set : ~set;
+                }
             }
             const int at = in ? mine[l] + __popcll(same & ((uint64_t(1) << lane) - 1)) : 0;
-            __builtin_amdgcn_wave_barrier();
+            asm volatile("" ::: "memory");
             if (in && pass) a.order[at] = int(m);
             if (in && m < kHeld) place[m] = uint16_t(at);
             if (in && same >> lane == 1) mine[l] = at + 1;
-            __builtin_amdgcn_wave_barrier();
+            asm volatile("" ::: "memory");
         }
         if (pass) break;
         __syncthreads();
@@ -137,16 +149,88 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group(GroupArgs a) {
     }
 }
 
+__global__ void __launch_bounds__(kGroupThreads) lora_group(GroupArgs a) {
+    extern __shared__ int lds[];
+    group_rows(a, lds);
+}
+
+// A 64 x 64 tile of a transposed matrix a workgroup.
+template <typename E>
+__device__ void turn_tile(const TurnArgs& a, int64_t t, E* tile) {
+    constexpr int PITCH = 64 + 4 / sizeof(E);
+    const int64_t l = t / (a.tiles_r * a.tiles_c), q = t % (a.tiles_r * a.tiles_c);
+    const int64_t r0 = q / a.tiles_c * 64, c0 = q % a.tiles_c * 64;
+    const E* const w = static_cast<const E*>(a.W) + l * a.sw;
+    E v[4096 / kGroupThreads];
+#pragma unroll
+    for (int u = 0; u < 4096 / kGroupThreads; u++) {
+        const int e = u * kGroupThreads + int(threadIdx.x);
+        const int64_t r = r0 + e / 64, c = c0 + e % 64;
+        const bool in = r < a.rows && c < a.cols;
+        v[u] = w[in ? r * a.ldw + c : 0];
+        if (!in) v[u] = E(0);
+    }
+#pragma unroll
+    for (int u = 0; u < 4096 / kGroupThreads; u++) {
+        const int e = u * kGroupThreads + int(threadIdx.x);
+        tile[e / 64 * PITCH + e % 64] = v[u];
+    }
+    __syncthreads();
+    E* const out = static_cast<E*>(a.out) + l * a.cols * a.pitch;
+#pragma unroll
+    for (int u = 0; u < 4096 / kGroupThreads; u++) {
+        const int e = u * kGroupThreads + int(threadIdx.x);
+        const int64_t c = c0 + e / 64, r = r0 + e % 64;
+        if (c < a.cols && r < a.pitch) out[c * a.pitch + r] = tile[e % 64 * PITCH + e / 64];
+    }
+    __syncthreads();
+}
+
+// Workgroup 0 sorts, the others transpose meanwhile.
+template <typename E>
+__global__ void __launch_bounds__(kGroupThreads) lora_prepare(GroupArgs g, TurnArgs a, TurnArgs b, int64_t tiles_a,
+                                                              int64_t tiles) {
+    extern __shared__ int lds[];
+    const int first = g.order ? 1 : 0;
+    if (first && blockIdx.x == 0) {
+        group_rows(g, lds);
+        return;
+    }
+    for (int64_t t = int64_t(blockIdx.x) - first; t < tiles; t += int64_t(gridDim.x) - first) {
+        if (t < tiles_a) turn_tile<E>(a, t, reinterpret_cast<E*>(lds));
+        else turn_tile<E>(b, t - tiles_a, reinterpret_cast<E*>(lds));
+    }
+}
+
+// Waves that sort, by the tables of all of them and the tiles' prefix sums in what
+// held, place and scan leave of 64 KiB; and these tables' bytes.
+size_t group_waves(GroupArgs& a) {
+    const int groups = a.L + 1, ints = 7900;
+    a.waves = (ints - groups - 1) / groups;
+    a.waves = a.waves > kGroupThreads / 64 ? kGroupThreads / 64 : a.waves < 1 ? 1 : a.waves;
+    return size_t(a.waves * groups + groups + 1) * sizeof(int);
+}
+
 }  // namespace
 
 hipError_t launch_lora_group(const GroupArgs& in, hipStream_t s) {
     GroupArgs a = in;
-    // Tables of all waves and the tiles' prefix sums in what held and scan leave of 64 KiB.
-    const int groups = a.L + 1, ints = 8000;
-    a.waves = (ints - groups - 1) / groups;
-    a.waves = a.waves > kGroupThreads / 64 ? kGroupThreads / 64 : a.waves < 1 ? 1 : a.waves;
-    const size_t bytes = size_t(a.waves * groups + groups + 1) * sizeof(int);
+    const size_t bytes = group_waves(a);
     hipLaunchKernelGGL(lora_group, dim3(1), dim3(kGroupThreads), bytes, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_lora_prepare(int type, const GroupArgs& in, const TurnArgs& a, const TurnArgs& b, hipStream_t s) {
+    GroupArgs g = in;
+    size_t bytes = g.order ? group_waves(g) : 0;
+    const int64_t na = g.L * a.tiles_r * a.tiles_c, n = na + g.L * b.tiles_r * b.tiles_c;
+    const int64_t grid = (g.order ? 1 : 0) + n;
+    if (grid == 0) return hipSuccess;
+    if (n > 0 && bytes < 64 * 68 * 4) bytes = 64 * 68 * 4;
+    // 1024 lanes a workgroup: 2^20 of them stay within the 32-bit dispatch size.
+    const dim3 blocks(grid_for(grid)), lanes(kGroupThreads);
+    if (type == T_F32) hipLaunchKernelGGL(lora_prepare<uint32_t>, blocks, lanes, bytes, s, g, a, b, na, n);
+    else hipLaunchKernelGGL(lora_prepare<uint16_t>, blocks, lanes, bytes, s, g, a, b, na, n);
     return hipGetLastError();
 }
 

@@ -316,16 +316,17 @@ lora_expand(ExpandArgs a) {
                     int at[TMB];
 #pragma unroll
                     for (int m = 0; m < TMB; m++) at[m] = in[m] ? (16 * m + int(threadIdx.x >> 4)) * hp + rq : rq;
+                    constexpr int AT_ONCE = TMB == 1 ? 8 : 4;
                     int z = 0;
-                    for (; z + 4 <= a.planes; z += 4) {
-                        v4f q[4][TMB];
+                    for (; z + AT_ONCE <= a.planes; z += AT_ONCE) {
+                        v4f q[AT_ONCE][TMB];
 #pragma unroll
-                        for (int y = 0; y < 4; y++)
+                        for (int y = 0; y < AT_ONCE; y++)
 #pragma unroll
                             for (int m = 0; m < TMB; m++)
                                 q[y][m] = *reinterpret_cast<const v4f*>(P + (z + y) * a.plane + at[m]);
 #pragma unroll
-                        for (int y = 0; y < 4; y++)
+                        for (int y = 0; y < AT_ONCE; y++)
 #pragma unroll
                             for (int m = 0; m < TMB; m++) v[m] += q[y][m];
                     }
@@ -644,6 +645,89 @@ lora_expand_tiles(ExpandArgs a) {
                     }
         }
     }
+}
+
+// ---- few rows ------------------------------------------------------------------
+
+// A row's Y, 512 columns a workgroup, in one launch: every workgroup forms the row's
+// H for itself (its eight waves share K), then a lane a column its sum of R terms, in
+// float.  The adapter's A is so read once for each 512 columns, by one CU at about
+// 25 GB/s: worth it where both are small (see few_rows).
+constexpr int kFewCols = 512;
+
+template <int T, bool ODD>
+__global__ void __launch_bounds__(512) lora_few(LoraArgs a) {
+    using E = typename Elem<T>::type;
+    constexpr int V = kVec<T>, STEP = 4 * V, KEPT = T == T_F32 ? 16 : 32;  // ranks fetched ahead
+    __shared__ float part[8][64], h[256];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int i = lane & 15, g = lane >> 4;
+    const int64_t m = blockIdx.y, n = int64_t(blockIdx.x) * kFewCols + threadIdx.x;
+    const int l = __builtin_amdgcn_readfirstlane(a.ids ? adapter_of(a.ids, a.id64, a.L, m) : 0);
+    const bool has = l >= 0, in = n < a.N;
+    const float b = in && a.base ? float(static_cast<const E*>(a.base)[m * a.ldbase + n]) : 0.0f;
+    if (has) {
+        const E* const w = static_cast<const E*>(a.B) + l * a.sb + (in ? n : a.N - 1) * a.ldb;
+        u32x4 kept[KEPT / V];
+        if (a.N > 0)
+#pragma unroll
+            for (int q = 0; q < KEPT / V; q++) kept[q] = load_ranks<T, ODD>(w, q * V, a.R);
+        const E* const x = static_cast<const E*>(a.X) + m * a.ldx;
+        for (int r0 = 0; r0 < a.R; r0 += 64) {
+            const E* wr[4];
+            v4f acc[4];
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const int r = r0 + 16 * q + i;
+                wr[q] = static_cast<const E*>(a.A) + l * a.sa + int64_t(r < a.R ? r : a.R - 1) * a.lda;
+                acc[q] = v4f{0, 0, 0, 0};
+            }
+            const int blocks = (a.R - r0 + 15) / 16;
+            // Rows 1 .. 15 of the products' left operand repeat row 0; its results count.
+            int64_t k = wave * STEP;
+            for (; k + STEP <= a.K; k += 8 * STEP) {
+                const u32x4 xf = load16(x + k + g * V);
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                    if (q < blocks) acc[q] = mma16<T>(xf, load16(wr[q] + k + g * V), acc[q]);
+            }
+            if (k < a.K) {
+                const u32x4 xf = load_chunk<T>(x, k + g * V, a.K);
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                    if (q < blocks) acc[q] = mma16<T>(xf, load_chunk<T>(wr[q], k + g * V, a.K), acc[q]);
+            }
+            if (g == 0)
+#pragma unroll
+                for (int q = 0; q < 4; q++) part[wave][16 * q + i] = acc[q][0];
+            __syncthreads();
+            if (threadIdx.x < 64) {
+                float v = 0.0f;
+#pragma unroll
+                for (int q = 0; q < 8; q++) v += part[q][threadIdx.x];
+                if (r0 + int(threadIdx.x) < 256) h[r0 + threadIdx.x] = r0 + int(threadIdx.x) < a.R ? v : 0.0f;
+            }
+            __syncthreads();
+        }
+        float v = 0.0f;
+        auto add = [&](u32x4 q, int r) {
+            float f[V];
+            unpack<T>(q, f);
+#pragma unroll
+            for (int e = 0; e < V; e++) v = r + e < a.R ? fmaf(h[r + e], f[e], v) : v;
+        };
+        if (a.N > 0) {
+#pragma unroll
+            for (int q = 0; q < KEPT / V; q++) add(kept[q], q * V);
+            for (int r = KEPT; r < a.R; r += V) add(load_ranks<T, ODD>(w, r, a.R), r);
+        }
+        const float s = a.alpha * (a.scales ? a.scales[l] : 1.0f);
+        if (in) static_cast<E*>(a.Y)[m * a.ldy + n] = E(a.base ? b + s * v : s * v);
+    } else if (in) {
+        static_cast<E*>(a.Y)[m * a.ldy + n] = E(b);
+    }
+    if (a.H && blockIdx.x == 0)
+        for (int r = threadIdx.x; r < a.R; r += 512) a.H[m * a.ldh + r] = has ? h[r] : 0.0f;
 }
 
 }  // namespace

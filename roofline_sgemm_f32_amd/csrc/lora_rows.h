@@ -40,7 +40,7 @@ __device__ __forceinline__ int adapter_of(const void* ids, bool id64, int L, int
     // An int64 as its two halves, so that both types are loads without a branch.
     const uint32_t* const p = static_cast<const uint32_t*>(ids) + (id64 ? 2 * m : m);
     const uint32_t lo = p[0], hi = p[id64 ? 1 : 0];
-    return lo < uint32_t(L) && (!id64 || hi == 0) ? int(lo) : -1;
+    return (lo < uint32_t(L)) & (!id64 | (hi == 0)) ? int(lo) : -1;
 }
 
 // Tile t of `size` rows; count 0 past the last.

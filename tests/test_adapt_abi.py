@@ -39,7 +39,8 @@ def test_lora_refusals(lib):
     assert lora(lib, sa=-1) == LD and lora(lib, sb=-1) == LD
     for name in ("X", "A", "B", "Y"):
         assert lora(lib, **{name: None}) == NULLPTR, name
-    assert lora(lib, n=0) == SCRATCH and lora(lib, n=4) == SCRATCH
+    big = dict(M=400, N=8, K=6, base=None, Y=1 << 50, H=None)  # few rows take none
+    assert lora(lib, n=0, **big) == SCRATCH and lora(lib, n=4, **big) == SCRATCH
     assert lora(lib, ws=None) == ARG and lora(lib, ws=P[8] + 4) == ARG
     assert lora(lib, M=0, X=None, Y=None) == OK
     assert lora(lib, N=0, B=None, Y=None, H=None) == OK
@@ -121,6 +122,7 @@ def test_workspaces(lib):
         assert lib.sgemm_orthogonalize_workspace(*sizes) >= 0, sizes
     # Sizes stay in range at the largest arguments.
     big = (1 << 31) - 1
+    assert lib.sgemm_lora_workspace(0, 2, 1, 4096, 4096, 16, 8) == 0
     assert 0 < lib.sgemm_lora_workspace(0, 0, big, big, big, 256, 4096) < 1 << 60
     assert 0 < lib.sgemm_lora_workspace(1, 0, big, big, big, 256, 4096) < 1 << 60
     assert 0 < lib.sgemm_orthogonalize_workspace(65535, 65536, 65536) < 1 << 60

@@ -29,6 +29,20 @@ void expand_rows(const ExpandArgs& a, dim3 grid, hipStream_t s) {
     run(std::integral_constant<int, EXPAND_HELD>{});
 }
 
+// Single rows.
+template <int T>
+void expand_one(const ExpandArgs& a, dim3 grid, hipStream_t s) {
+    constexpr int V = kVec<T>;
+    auto run = [&](auto lanes) {
+        constexpr int G = decltype(lanes)::value;
+        if (a.R % V != 0) hipLaunchKernelGGL((lora_expand_one<T, G, true>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((lora_expand_one<T, G, false>), grid, dim3(256), 0, s, a);
+    };
+    if (a.R <= V) run(std::integral_constant<int, 1>{});
+    else if (a.R <= 2 * V) run(std::integral_constant<int, 2>{});
+    else run(std::integral_constant<int, 4>{});
+}
+
 // Tiles of 64 rows.
 template <int T>
 void expand_tiles(const ExpandArgs& a, dim3 grid, hipStream_t s) {
@@ -118,7 +132,8 @@ hipError_t launch_shrink(int type, const ShrinkArgs& a, const PassPlan& p, hipSt
 hipError_t launch_expand(int type, const ExpandArgs& a, const PassPlan& p, hipStream_t s) {
     const dim3 grid(grid_for(p.tiles), unsigned(ceil_div(a.N > 0 ? a.N : 1, a.nshare)));
     return by_type(type, [&](auto t) {
-        if (p.tmb == 1) expand_rows<decltype(t)::value>(a, grid, s);
+        if (p.mode == RowPlan::SINGLE) expand_one<decltype(t)::value>(a, grid, s);
+        else if (p.tmb == 1) expand_rows<decltype(t)::value>(a, grid, s);
         else expand_tiles<decltype(t)::value>(a, grid, s);
     });
 }

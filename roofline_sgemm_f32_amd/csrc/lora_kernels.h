@@ -647,6 +647,86 @@ lora_expand_tiles(ExpandArgs a) {
     }
 }
 
+// Y of single rows, each with an adapter of its own: G neighbouring lanes share a
+// column's sum, so that a wave reads the adapter in one piece, and H is in LDS in
+// float.  On the vector units: with one row the matrix instructions' other fifteen
+// would be empty, and what counts is how soon the loads are out (64 rows x 8192 of
+// rank 16: 5.9 us, lora_expand 9.1).
+constexpr int kOneCols = 4;  // columns of a lane group in flight
+
+template <int T, int G, bool ODD>
+__global__ void __launch_bounds__(256) lora_expand_one(ExpandArgs a) {
+    using E = typename Elem<T>::type;
+    constexpr int V = kVec<T>, COLS = 256 / G;  // columns of a workgroup at a time
+    __shared__ __attribute__((aligned(16))) float h[256 + 16];
+    const int lane = threadIdx.x % G, at = threadIdx.x / G;
+    const int64_t m = blockIdx.x;
+    const int64_t nb = blockIdx.y * a.nshare, ne = nb + a.nshare < a.N ? nb + a.nshare : a.N;
+    const int l = __builtin_amdgcn_readfirstlane(adapter_of(a.rows.ids, a.rows.id64, a.rows.L, m));
+    const bool has = l >= 0;
+    if (!has && a.base == a.Y && !a.H) return;
+    const float s = has ? a.alpha * (a.scales ? a.scales[l] : 1.0f) : 0.0f;
+    const E* const w = static_cast<const E*>(a.W) + (has ? l : 0) * a.sw;
+    const E* const base = static_cast<const E*>(a.base) + m * a.ldbase;
+    E* const out = static_cast<E*>(a.Y) + m * a.ldy;
+    // The first columns' pieces, before H is known.
+    u32x4 first[kOneCols];
+    float b[kOneCols];
+    auto fetch = [&](int64_t n0) {
+#pragma unroll
+        for (int q = 0; q < kOneCols; q++) {
+            const int64_t n = n0 + q * COLS + at < a.N ? n0 + q * COLS + at : a.N - 1;
+            if (has) first[q] = load_ranks<T, ODD>(w + n * a.ldw, lane * V, a.R);
+            b[q] = a.base ? float(base[n]) : 0.0f;
+        }
+    };
+    if (nb < ne) fetch(nb);
+    const int hp = lora_pitch(a.R);
+    for (int r = threadIdx.x; r < hp; r += 256) {
+        float v = 0.0f;
+        if (has) {
+            const float* const p = a.P + m * hp + r;
+            float q[8];
+#pragma unroll
+            for (int z = 0; z < 8; z++) q[z] = p[(z < a.planes ? z : 0) * a.plane];
+#pragma unroll
+            for (int z = 0; z < 8; z++) v += z < a.planes ? q[z] : 0.0f;
+        }
+        h[r] = r < a.R ? v : 0.0f;
+        if (a.H && blockIdx.y == 0 && r < a.R) a.H[m * a.ldh + r] = v;
+    }
+    __syncthreads();
+    for (int64_t n0 = nb; n0 < ne; n0 += kOneCols * COLS) {
+        float v[kOneCols] = {};
+        if (has)
+            for (int r = lane * V; r < a.R; r += G * V) {
+                float x[V];
+#pragma unroll
+                for (int e = 0; e < V; e += 4) {
+                    const v4f y = *reinterpret_cast<const v4f*>(&h[r + e]);
+                    x[e] = y[0], x[e + 1] = y[1], x[e + 2] = y[2], x[e + 3] = y[3];
+                }
+#pragma unroll
+                for (int q = 0; q < kOneCols; q++) {
+                    const int64_t n = n0 + q * COLS + at < a.N ? n0 + q * COLS + at : a.N - 1;
+                    float f[V];
+                    unpack<T>(r == lane * V ? first[q] : load_ranks<T, ODD>(w + n * a.ldw, r, a.R), f);
+                    // A zero of H past R may meet no more than a zero.
+#pragma unroll
+                    for (int e = 0; e < V; e++) v[q] = fmaf(x[e], f[e], v[q]);
+                }
+            }
+#pragma unroll
+        for (int q = 0; q < kOneCols; q++) {
+#pragma unroll
+            for (int d = 1; d < G; d *= 2) v[q] += __shfl_xor(v[q], d);
+            const int64_t n = n0 + q * COLS + at;
+            if (lane == 0 && n < ne) out[n] = E(!has ? b[q] : a.base ? b[q] + s * v[q] : s * v[q]);
+        }
+        if (n0 + kOneCols * COLS < ne) fetch(n0 + kOneCols * COLS);
+    }
+}
+
 // ---- few rows ------------------------------------------------------------------
 
 // A row's Y, 512 columns a workgroup, in one launch: every workgroup forms the row's

@@ -11,10 +11,10 @@ struct GroupArgs {
     int M, L;
     int waves;         // set by the launcher
     int* order;        // M
-    int tile;          // rows of a tile
+    int tile_shift;    // a tile's rows: 2^tile_shift
     int* tiles;        // number of tiles, 3 unused, then adapter, start, count, place among
                        // its adapter's of each
-    int chunk;         // the same for chunks of `chunk` rows, rows without adapter left out
+    int chunk_shift;   // the same for chunks of 2^chunk_shift rows, rows without adapter left out
     int* chunks;       // (null: none)
     int* chunk_start;  // L + 1: chunks before an adapter's
     int* slot_start;   // L + 1: the same of adapters with more than one

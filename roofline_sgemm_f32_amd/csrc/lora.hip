@@ -174,7 +174,7 @@ hipError_t launch_lora(const LoraArgs& g, hipStream_t s) {
     const RowPlan rows{p.mode, g.ids, g.id64, int(g.M), g.L, order, head};
     hipError_t e = hipSuccess;
     if (p.mode == RowPlan::SORTED) {
-        const GroupArgs a{g.ids, g.id64, int(g.M), g.L, 0, order, 16 * p.tmb, head, 0, nullptr, nullptr, nullptr};
+        const GroupArgs a{g.ids, g.id64, int(g.M), g.L, 0, order, p.tmb == 1 ? 4 : 6, head, 0, nullptr, nullptr, nullptr};
         if ((e = launch_lora_group(a, s)) != hipSuccess) return e;
     }
     float* const P = reinterpret_cast<float*>(ws + p.p_at);

@@ -406,7 +406,8 @@ hipError_t launch_lora_backward(const LoraGradArgs& b, hipStream_t s) {
             int* const order = reinterpret_cast<int*>(ws + p.pass.order_at);
             int* const head = reinterpret_cast<int*>(ws + p.pass.tiles_at);
             int* const ch = reinterpret_cast<int*>(ws + p.chunks_at);
-            group = {g.ids, g.id64, int(g.M), g.L, 0, order, 16 * p.pass.tmb, head, p.chunk, ch,
+            group = {g.ids, g.id64, int(g.M), g.L, 0, order, p.pass.tmb == 1 ? 4 : 6, head,
+                     __builtin_ctz(p.chunk), ch,
                      reinterpret_cast<int*>(ws + p.chunk_start_at), reinterpret_cast<int*>(ws + p.slot_start_at)};
             rows = {RowPlan::SORTED, g.ids, g.id64, int(g.M), g.L, order, head};
             chunks = rows;

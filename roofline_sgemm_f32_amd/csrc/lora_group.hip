@@ -8,70 +8,82 @@ namespace {
 constexpr int kGroupThreads = 1024;
 constexpr int kHeld = 8192;
 
-// Exclusive prefix sums of n ints in LDS, in the order at(0), at(1), ...; returns
-// the total.  Every thread of the workgroup calls it.
-template <class At>
-__device__ int scan(int n, At at) {
+// Exclusive prefix sums of n ints in LDS; returns the total.  Every thread of the
+// workgroup calls it.
+__device__ __forceinline__ int scan(int* v, int n) {
     __shared__ int part[kGroupThreads / 64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int each = (n + kGroupThreads - 1) / kGroupThreads;
     const int lo = min(int(threadIdx.x) * each, n), hi = min(lo + each, n);
     int sum = 0;
 #pragma unroll 1
-    for (int e = lo; e < hi; e++) sum += at(e);
+    for (int e = lo; e < hi; e++) sum += v[e];
     int incl = sum;
 #pragma unroll 1
     for (int d = 1; d < 64; d *= 2) {
         const int up = __shfl_up(incl, d);
-        if (int(threadIdx.x & 63) >= d) incl += up;
+        if (lane >= d) incl += up;
     }
+    if (lane == 63) part[wave] = incl;
     __syncthreads();
-    if ((threadIdx.x & 63) == 63) part[threadIdx.x >> 6] = incl;
-    __syncthreads();
-    int before = incl - sum, total = 0;
+    // The waves' sums, added the same way by every wave.
+    int waves = part[lane & (kGroupThreads / 64 - 1)];
 #pragma unroll 1
-    for (int w = 0; w < kGroupThreads / 64; w++) {
-        if (w < int(threadIdx.x >> 6)) before += part[w];
-        total += part[w];
+    for (int d = 1; d < kGroupThreads / 64; d *= 2) {
+        const int up = __shfl_up(waves, d, kGroupThreads / 64);
+        if ((lane & (kGroupThreads / 64 - 1)) >= d) waves += up;
     }
+    const int total = __shfl(waves, kGroupThreads / 64 - 1), before_wave = wave ? __shfl(waves, wave - 1) : 0;
+    int before = before_wave + incl - sum;
 #pragma unroll 1
     for (int e = lo; e < hi; e++) {
-        const int v = at(e);
-        at(e) = before;
-        before += v;
+        const int x = v[e];
+        v[e] = before;
+        before += x;
     }
     __syncthreads();
     return total;
 }
 
 // One workgroup.  Each of `waves` waves has a run of rows of its own: it counts
-// its ids in a table of its own, the tables' prefix sums over (adapter, wave)
-// are where its rows of an adapter go, and it deals them out in order, 64 rows
-// at a time, a row's place among equal ids of the 64 from ballots; the last of the equals counts for all (LDS atomics on one address take
-// their turns).  Rows without adapter come last.  Up to kHeld rows' groups and
-// places stay in LDS between the two passes.  The loops are not unrolled: the code runs
-// once, on one CU, and fetching it takes longer than running it.
+// its ids, the counts' prefix sums over (adapter, wave) are where its rows of an
+// adapter go, and it deals them out in order, 64 rows at a time, a row's place
+// among equal ids of the 64 from ballots; the last of the equals counts for all
+// (LDS atomics on one address take their turns).  Rows without adapter come last.
+// Up to kHeld rows' groups and places stay in LDS between the two passes.  The
+// loops are not unrolled and the code is short: it runs once, on one CU, and is
+// fetched from memory first.
 __device__ __forceinline__ void group_rows(const GroupArgs& a, int* lds) {
-    const int groups = a.L + 1;                  // the last: no adapter
-    int* const first = lds;                      // groups + 1: tiles before a group's
-    int* const table = lds + groups + 1;         // waves x groups
+    const int groups = a.L + 1;           // the last: no adapter
+    int* const first = lds;               // groups + 1: tiles before a group's
+    int* const table = lds + groups + 1;  // groups x waves
     __shared__ uint16_t held[kHeld], place[kHeld];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t run = ((a.M + a.waves - 1) / a.waves + 63) / 64 * 64;
-    const int64_t begin = wave * run, end = wave >= a.waves ? 0 : begin + run < a.M ? begin + run : a.M;
+    const int run = ((a.M + a.waves - 1) / a.waves + 63) / 64 * 64;
+    const int64_t begin = int64_t(wave) * run, end = wave >= a.waves ? 0 : begin + run < a.M ? begin + run : a.M;
     auto group_of = [&](int64_t m) {
         const int l = adapter_of(a.ids, a.id64, a.L, m);
         return l < 0 ? a.L : l;
     };
-#pragma unroll 8
-    for (int m = threadIdx.x; m < (a.M < kHeld ? a.M : kHeld); m += kGroupThreads) held[m] = uint16_t(group_of(m));
+    const int h = a.M < kHeld ? a.M : kHeld;
+#pragma unroll 1
+    for (int m = threadIdx.x; m < h; m += 4 * kGroupThreads) {
+        // Four in flight; past the end the last one again.
+        int l[4];
+#pragma unroll
+        for (int u = 0; u < 4; u++) l[u] = group_of(min(m + u * kGroupThreads, h - 1));
+#pragma unroll
+        for (int u = 0; u < 4; u++) held[min(m + u * kGroupThreads, h - 1)] = uint16_t(l[u]);
+    }
 #pragma unroll 1
     for (int e = threadIdx.x; e < a.waves * groups; e += kGroupThreads) table[e] = 0;
     // The wave's own counts, written by any lane of it: a barrier to the compiler
     // orders the accesses (volatile ones would leave the LDS instructions: they took
     // 1.4 us for each 1024 rows).
-    int* const mine = table + wave * groups;
-    // Pass 0 counts, pass 1 deals out (without counting again where all
-    // places are held).
+    int* const mine = table + wave;
+    const int w = a.waves;
+    // Pass 0 counts, pass 1 deals out (without counting again where all places are
+    // held).
 #pragma unroll 1
     for (int pass = 0; pass < 2; pass++) {
         __syncthreads();
@@ -81,7 +93,7 @@ __device__ __forceinline__ void group_rows(const GroupArgs& a, int* lds) {
             const bool in = m < end;
             const int l = !in ? 0 : m < kHeld ? held[m] : group_of(m);
             if (pass && a.M <= kHeld) {
-                if (in) a.order[mine[l] + place[m]] = int(m);
+                if (in) a.order[mine[l * w] + place[m]] = int(m);
                 continue;
             }
             // Lanes with the same id: of up to three ids one by one (runs of rows), else
@@ -101,32 +113,32 @@ __device__ __forceinline__ void group_rows(const GroupArgs& a, int* lds) {
                     same &= l >> b & 1 ? set : ~set;
                 }
             }
-            const int at = in ? mine[l] + __popcll(same & ((uint64_t(1) << lane) - 1)) : 0;
+            const int at = in ? mine[l * w] + __popcll(same & ((uint64_t(1) << lane) - 1)) : 0;
             asm volatile("" ::: "memory");
             if (in && pass) a.order[at] = int(m);
             if (in && m < kHeld) place[m] = uint16_t(at);
-            if (in && same >> lane == 1) mine[l] = at + 1;
+            if (in && same >> lane == 1) mine[l * w] = at + 1;
             asm volatile("" ::: "memory");
         }
         if (pass) break;
-        __syncthreads();
-        scan(a.waves * groups, [&](int e) -> int& { return table[e % a.waves * groups + e / a.waves]; });
-        // table[l] is now where adapter l's rows start.
-        auto start_of = [&](int l) { return l < groups ? table[l] : a.M; };
-        // Tiles, chunks, and the chunks of adapters that have more than one.
+        // Where every wave's rows of every group start; then tiles, chunks, and the
+        // chunks of adapters that have more than one.  table[l w] is where l's rows start.
+        auto start_of = [&](int l) { return l < groups ? table[l * w] : a.M; };
 #pragma unroll 1
-        for (int kind = 0; kind < 3; kind++) {
-            const int size = kind ? a.chunk : a.tile;
-            int* const head = kind ? a.chunks : a.tiles;
+        for (int kind = -1; kind < 3; kind++) {
+            const int shift = kind > 0 ? a.chunk_shift : a.tile_shift, size = 1 << shift;
+            int* const head = kind > 0 ? a.chunks : a.tiles;
             if (!head) continue;
-            const int last = kind ? a.L : groups;  // chunks are of adapters only
+            const int last = kind > 0 ? a.L : groups;  // chunks are of adapters only
+            if (kind >= 0)
 #pragma unroll 1
-            for (int l = threadIdx.x; l < last; l += kGroupThreads) {
-                const int n = (start_of(l + 1) - start_of(l) + size - 1) / size;
-                first[l] = kind == 2 && n == 1 ? 0 : n;
-            }
+                for (int l = threadIdx.x; l < last; l += kGroupThreads) {
+                    const int n = (start_of(l + 1) - start_of(l) + size - 1) >> shift;
+                    first[l] = kind == 2 && n == 1 ? 0 : n;
+                }
             __syncthreads();
-            const int total = scan(last, [&](int e) -> int& { return first[e]; });
+            const int total = scan(kind < 0 ? table : first, kind < 0 ? w * groups : last);
+            if (kind < 0) continue;
             int* const starts = kind == 1 ? a.chunk_start : kind == 2 ? a.slot_start : nullptr;
             if (starts)
                 for (int l = threadIdx.x; l <= last; l += kGroupThreads) starts[l] = l < last ? first[l] : total;
@@ -139,7 +151,7 @@ __device__ __forceinline__ void group_rows(const GroupArgs& a, int* lds) {
                     if (first[mid] <= t) lo = mid;
                     else hi = mid - 1;
                 }
-                const int s = start_of(lo) + (t - first[lo]) * size, n = start_of(lo + 1) - s;
+                const int s = start_of(lo) + ((t - first[lo]) << shift), n = start_of(lo + 1) - s;
                 reinterpret_cast<int4*>(head)[1 + int64_t(t)] =
                     int4{lo < a.L ? lo : -1, s, n < size ? n : size, t - first[lo]};
             }

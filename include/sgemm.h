@@ -425,8 +425,8 @@ int sgemm_lora_backward(int type, int64_t M, int64_t N, int64_t K, int64_t R, in
  *   The norm is summed in double.  Matrices with a side of up to 64 are computed
  * in double.  For others X and S are kept between the steps as two float16 parts
  * each, 22 bits, times a power of two, and products are summed in float.  The power comes from a bound of X that follows from the coefficients
- * alone (|X| <= 1 at the start); coefficients that are not finite or let it pass
- * 64 are SGEMM_ERR_ARG.  A matrix of zeros gives zeros; an infinity or NaN in G
+ * alone (|X| <= 1 at the start); coefficients that are not finite, let it pass 64
+ * or bring it below 2^-40 are SGEMM_ERR_ARG.  A matrix of zeros gives zeros; an infinity or NaN in G
  * makes its matrix's results NaN.
  *   `workspace`: at least sgemm_orthogonalize_workspace bytes, 256-byte aligned.
  * No allocation, no synchronisation, every call can be captured. */

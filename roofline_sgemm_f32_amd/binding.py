@@ -696,14 +696,14 @@ def lora_backward(dY, X, A, B, H, ids=None, scale=1.0, base=None, need_dx=True, 
     lddx = ldda = lddb = 1
     sda = sdb = 0
     if need_dx:
-        dX = torch.empty((M, K), dtype=t, device=X.device) if dX is None else dX
+        dX = X.new_empty((M, K)) if dX is None else dX
         lddx = _rows(dX, "dX", (M, K), (t,))
     else:
         dX = None
     dA = dB = None
     if need_dw:
         dA, dB = _two(dW, "dW") if dW is not None else (
-            torch.empty((L, R, K), dtype=t, device=X.device), torch.empty((L, N, R), dtype=t, device=X.device))
+            X.new_empty((L, R, K)), X.new_empty((L, N, R)))
         (ldda, sda), (lddb, sdb) = _stack(dA, "dA", (L, R, K), t), _stack(dB, "dB", (L, N, R), t)
     sizes = (_FLOATS[t], M, N, K, R, L)
     ws, at, n = _workspace(X, "sgemm_lora_workspace", 1, *sizes)
@@ -732,30 +732,43 @@ def orthogonalize(G, steps=5, coefficients=MUON, eps=1e-7, out=None):
     _FLOATS or _use_torch()
     if not isinstance(G, torch.Tensor) or G.dtype not in _FLOATS:
         raise TypeError(f"G must be a tensor of {' or '.join(str(d) for d in _FLOATS)}")
-    if G.dim() not in (2, 3):
+    t, shape = G.dtype, G.shape
+    if len(shape) == 2:
+        batch, (M, N) = 1, shape
+    elif len(shape) == 3:
+        batch, M, N = shape
+    else:
         raise ValueError("G must be a matrix or a stack of matrices")
-    coef = _triples(coefficients, steps)
-    g3 = G if G.dim() == 3 else G.unsqueeze(0)
-    ldg, sg = _stack(g3, "G", None, G.dtype)
+    try:
+        coef = _triples(coefficients, steps)
+    except TypeError:  # lists, which have no hash
+        coef = _triples(tuple(tuple(r) if isinstance(r, list) else r for r in coefficients), steps)
+    ldg, sg = _matrices(G, "G", shape, t)
     if out is None:
-        out = torch.empty(G.shape, dtype=G.dtype, device=G.device)
-    elif not isinstance(out, torch.Tensor) or out.shape != G.shape:
+        out = G.new_empty(shape)
+    elif not isinstance(out, torch.Tensor) or out.shape != shape:
         raise ValueError("out has the wrong shape")
-    ldo, so = _stack(out if out.dim() == 3 else out.unsqueeze(0), "out", tuple(g3.shape), G.dtype)
-    batch, M, N = g3.shape
+    ldo, so = _matrices(out, "out", shape, t)
     ws, at, n = _workspace(G, "sgemm_orthogonalize_workspace", batch, M, N)
-    _call(load().sgemm_orthogonalize, "sgemm_orthogonalize", G, (out,), _FLOATS[G.dtype], batch, M, N,
-          G.data_ptr(), ldg, sg, out.data_ptr(), ldo, so, len(coef) // 3, coef, float(eps),
-          at, n)
+    _call(load().sgemm_orthogonalize, "sgemm_orthogonalize", G, (out,), _FLOATS[t], batch, M, N,
+          G.data_ptr(), ldg, sg, out.data_ptr(), ldo, so, len(coef) // 3, coef, eps, at, n)
     return out
 
 
+def _matrices(t, name, shape, dtype):
+    """(row stride, matrix stride) of a matrix or a stack of them, checked."""
+    if len(shape) == 2:
+        return _rows(t, name, tuple(shape), (dtype,)), 0
+    return _stack(t, name, tuple(shape), dtype)
+
+
+@functools.lru_cache(maxsize=64)
 def _triples(coefficients, steps):
-    """The coefficients of every step as a C array of doubles."""
+    """The coefficients of every step as a C array of doubles, which is only read."""
     rows = list(coefficients)
     if rows and not isinstance(rows[0], (tuple, list)):
         rows = [rows] * int(steps)
-    if not rows or any(len(r) != 3 for r in rows):
+    if not rows or any(not isinstance(r, (tuple, list)) or len(r) != 3 for r in rows):
         raise ValueError("coefficients must be a triple (a, b, c), or one triple for each step")
     flat = [float(v) for r in rows for v in r]
     return (ctypes.c_double * len(flat))(*flat)

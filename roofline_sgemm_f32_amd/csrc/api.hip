@@ -255,7 +255,7 @@ bool ortho_bounds(int steps, const double* coef, double* bounds) {
             if (q > 0 && q < r * r) top = std::max(top, p(q));
         // Roundings of a step and of its result, counted generously.
         r = top * 1.01;
-        if (!(r <= 64.0)) return false;
+        if (!(r <= 64.0) || r < 0x1p-40) return false;
         // The factor a + b s^2 + c s^4 is stored too.
         if (!(std::fabs(a) + std::fabs(b) * bounds[i] * bounds[i] + std::fabs(c) * std::pow(bounds[i], 4) <= 1e9))
             return false;

@@ -59,8 +59,8 @@ __device__ __forceinline__ void group_rows(const GroupArgs& a, int* lds) {
     int* const table = lds + groups + 1;  // groups x waves
     __shared__ uint16_t held[kHeld], place[kHeld];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int run = ((a.M + a.waves - 1) / a.waves + 63) / 64 * 64;
-    const int64_t begin = int64_t(wave) * run, end = wave >= a.waves ? 0 : begin + run < a.M ? begin + run : a.M;
+    const int64_t run = ((int64_t(a.M) + a.waves - 1) / a.waves + 63) / 64 * 64;
+    const int64_t begin = wave * run, end = wave >= a.waves ? 0 : begin + run < a.M ? begin + run : a.M;
     auto group_of = [&](int64_t m) {
         const int l = adapter_of(a.ids, a.id64, a.L, m);
         return l < 0 ? a.L : l;
@@ -133,7 +133,7 @@ __device__ __forceinline__ void group_rows(const GroupArgs& a, int* lds) {
             if (kind >= 0)
 #pragma unroll 1
                 for (int l = threadIdx.x; l < last; l += kGroupThreads) {
-                    const int n = (start_of(l + 1) - start_of(l) + size - 1) >> shift;
+                    const int n = int((uint32_t(start_of(l + 1) - start_of(l)) + size - 1) >> shift);
                     first[l] = kind == 2 && n == 1 ? 0 : n;
                 }
             __syncthreads();

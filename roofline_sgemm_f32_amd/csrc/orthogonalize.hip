@@ -423,7 +423,7 @@ ortho_product(ProductArgs a) {
                 float v[4];
 #pragma unroll
                 for (int e = 0; e < 4; e++) v[e] = SPLIT ? acc[m][n][4 * g + e] : acc[m][n][4 * g + e] * a.scale;
-                if constexpr (EPI == POLY && !SPLIT) {
+                if constexpr (EPI == POLY) {
                     // S[r + e][c] as S[c][r + e].
                     if (r < a.K) {
                         const _Float16* at = a.A + z * a.stride_a + c * a.K * 2 + part_at(r);
@@ -470,15 +470,15 @@ ortho_product(ProductArgs a) {
     }
 }
 
-// The shares' sums added in order, then as above: 64 x 64 of a tile a workgroup.
-template <int SIDE, int EPI>
+// S from the shares' sums, added in order: 64 x 64 of a tile a workgroup.
+template <int SIDE>
 __global__ void __launch_bounds__(256) ortho_finish(ProductArgs a, int tiles, int shares) {
     __shared__ float tile[64][68];
     constexpr int B = SIDE / 64;
     const int64_t z = blockIdx.z;
     const int t = blockIdx.x / (B * B), by = blockIdx.x % (B * B) / B, bx = blockIdx.x % B;
     int ti, tj;
-    tile_of<EPI>(a, t, ti, tj);
+    tile_of<GRAM>(a, t, ti, tj);
     const int64_t r0 = int64_t(ti) * SIDE + 64 * by, c0 = int64_t(tj) * SIDE + 64 * bx;
     const float* const from = a.partial + (z * shares * tiles + t) * SIDE * SIDE + int64_t(64 * by) * SIDE + 64 * bx;
     const int64_t plane = int64_t(tiles) * SIDE * SIDE;
@@ -489,42 +489,22 @@ __global__ void __launch_bounds__(256) ortho_finish(ProductArgs a, int tiles, in
         const float* at = from + y * SIDE + cx;
 #pragma unroll 4
         for (int s = 0; s < shares; s++) v += *reinterpret_cast<const v4f*>(at + s * plane);
-        v *= a.scale;
-        if constexpr (EPI == POLY) {
-            const int64_t r = r0 + y, c = c0 + cx;
-            if (c < a.K) {
-                const _Float16* p = a.A + z * a.stride_a + r * a.K * 2 + part_at(c);
-                const f16x4 h = *reinterpret_cast<const f16x4*>(p), l = *reinterpret_cast<const f16x4*>(p + 32);
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    v[i] = fmaf(a.b, float(h[i]) + float(l[i]), v[i]);
-                    if (c + i == r) v[i] += a.diagonal;
-                }
-            }
-        }
-        *reinterpret_cast<v4f*>(&tile[y][cx]) = v;
+        *reinterpret_cast<v4f*>(&tile[y][cx]) = v * a.scale;
     }
     __syncthreads();
-    if constexpr (EPI == LAST) {
-        for (int e = threadIdx.x; e < 4096; e += 256) {
-            if (a.tall) store_out(a, z, r0 + e % 64, c0 + e / 64, tile[e % 64][e / 64]);
-            else store_out(a, z, r0 + e / 64, c0 + e % 64, tile[e / 64][e % 64]);
-        }
-    } else {
-        for (int e = threadIdx.x; e < 512; e += 256) {
-            const int y = e / 8, cx = e % 8 * 8;
-            float v[8];
+    for (int e = threadIdx.x; e < 512; e += 256) {
+        const int y = e / 8, cx = e % 8 * 8;
+        float v[8];
 #pragma unroll
-            for (int i = 0; i < 8; i++) v[i] = tile[y][cx + i];
-            store_row(a, z, r0 + y, c0 + cx, v);
-        }
-        if (!((EPI == GRAM || EPI == POLY) && ti == tj))
-            for (int e = threadIdx.x; e < 1024; e += 256) {
-                const int y = e % 16 * 4, cx = e / 16;
-                const float v[4] = {tile[y][cx], tile[y + 1][cx], tile[y + 2][cx], tile[y + 3][cx]};
-                store_column(a, z, r0 + y, c0 + cx, v);
-            }
+        for (int i = 0; i < 8; i++) v[i] = tile[y][cx + i];
+        store_row(a, z, r0 + y, c0 + cx, v);
     }
+    if (ti != tj)
+        for (int e = threadIdx.x; e < 1024; e += 256) {
+            const int y = e % 16 * 4, cx = e / 16;
+            const float v[4] = {tile[y][cx], tile[y + 1][cx], tile[y + 2][cx], tile[y + 3][cx]};
+            store_column(a, z, r0 + y, c0 + cx, v);
+        }
 }
 
 // ---- host ---------------------------------------------------------------------------
@@ -535,14 +515,17 @@ struct ProductPlan {
     int64_t tiles;            // of a matrix
 };
 
-// The cheapest by a model of rounds of workgroups over the 256 CUs: a step's
-// time with every CU busy (us), measured on 4096 x 4096 and 1024 x 4096.
-ProductPlan product_plan(bool half, int64_t rows, int64_t cols, int64_t K, int64_t batch) {
+// The cheapest by a model of rounds of workgroups over the 256 CUs, fitted (us) to
+// every configuration and 1 to 8 shares on ten shapes of 256 x 256 to 4096 x 4096.  For
+// example S of 4096 x 4096: tiles of 64 242, 128 250, 192 199, 256 250; P X there 471,
+// 375, 383, 317; S of 1024 x 4096: 29, 68, 149, 217, and 29 and 30 in three and four
+// shares of tiles of 64 and 128; P X of 2048 x 2048: 61, 55, 94, 131.
+ProductPlan product_plan(bool half, bool long_sum, int64_t rows, int64_t cols, int64_t K, int64_t batch) {
     struct Option {
-        int side, per_cu;
-        double step, fixed;
+        int side;
+        double step, tile;  // of a workgroup, with every CU busy
     };
-    static const Option options[] = {{64, 2, 0.45, 3.0}, {128, 2, 1.45, 5.0}, {192, 1, 1.15, 8.0}, {256, 1, 1.6, 10.0}};
+    static const Option options[] = {{64, 0.23, 0.8}, {128, 0.72, 5.0}, {192, 1.48, 8.0}, {256, 2.42, 8.0}};
     ProductPlan best{};
     double least = 0;
     const int64_t steps = ceil_div(K, kStep);
@@ -550,13 +533,16 @@ ProductPlan product_plan(bool half, int64_t rows, int64_t cols, int64_t K, int64
         const int64_t tm = ceil_div(rows, o.side), tn = ceil_div(cols, o.side);
         const int64_t tiles = half ? tm * (tm + 1) / 2 : tm * tn;
         for (int shares : {1, 2, 3, 4, 6, 8, 12, 16}) {
-            if (shares > 1 && steps / shares < 4) break;
+            // Only S has sums long enough against its tiles.
+            if (shares > 1 && (!long_sum || steps / shares < 4)) break;
             const int64_t share = ceil_div(steps, shares), n = ceil_div(steps, share);
-            const int64_t units = tiles * n * batch, slots = 256 * o.per_cu;
-            // A round with one workgroup a CU takes about half of one with two.
-            const double rounds = o.per_cu == 2 && units <= 256 ? 0.6 : double(ceil_div(units, slots));
-            double us = rounds * (double(share) * o.step + o.fixed);
-            if (n > 1) us += 5.0 + double(tiles * batch * o.side * o.side) * double(n) * 8 / 4e6;
+            const double u = double(tiles * n * batch) / 256, whole = std::floor(u), part = u - whole;
+            // Two workgroups of tiles of 64 run on a CU at a time, which evens the rounds
+            // out; one of larger tiles, faster where fewer CUs are busy.
+            const double rounds = o.side == 64 ? std::max(1.0, std::min(u + 0.5, std::ceil(u)))
+                                               : whole + (part > 0 ? 0.65 + 0.35 * part : 0.0);
+            double us = 4.0 + rounds * (double(share) * o.step + o.tile);
+            if (n > 1) us += 6.0 + double(tiles * batch * o.side * o.side) * double(n) * 4 / 4e6;
             if (best.side == 0 || us < least) {
                 least = us;
                 best = {o.side, int(n), int(share), tiles};
@@ -582,10 +568,10 @@ OrthoPlan ortho_plan(int64_t batch, int64_t M, int64_t N) {
     p.kn = ceil_div(p.n, 32) * 32;
     p.am = p.km + 256;
     p.an = p.kn + 256;
-    p.gram = product_plan(true, p.m, p.m, p.n, batch);
-    p.poly = product_plan(true, p.m, p.m, p.m, batch);
-    p.apply = product_plan(false, p.m, p.n, p.m, batch);
-    size_t at = 0, partial = 0;
+    p.gram = product_plan(true, true, p.m, p.m, p.n, batch);
+    p.poly = product_plan(true, false, p.m, p.m, p.m, batch);
+    p.apply = product_plan(false, false, p.m, p.n, p.m, batch);
+    size_t at = 0;
     auto take = [&](size_t n) {
         const size_t here = at;
         at += (n + 255) / 256 * 256;
@@ -597,9 +583,7 @@ OrthoPlan ortho_plan(int64_t batch, int64_t M, int64_t N) {
     p.xt_at[1] = take(size_t(batch) * p.an * p.km * 4);
     p.s_at = take(size_t(batch) * p.am * p.km * 4);
     p.p_at = take(size_t(batch) * p.am * p.km * 4);
-    for (const ProductPlan* q : {&p.gram, &p.poly, &p.apply})
-        if (q->shares > 1) partial = std::max(partial, size_t(batch) * q->shares * q->tiles * q->side * q->side * 4);
-    p.partial_at = take(partial);
+    p.partial_at = take(p.gram.shares > 1 ? size_t(batch) * p.gram.shares * p.gram.tiles * p.gram.side * p.gram.side * 4 : 0);
     p.bytes = at;
     return p;
 }
@@ -614,14 +598,16 @@ int power_for(double bound) {
 template <class CF, int EPI>
 void launch_tiles(const ProductArgs& a, const ProductPlan& p, unsigned batch, hipStream_t s) {
     const dim3 grid(unsigned(p.tiles), p.shares, batch), block(64 * CF::WAVES);
-    if (p.shares == 1) {
-        hipLaunchKernelGGL((ortho_product<CF, EPI, false>), grid, block, 0, s, a);
-    } else {
-        hipLaunchKernelGGL((ortho_product<CF, EPI, true>), grid, block, 0, s, a);
-        constexpr int B = CF::SIDE / 64;
-        hipLaunchKernelGGL((ortho_finish<CF::SIDE, EPI>), dim3(unsigned(p.tiles * B * B), 1, batch), dim3(256), 0, s, a,
-                           int(p.tiles), p.shares);
+    if constexpr (EPI == GRAM) {
+        if (p.shares > 1) {
+            hipLaunchKernelGGL((ortho_product<CF, EPI, true>), grid, block, 0, s, a);
+            constexpr int B = CF::SIDE / 64;
+            hipLaunchKernelGGL(ortho_finish<CF::SIDE>, dim3(unsigned(p.tiles * B * B), 1, batch), dim3(256), 0, s, a,
+                               int(p.tiles), p.shares);
+            return;
+        }
     }
+    hipLaunchKernelGGL((ortho_product<CF, EPI, false>), grid, block, 0, s, a);
 }
 
 template <int EPI>

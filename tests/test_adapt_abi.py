@@ -97,7 +97,8 @@ def test_ortho_refusals(lib):
     assert ortho(lib, t=3) == ARG and ortho(lib, steps=0) == ARG and ortho(lib, steps=65) == ARG
     assert ortho(lib, eps=-1.0) == ARG and ortho(lib, eps=nan) == ARG and ortho(lib, eps=inf) == ARG
     assert ortho(lib, coef=(1.0, nan, 0.0)) == ARG and ortho(lib, coef=(inf, 0.0, 0.0)) == ARG
-    assert ortho(lib, coef=(65.0, 0.0, 0.0)) == ARG
+    assert ortho(lib, coef=(65.0, 0.0, 0.0)) == ARG and ortho(lib, coef=(0.0, 0.0, 0.0)) == ARG
+    assert ortho(lib, coef=(1e-300, 0.0, 0.0)) == ARG
     assert ortho(lib, coef=(8.0, 0.0, 0.0) * 3, steps=3) == ARG       # grows past 64 in the third step
     assert ortho(lib, coef=None) == NULLPTR
     for name in ("batch", "M", "N"):

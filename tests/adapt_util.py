@@ -92,11 +92,9 @@ def lora_backward64(dY, X, A, B, H, ids, scale, base):
     return (dX, dA, dB), (eX, eA, eB)
 
 
-def ortho64(G, coefficients, eps=1e-7):
-    """The update of one matrix (or a stack) in float64 on the CPU."""
-    if G.dim() == 3:
-        return torch.stack([ortho64(g, coefficients, eps) for g in G]) if len(G) else G.double()
-    X = G.detach().cpu().double()
+def ortho64(G, coefficients, eps=1e-7, device="cpu"):
+    """The update of one matrix in float64."""
+    X = G.detach().to(device).double()
     X = X / (X.norm() + eps)
     for a, b, c in coefficients:
         S = X @ X.t()
@@ -116,12 +114,12 @@ def product_err(k):
     return 3 * Q + sum_err(k)
 
 
-def ortho_step64(G, abc, eps=1e-7):
+def ortho_step64(G, abc, eps=1e-7, device="cpu"):
     """One step in float64 and an elementwise bound of its error."""
     a, b, c = abc
-    X = G.detach().cpu().double()
+    X = G.detach().to(device).double()
     if X.shape[0] > X.shape[1]:
-        O, e = ortho_step64(G.t(), abc, eps)
+        O, e = ortho_step64(G.t(), abc, eps, device)
         return O.t(), e.t()
     X = X / (X.norm() + eps)
     m, n = X.shape
@@ -130,14 +128,15 @@ def ortho_step64(G, abc, eps=1e-7):
     S = X @ X.t()
     eS = product_err(n) * (ax @ ax.t()) + ex @ ax.t() + ax @ ex.t() + Q * S.abs() + FLOOR
     aS = S.abs() + eS
-    P = a * torch.eye(m, dtype=torch.float64) + b * S + c * (S @ S)
+    eye = torch.eye(m, dtype=torch.float64, device=device)
+    P = a * eye + b * S + c * (S @ S)
     eP = abs(b) * eS + abs(c) * (eS @ aS + aS @ eS + product_err(m) * (aS @ aS)) + Q * P.abs() + FLOOR
-    eP += 4 * U * (abs(a) * torch.eye(m, dtype=torch.float64) + abs(b) * aS + abs(c) * (aS @ aS))
+    eP += 4 * U * (abs(a) * eye + abs(b) * aS + abs(c) * (aS @ aS))
     aP = P.abs() + eP
     return P @ X, eP @ ax + aP @ ex + product_err(m) * (aP @ ax) + FLOOR
 
 
-def ortho_norm_bound(G, coefficients, eps=1e-7):
+def ortho_norm_bound(G, coefficients, eps=1e-7, device="cpu"):
     """A bound of the Frobenius norm of the error after all steps.  A step's own
     error: a sum of k products x_i y_i has partial sums of at most |x| |y|, so k
     / 16 roundings of 2 U (matrix instructions add 16 at a time) and the parts'
@@ -145,7 +144,7 @@ def ortho_norm_bound(G, coefficients, eps=1e-7):
     by the largest |p'| over the singular values reached (the divided
     differences of an odd p are at most that); the values themselves may be off
     by a little, which the factor 1.05 covers."""
-    X = G.detach().cpu().double()
+    X = G.detach().to(device).double()
     if X.shape[0] > X.shape[1]:
         X = X.t()
     X = X / (X.norm() + eps)
@@ -157,7 +156,7 @@ def ortho_norm_bound(G, coefficients, eps=1e-7):
 
     for a, b, c in coefficients:
         S = X @ X.t()
-        P = a * torch.eye(m, dtype=torch.float64) + b * S + c * S @ S
+        P = a * torch.eye(m, dtype=torch.float64, device=device) + b * S + c * S @ S
         top = float(torch.linalg.matrix_norm(X, 2))
         s = torch.linspace(0, 1.05 * top, 2001, dtype=torch.float64)
         lip = float((a + 3 * b * s ** 2 + 5 * c * s ** 4).abs().max())

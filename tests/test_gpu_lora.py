@@ -73,6 +73,74 @@ def test_backward(shape, t):
         assert guard.intact(), name
 
 
+# More rows than the sort holds at a time, in many groups and few; the most adapters.
+@pytest.mark.parametrize("M, L, kind", [(8192, 3, "mixed"), (9001, 7, "mixed"), (9000, 4096, "mixed"), (20000, 40, "runs"),
+                                        (8200, 1, "one"), (150, 4096, "mixed"), (65, 2, "none")])
+def test_many_rows(M, L, kind):
+    gen = torch.Generator().manual_seed(M)
+    N, K, R = 24, 16, 4
+    dt = (torch.float16, torch.bfloat16, torch.float32)[M % 3]
+    X, A, B, ids, scale, base = make(gen, M, N, K, R, L, dt, kind)
+    dY = torch.randn((M, N), generator=gen).to(dt)
+    of = ids.long().clamp_min(0)
+    has = (ids >= 0)[:, None].double()
+    x, a, b, sc = X.double(), A.double()[of], B.double()[of], (scale.double()[of] * has[:, 0])[:, None]
+    h = (a * x[:, None, :]).sum(2) * has
+    eh = 2 * (K + 24) * 2.0 ** -24 * (a.abs() * x.abs()[:, None, :]).sum(2)
+    d = (b * h[:, None, :]).sum(2)
+    ed = (b.abs() * (eh + (2 * (R + 24) * 2.0 ** -24 + 2.0 ** -16) * h.abs())[:, None, :]).sum(2)
+    ref = base.double() + sc * d
+    err = sc * (ed + 4 * 2.0 ** -24 * d.abs()) + 4 * 2.0 ** -24 * (ref.abs() + base.double().abs())
+    Y, H = rs.lora(X.cuda(), A.cuda(), B.cuda(), ids.cuda(), scale=scale.cuda(), base=base.cuda(), save=True)
+    assert_within(H, h, eh, "H")
+    assert_within(Y, ref, rounded(ref, err, dt), "Y")
+    Hh = torch.randn((M, R), generator=gen)
+    refs, errs = lora_backward64(dY, X, A, B, Hh, ids, scale, None)
+    got = rs.lora_backward(dY.cuda(), X.cuda(), A.cuda(), B.cuda(), Hh.cuda(), ids.cuda(), scale=scale.cuda())
+    for name, g, r, e in zip(("dX", "dA", "dB"), got, refs, errs):
+        assert_within(g, r, rounded(r, e, dt), name)
+
+
+def test_small_halves_are_not_flushed():
+    """float16 adapters and activations below its normal numbers count in full."""
+    gen = torch.Generator().manual_seed(8)
+    for M in (2, 40, 200):
+        X, A, B, ids, scale, _ = make(gen, M, 72, 96, 16, 3, torch.float16)
+        X, A, B = (v * 2.0 ** -16 if v is not B else v for v in (X, A, B)) if M == 2 else (X * 2.0 ** -17, A, B * 2.0 ** -16)
+        scale = scale * 2.0 ** 30
+        (ref, h), (err, eh) = lora64(X, A, B, ids, scale, None)
+        Y, H = rs.lora(X.cuda(), A.cuda(), B.cuda(), ids.cuda(), scale=scale.cuda(), save=True)
+        assert_within(H, h, eh, "H")
+        assert_within(Y, ref, rounded(ref, err, torch.float16), "Y")
+
+
+def test_offsets_past_32_bits():
+    """Results and activations of more than 2^32 bytes: the first and last rows."""
+    M, wide, N, K, R = 70000, 33000, 32768, 24, 4
+    gen = torch.Generator().manual_seed(11)
+    A, B = torch.randn((1, R, K), generator=gen).bfloat16(), torch.randn((1, N, R), generator=gen).bfloat16()
+    buf = torch.zeros((M, wide), dtype=torch.bfloat16, device="cuda")
+    X = buf[:, wide - K:]
+    rows = torch.tensor([0, 1, M // 2, M - 2, M - 1])
+    x = torch.randn((len(rows), K), generator=gen).bfloat16()
+    X[rows.cuda()] = x.cuda()
+    Y = rs.lora(X, A.cuda(), B.cuda())
+    (ref, _), (err, _) = lora64(x, A, B, torch.zeros(len(rows), dtype=torch.int32), torch.ones(1), None)
+    assert_within(Y[rows.cuda()], ref, rounded(ref, err, torch.bfloat16))
+    assert not Y[2].any()
+    # The same buffers as gradients: dY is Y, dX of its own.
+    ids = torch.zeros(M, dtype=torch.int32, device="cuda")
+    H = torch.zeros((M, R), device="cuda")
+    h = torch.randn((len(rows), R), generator=gen)
+    H[rows.cuda()] = h.cuda()
+    dy = Y[rows.cuda()].cpu()
+    refs, errs = lora_backward64(dy, x, A, B, h, torch.zeros(len(rows), dtype=torch.int32), torch.ones(1), None)
+    dX, dA, dB = rs.lora_backward(Y, X, A.cuda(), B.cuda(), H, ids)
+    # Sums over 70000 rows, of which these few are not zero: adding zeros rounds nothing.
+    for got, r, e in zip((dX[rows.cuda()], dA, dB), refs, errs):
+        assert_within(got, r, rounded(r, 2 * e, torch.bfloat16))
+
+
 def test_gradient_against_differences():
     """The kernels' own forward pass in float32 moved along one direction."""
     gen = torch.Generator().manual_seed(3)

@@ -52,6 +52,34 @@ def test_all_steps(shape, t, coef):
     assert float((got - ref).norm()) <= bound
 
 
+# Stacks that take each tile of each product in turn: (count, rows, columns) and the
+# tiles of S (with its shares), of P and of P X.
+STACKS = [(1, 65, 1030), (12, 640, 400), (16, 130, 2601), (16, 4097, 130), (12, 701, 699), (3, 770, 4096),
+          (16, 900, 905), (3, 1100, 4099), (12, 1300, 1299), (2, 2048, 3001), (16, 1031, 1500)]
+
+
+@pytest.mark.parametrize("shape", STACKS, ids=lambda s: "x".join(map(str, s)))
+def test_every_tile(shape):
+    """64/7 64 64; 64 64 128; 64/2 64 192; 64/2 64 256; 128 128 64; 128/3 64 256;
+    192 192 256; 192/4 64 256; 256 256 192; 256/3 64 256: one step elementwise, two
+    steps by norm, in float64 on the GPU."""
+    i = STACKS.index(shape)
+    gen = torch.Generator(device="cuda").manual_seed(i)
+    dt = list(TYPES.values())[i % 3]
+    b, m, n = shape
+    G = torch.randn(shape, generator=gen, device="cuda")
+    G += 2 * torch.randn((b, m, 1), generator=gen, device="cuda") * torch.randn((b, 1, n), generator=gen, device="cuda")
+    G = (1e-3 * G).to(dt)
+    one, two = rs.orthogonalize(G, steps=1), rs.orthogonalize(G, steps=2, coefficients=CUBIC)
+    for k in {0, b // 2, b - 1}:
+        ref, err = ortho_step64(G[k], MUON, device="cuda")
+        d = (one[k].double() - ref).abs()
+        assert bool((d <= rounded(ref, err, dt)).all()), k
+        ref = ortho64(G[k], [CUBIC] * 2, device="cuda")
+        bound = ortho_norm_bound(G[k], [CUBIC] * 2, device="cuda") + HALF_STEP[dt] * float(ref.norm())
+        assert float((two[k].double() - ref).norm()) <= bound, k
+
+
 @pytest.mark.parametrize("t", TYPES)
 @pytest.mark.parametrize("shape", [(3, 70, 40), (5, 16, 520), (2, 200, 136)], ids=lambda s: "x".join(map(str, s)))
 def test_stacks_views_and_in_place(shape, t):
@@ -76,13 +104,14 @@ def test_stacks_views_and_in_place(shape, t):
     assert all(torch.equal(alone[1], o) for o in same)
 
 
-def test_zeros_and_what_is_not_finite():
+@pytest.mark.parametrize("shape", [(40, 70), (90, 70), (70, 1100)], ids=lambda s: "x".join(map(str, s)))
+def test_zeros_and_what_is_not_finite(shape):
     for t in TYPES.values():
-        G = torch.zeros((3, 40, 70), dtype=t, device="cuda")
+        G = torch.zeros((3, *shape), dtype=t, device="cuda")
         assert not rs.orthogonalize(G).any()
         assert not rs.orthogonalize(G, eps=0.0).any()
         for bad in (float("nan"), float("inf"), -float("inf")):
-            G = torch.ones((3, 40, 70), dtype=t, device="cuda")
+            G = torch.ones((3, *shape), dtype=t, device="cuda")
             G[:, 0] = 2
             G[1, 5, 6] = bad
             O = rs.orthogonalize(G)
@@ -90,18 +119,21 @@ def test_zeros_and_what_is_not_finite():
             assert bool(torch.isfinite(O[0]).all()) and torch.equal(O[0], O[2])
 
 
+@pytest.mark.parametrize("rows", [50, 100])
 @pytest.mark.parametrize("factor", [2.0 ** -100, 2.0 ** 100])
-def test_scale_of_the_gradient_does_not_matter(factor):
+def test_scale_of_the_gradient_does_not_matter(factor, rows):
     """Squares outside float's range; without eps a power of two changes no bit."""
     gen = torch.Generator().manual_seed(1)
-    G = gradient(gen, 50, 80, torch.float32).cuda()
+    G = gradient(gen, rows, 80, torch.float32).cuda()
     assert torch.equal(rs.orthogonalize(G * factor, eps=0.0), rs.orthogonalize(G, eps=0.0))
 
 
-def test_one_large_element():
-    """All of the norm in one place: the small ones keep their own precision."""
+@pytest.mark.parametrize("shape", [(40, 60), (100, 90)], ids=lambda s: "x".join(map(str, s)))
+def test_one_large_element(shape):
+    """All of the norm in one place: the small ones keep their own precision (their
+    parts are below float16's normal numbers)."""
     gen = torch.Generator().manual_seed(2)
-    G = torch.randn((40, 60), generator=gen) * 1e-4
+    G = torch.randn(shape, generator=gen) * 1e-4
     G[3, 4] = 1.0
     ref, err = ortho_step64(G, MUON)
     assert_within(rs.orthogonalize(G.cuda(), steps=1), ref, rounded(ref, err, torch.float32))

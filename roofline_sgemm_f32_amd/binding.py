@@ -633,7 +633,7 @@ def _workspace(like, name, *sizes):
 def lora(X, A, B, ids=None, scale=1.0, base=None, out=None, save=False):
     """Low-rank adapters of many requests beside a shared projection, on the
     current stream: Y[m] = base[m] + scale[l] (X[m] A[l]^T) B[l]^T with l =
-    ids[m].  X is M x K, A is L x R x K, B is L x N x R (R up to 256), ``base``
+    ids[m].  X is M x K, A is L x R x K, B is L x N x R (R up to 256, L up to 4096), ``base``
     (the projection's result; None: zero) and Y are M x N, all float32, float16
     or bfloat16.  ``ids`` (int32 or int64, M) names each row's adapter; an id
     outside 0..L-1, -1 say, means none: Y[m] = base[m].  None: every row has the
@@ -739,10 +739,7 @@ def orthogonalize(G, steps=5, coefficients=MUON, eps=1e-7, out=None):
         batch, M, N = shape
     else:
         raise ValueError("G must be a matrix or a stack of matrices")
-    try:
-        coef = _triples(coefficients, steps)
-    except TypeError:  # lists, which have no hash
-        coef = _triples(tuple(tuple(r) if isinstance(r, list) else r for r in coefficients), steps)
+    coef = _triples(coefficients, steps)
     ldg, sg = _matrices(G, "G", shape, t)
     if out is None:
         out = G.new_empty(shape)
@@ -762,10 +759,9 @@ def _matrices(t, name, shape, dtype):
     return _stack(t, name, tuple(shape), dtype)
 
 
-@functools.lru_cache(maxsize=64)
 def _triples(coefficients, steps):
-    """The coefficients of every step as a C array of doubles, which is only read."""
-    rows = list(coefficients)
+    """The coefficients of every step as a C array of doubles."""
+    rows = list(coefficients.tolist() if hasattr(coefficients, "tolist") else coefficients)
     if rows and not isinstance(rows[0], (tuple, list)):
         rows = [rows] * int(steps)
     if not rows or any(not isinstance(r, (tuple, list)) or len(r) != 3 for r in rows):

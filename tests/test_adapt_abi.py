@@ -167,3 +167,20 @@ def test_reference_gradients_match_differences():
             # only the 64-bit rounding of sums of order 10 over 2 h remains.
             assert abs((ends[0] - ends[1]) / 2e-6 - float(grad.reshape(-1)[j])) < 1e-7
     assert not grads[1][1].any() and not grads[2][1].any()  # no row has adapter 1
+
+
+def test_coefficients_are_read_at_every_call():
+    from roofline_sgemm_f32_amd.binding import _triples
+    t = torch.tensor([2.0, -1.5, 0.5])
+    assert list(_triples(t, 2)) == [2.0, -1.5, 0.5] * 2
+    t[0] = 3.0
+    assert list(_triples(t, 1)) == [3.0, -1.5, 0.5]
+    u = torch.tensor([[2.0, -1.5, 0.5], [3.0, 0.0, 1.0]], dtype=torch.float64)
+    assert list(_triples(u, 7)) == [2.0, -1.5, 0.5, 3.0, 0.0, 1.0]
+    rows = [[2, -1.5, 0.5], (3, 0, 1)]
+    assert list(_triples(rows, 7)) == list(_triples(u.numpy(), 7)) == list(u.flatten())
+    for bad in ((), (1.0, 2.0), [[1.0, 2.0]], [(1, 2, 3), 4], torch.zeros(2, 2)):
+        with pytest.raises(ValueError):
+            _triples(bad, 1)
+    with pytest.raises(ValueError):
+        _triples((1.0, 2.0, 3.0), 0)

@@ -17,11 +17,11 @@ void shrink(const ShrinkArgs& a, const PassPlan& p, hipStream_t s) {
 // Tiles of 16 rows.
 template <int T>
 void expand_rows(const ExpandArgs& a, dim3 grid, hipStream_t s) {
-    const size_t lds = expand_lds<T>(a.R, 16);
+    const size_t lds = expand_lds<T>(a.R);
     auto run = [&](auto kind) {
         constexpr int KIND = decltype(kind)::value;
-        if (a.R % kVec<T> != 0) hipLaunchKernelGGL((lora_expand<T, 1, KIND, true>), grid, dim3(256), lds, s, a);
-        else hipLaunchKernelGGL((lora_expand<T, 1, KIND, false>), grid, dim3(256), lds, s, a);
+        if (a.R % kVec<T> != 0) hipLaunchKernelGGL((lora_expand<T, KIND, true>), grid, dim3(256), lds, s, a);
+        else hipLaunchKernelGGL((lora_expand<T, KIND, false>), grid, dim3(256), lds, s, a);
     };
     if (a.R > (T == T_F32 ? 32 : 64)) return run(std::integral_constant<int, EXPAND_LONG>{});
     if constexpr (T != T_F32)

@@ -48,14 +48,6 @@ __device__ __forceinline__ int64_t slot_of(const WeightArgs& a, const RowTile& t
     return a.slot_start[t.adapter + 1] > first ? first + t.place : -1;
 }
 
-// 2^(14 - exponent of top); 1 for zero.
-__device__ __forceinline__ float half_power(float top) {
-    if (!(top > 0.0f)) return 1.0f;
-    int ex = int(__float_as_uint(top) >> 23) - 127;
-    ex = ex < -100 ? -100 : ex;
-    return __uint_as_float(uint32_t(14 - ex + 127) << 23);
-}
-
 // A workgroup: a chunk of an adapter's rows, four waves' column groups, 16 RB of
 // the ranks.  The sum of a matrix instruction runs over rows, so its operands
 // hold 8 rows of one column (16-bit types: a lane's 8 rows x 8 columns, 16 bytes a
@@ -110,7 +102,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) l
                 const v4f v = v_at(e / (RN / 4), r);
 #pragma unroll
                 for (int y = 0; y < 4; y++)  // a maximum has no order
-                    if (fabsf(v[y]) <= 3.4e38f) atomicMax(&top[r + y], __float_as_uint(fabsf(v[y])));
+                    if (fabsf(v[y]) < __builtin_inff()) atomicMax(&top[r + y], __float_as_uint(fabsf(v[y])));
             }
         }
         v4f acc[V][RB];
@@ -143,17 +135,8 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) l
 #pragma unroll
                     for (int y = 0; y < 4; y++) {
                         uint16_t* const at = reinterpret_cast<uint16_t*>(vs) + (r + y) * VP + p;
-                        if constexpr (T == T_F16) {
-                            const float x = v[y] * half_power(__uint_as_float(top[r + y]));
-                            const _Float16 h = _Float16(x);
-                            at[0] = __builtin_bit_cast(uint16_t, h);
-                            at[RN * VP] = __builtin_bit_cast(uint16_t, _Float16(fabsf(x) <= 65504.0f ? x - float(h) : 0.0f));
-                        } else {
-                            const uint32_t cut = __float_as_uint(v[y]) & 0xFFFF0000u;
-                            const bool finite = (cut & 0x7F800000u) != 0x7F800000u;
-                            at[0] = uint16_t(!finite && v[y] != v[y] ? 0x7FC0u : cut >> 16);
-                            at[RN * VP] = __builtin_bit_cast(uint16_t, __bf16(finite ? v[y] - __uint_as_float(cut) : 0.0f));
-                        }
+                        const float up = T == T_F16 ? half_factor(__uint_as_float(top[r + y])) : 1.0f;
+                        split_element<T>(v[y], up, at[0], at[RN * VP]);
                     }
                 }
             }
@@ -173,17 +156,22 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) l
                 return z;
             };
             if constexpr (T == T_F32) {
-#pragma unroll 4
-                for (int q = 0; q < kWeightRows / 4; q++) {
-                    if (4 * q >= left) break;
-                    const u32x4 z = load_z(4 * q + g);
+                // Eight loads in flight.
+#pragma unroll 1
+                for (int q0 = 0; q0 < kWeightRows / 4; q0 += 8) {
+                    if (4 * q0 >= left) break;
+                    u32x4 z[8];
 #pragma unroll
-                    for (int n = 0; n < RB; n++) {
-                        const float v = reinterpret_cast<const float*>(vs)[(4 * q + g) * RN + 16 * n + i];
+                    for (int q = 0; q < 8; q++) z[q] = load_z(4 * (q0 + q) + g);
 #pragma unroll
-                        for (int e = 0; e < V; e++)
-                            acc[e][n] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, __uint_as_float(z[e]), acc[e][n], 0, 0, 0);
-                    }
+                    for (int q = 0; q < 8; q++)
+#pragma unroll
+                        for (int n = 0; n < RB; n++) {
+                            const float v = reinterpret_cast<const float*>(vs)[(4 * (q0 + q) + g) * RN + 16 * n + i];
+#pragma unroll
+                            for (int e = 0; e < V; e++)
+                                acc[e][n] = __builtin_amdgcn_mfma_f32_16x16x4f32(v, __uint_as_float(z[q][e]), acc[e][n], 0, 0, 0);
+                        }
                 }
             } else {
 #pragma unroll
@@ -192,23 +180,21 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) l
                     u32x4 z[8];
 #pragma unroll
                     for (int y = 0; y < 8; y++) z[y] = load_z(32 * q + 8 * g + y);
-                    u32x4 hi[RB], lo[RB];
+                    u32x4 x[V];  // column e of the lane's 8 x 8
+#pragma unroll
+                    for (int e = 0; e < V; e++)
+#pragma unroll
+                        for (int y = 0; y < 4; y++)
+                            x[e][y] = __builtin_amdgcn_perm(z[2 * y + 1][e / 2], z[2 * y][e / 2], e % 2 ? 0x07060302u : 0x05040100u);
 #pragma unroll
                     for (int n = 0; n < RB; n++) {
                         const char* const at = vs + ((16 * n + i) * VP + 32 * q + 8 * g) * 2;
-                        hi[n] = *reinterpret_cast<const u32x4*>(at);
-                        lo[n] = *reinterpret_cast<const u32x4*>(at + RN * VP * 2);
-                    }
+                        const u32x4 hi = *reinterpret_cast<const u32x4*>(at);
+                        const u32x4 lo = *reinterpret_cast<const u32x4*>(at + RN * VP * 2);
 #pragma unroll
-                    for (int e = 0; e < V; e++) {
-                        u32x4 x;  // column e of the lane's 8 x 8
-#pragma unroll
-                        for (int y = 0; y < 4; y++)
-                            x[y] = __builtin_amdgcn_perm(z[2 * y + 1][e / 2], z[2 * y][e / 2], e % 2 ? 0x07060302u : 0x05040100u);
-#pragma unroll
-                        for (int n = 0; n < RB; n++) {
-                            acc[e][n] = mma16<T>(hi[n], x, acc[e][n]);
-                            acc[e][n] = mma16<T>(lo[n], x, acc[e][n]);
+                        for (int e = 0; e < V; e++) {
+                            acc[e][n] = mma16<T>(hi, x[e], acc[e][n]);
+                            acc[e][n] = mma16<T>(lo, x[e], acc[e][n]);
                         }
                     }
                 }
@@ -224,7 +210,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) l
                 const int r = 16 * n + 4 * g + y;
                 if (r0 + r >= a.R) continue;
                 float f = s;
-                if constexpr (T == T_F16) f = s / half_power(__uint_as_float(top[r]));
+                if constexpr (T == T_F16) f = s / half_factor(__uint_as_float(top[r]));
                 if (slot >= 0) {
                     float* const at = sd.partial + (slot * a.R + r0 + r) * sd.C + c;
 #pragma unroll

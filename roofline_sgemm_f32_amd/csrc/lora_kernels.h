@@ -4,8 +4,9 @@
 // R results a row) in float partial sums, one plane for each share of K;
 // lora_expand adds the planes up and forms Y (short sums, N results a row).
 // Rows come in tiles of one adapter each (RowPlan), so an adapter is read once
-// for up to 64 rows.  Nothing is staged: the matrix instructions' operands are
-// 16 bytes along K (or R) of one row, which is how memory holds them.
+// for up to 64 rows.  The matrix instructions' operands are 16 bytes along K (or
+// R) of one row, which is how memory holds them: they are loaded as they are, but
+// for what four waves share (lora_expand_tiles' adapter, through LDS).
 #pragma once
 #include "lora.h"
 
@@ -127,9 +128,9 @@ enum ExpandKind { EXPAND_PACKED, EXPAND_HELD, EXPAND_LONG };
 // LDS of a workgroup: H in the operands' form (two 16-bit parts, or floats) with
 // rows padded by 16 bytes, and a factor for each row.
 __host__ __device__ constexpr int expand_ranks(int R) { return R <= 16 ? 32 : (R + 63) / 64 * 64; }
-template <int T> inline size_t expand_lds(int R, int rows) {
+template <int T> inline size_t expand_lds(int R) {
     const int rp = expand_ranks(R);
-    return size_t(rows) * (T == T_F32 ? (rp + 4) * 4 : 2 * (rp + 8) * 2) + size_t(rows) * 4;
+    return 16 * size_t((T == T_F32 ? (rp + 4) * 4 : 2 * (rp + 8) * 2) + 4);
 }
 
 // The largest of sixteen lanes' values.
@@ -138,36 +139,11 @@ __device__ __forceinline__ float group_max(float v) {
     for (int d = 1; d < 16; d *= 2) v = fmaxf(v, __shfl_xor(v, d, 16));
     return v;
 }
-// 2^(14 - exponent of top); 1 for zero.
-__device__ __forceinline__ float half_factor(float top) {
-    if (!(top > 0.0f)) return 1.0f;
-    int ex = int(__float_as_uint(top) >> 23) - 127;
-    ex = ex < -100 ? -100 : ex;
-    return __uint_as_float(uint32_t(14 - ex + 127) << 23);
-}
-// H in two parts of 16 bits, times up (float16).
-template <int T, int NE>
-__device__ __forceinline__ void split_elements(const float (&v)[NE], float up, uint16_t (&h)[NE], uint16_t (&l)[NE]) {
-#pragma unroll
-    for (int e = 0; e < NE; e++) {
-        if constexpr (T == T_F16) {
-            const float x = v[e] * up;
-            const _Float16 top = _Float16(x);
-            h[e] = __builtin_bit_cast(uint16_t, top);
-            l[e] = __builtin_bit_cast(uint16_t, _Float16(fabsf(x) <= 65504.0f ? x - float(top) : 0.0f));
-        } else {
-            const uint32_t cut = __float_as_uint(v[e]) & 0xFFFF0000u;
-            const bool finite = (cut & 0x7F800000u) != 0x7F800000u;
-            // A NaN whose payload is in the cut bits stays one.
-            h[e] = uint16_t(!finite && v[e] != v[e] ? 0x7FC0u : cut >> 16);
-            l[e] = __builtin_bit_cast(uint16_t, __bf16(finite ? v[e] - __uint_as_float(cut) : 0.0f));
-        }
-    }
-}
 template <int T>
 __device__ __forceinline__ void split_h(const float (&v)[8], float up, u32x4& h, u32x4& l) {
     uint16_t a[8], b[8];
-    split_elements<T, 8>(v, up, a, b);
+#pragma unroll
+    for (int e = 0; e < 8; e++) split_element<T>(v[e], up, a[e], b[e]);
     __builtin_memcpy(&h, a, 16);
     __builtin_memcpy(&l, b, 16);
 }
@@ -178,8 +154,8 @@ __device__ __forceinline__ void store_h(char* hi, char* lo, int r, v4f v, float 
         *reinterpret_cast<v4f*>(hi + r * 4) = v;
     } else {
         uint16_t h[4], l[4];
-        const float f[4] = {v[0], v[1], v[2], v[3]};
-        split_elements<T, 4>(f, up, h, l);
+#pragma unroll
+        for (int e = 0; e < 4; e++) split_element<T>(v[e], up, h[e], l[e]);
         __builtin_memcpy(hi + r * 2, h, 8);
         __builtin_memcpy(lo + r * 2, l, 8);
     }
@@ -220,22 +196,21 @@ __device__ __forceinline__ u32x4 load_ranks(const typename Elem<T>::type* row, i
     return v;
 }
 
-// A workgroup: 16 TMB rows of a tile and a share of N, 64 columns a wave at a
-// time.  H is rounded to no fewer than 16 bits: for 16-bit types it is the sum
+// A workgroup: a tile of 16 rows and a share of N, 64 columns a wave at a time.  H is rounded to no fewer than 16 bits: for 16-bit types it is the sum
 // of two parts, of bfloat16 cut off and rounded (2^-16 of an element), or of
 // float16 after a power of two for the row that brings its largest element
 // below 2^15 (2^-22, and 2^-39 of that element).  One matrix instruction of a
 // 16-bit type sums over 32: both parts of a rank of up to 16 (PACKED), else one
-// part of 32.  Ranks up to 64 (float: 32) are HELD in registers for all rows of
-// the tile; larger ones are read again, from the caches, for each 16 rows (LONG).
-template <int T, int TMB, int KIND, bool ODD>
-__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(TMB > 1 ? 2 : 3)))
-lora_expand(ExpandArgs a) {
+// part of 32.  Of ranks up to 64 (float: 32) the next columns'
+// operands are fetched while these are multiplied (HELD); of more ranks there are
+// too many for that (LONG).
+template <int T, int KIND, bool ODD>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(T == T_F32 ? 2 : 3))) lora_expand(ExpandArgs a) {
     using E = typename Elem<T>::type;
-    constexpr int V = kVec<T>, TM = 16 * TMB, STEP = 4 * V;
-    // Operands of the adapter held at a time, for all of the tile's rows unless LONG.
+    constexpr int V = kVec<T>, TM = 16, STEP = 4 * V;
+    // Operands of the adapter at a time.
     constexpr int HELD = KIND == EXPAND_PACKED ? 1 : 2;
-    constexpr int NG = 16 / V;  // groups of V results a lane and 16 rows
+    constexpr int NG = 16 / V;  // groups of V results a lane
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const int rp = expand_ranks(a.R), steps = rp / STEP;
     const int pitch = T == T_F32 ? (rp + 4) * 4 : (rp + 8) * 2;  // bytes
@@ -259,19 +234,13 @@ lora_expand(ExpandArgs a) {
         if (!has && in_place && !a.H) continue;
         const float s = !has || !a.scaled ? 1.0f : a.alpha * (a.scales ? a.scales[tile.adapter] : 1.0f);
         const E* const w = static_cast<const E*>(a.W) + (has ? tile.adapter : 0) * a.sw;
-        const E* base[TMB];
-        E* out[TMB];
-        bool own[TMB];
-#pragma unroll
-        for (int m = 0; m < TMB; m++) {
-            own[m] = 16 * m + i < tile.count;
-            const int64_t at = row_at(a.rows, tile.start + (own[m] ? 16 * m + i : 0));
-            base[m] = static_cast<const E*>(a.base) + at * a.ldbase;
-            out[m] = static_cast<E*>(a.Y) + at * a.ldy;
-        }
+        const bool own = i < tile.count;
+        const int64_t row = row_at(a.rows, tile.start + (own ? i : 0));
+        const E* const base = static_cast<const E*>(a.base) + row * a.ldbase;
+        E* const out = static_cast<E*>(a.Y) + row * a.ldy;
         // What 64 columns take from memory, fetched one turn ahead.
         struct Turn {
-            u32x4 b[TMB][NG], w[HELD][4];
+            u32x4 b[NG], w[HELD][4];
         };
         auto load_w = [&](int64_t n0, int u, Turn& v) {
 #pragma unroll
@@ -288,9 +257,7 @@ lora_expand(ExpandArgs a) {
             if (n0 >= ne) return;
             if (n0 + 64 <= a.N && a.base) {
 #pragma unroll
-                for (int m = 0; m < TMB; m++)
-#pragma unroll
-                    for (int j = 0; j < NG; j++) v.b[m][j] = load16(base[m] + n0 + col(j));
+                for (int j = 0; j < NG; j++) v.b[j] = load16(base + n0 + col(j));
             }
             if (has && KIND != EXPAND_LONG) load_w(n0, 0, v);
         };
@@ -299,129 +266,100 @@ lora_expand(ExpandArgs a) {
         __syncthreads();
         // Sixteen lanes a row, four neighbours of each 64 columns a lane; the loads
         // of the planes in flight together.
-        const int c = threadIdx.x & 15, hp = lora_pitch(a.R);
-        const float* const P = a.P + int64_t(tile.start) * hp;
-        bool in[TMB];
-#pragma unroll
-        for (int m = 0; m < TMB; m++) in[m] = 16 * m + int(threadIdx.x >> 4) < tile.count;
-        float top[TMB] = {};
+        const int c = threadIdx.x & 15, p = threadIdx.x >> 4, hp = lora_pitch(a.R);
+        const bool in = p < tile.count;
+        // Rows past the tile's repeat its first.
+        const float* const P = a.P + (int64_t(tile.start) + (in ? p : 0)) * hp;
+        float top = 0.0f;
         for (int pass = 0; pass < (T == T_F16 && rp > 64 ? 2 : 1); pass++) {
             for (int q0 = 0; q0 < rp; q0 += 64) {
                 const int rq = q0 + 4 * c;
-                v4f v[TMB];
-#pragma unroll
-                for (int m = 0; m < TMB; m++) v[m] = v4f{0, 0, 0, 0};
+                v4f v = {0, 0, 0, 0};
                 if (has && rq < hp) {
-                    // Rows past the tile's repeat its first.
-                    int at[TMB];
-#pragma unroll
-                    for (int m = 0; m < TMB; m++) at[m] = in[m] ? (16 * m + int(threadIdx.x >> 4)) * hp + rq : rq;
-                    constexpr int AT_ONCE = TMB == 1 ? 8 : 4;
+                    constexpr int AT_ONCE = 8;
                     int z = 0;
                     for (; z + AT_ONCE <= a.planes; z += AT_ONCE) {
-                        v4f q[AT_ONCE][TMB];
+                        v4f q[AT_ONCE];
 #pragma unroll
-                        for (int y = 0; y < AT_ONCE; y++)
+                        for (int y = 0; y < AT_ONCE; y++) q[y] = *reinterpret_cast<const v4f*>(P + (z + y) * a.plane + rq);
 #pragma unroll
-                            for (int m = 0; m < TMB; m++)
-                                q[y][m] = *reinterpret_cast<const v4f*>(P + (z + y) * a.plane + at[m]);
-#pragma unroll
-                        for (int y = 0; y < AT_ONCE; y++)
-#pragma unroll
-                            for (int m = 0; m < TMB; m++) v[m] += q[y][m];
+                        for (int y = 0; y < AT_ONCE; y++) v += q[y];
                     }
-                    for (; z < a.planes; z++)
-#pragma unroll
-                        for (int m = 0; m < TMB; m++)
-                            v[m] += *reinterpret_cast<const v4f*>(P + z * a.plane + at[m]);
+                    for (; z < a.planes; z++) v += *reinterpret_cast<const v4f*>(P + z * a.plane + rq);
                 }
+                if (!in) v = v4f{0, 0, 0, 0};
+                float up = 1.0f;
+                if constexpr (T == T_F16) {
+                    // The power that brings the row's largest finite element into [2^14, 2^15).
+                    if (pass == 0) {
 #pragma unroll
-                for (int m = 0; m < TMB; m++) {
-                    const int p = 16 * m + (threadIdx.x >> 4);
-                    if (!in[m]) v[m] = v4f{0, 0, 0, 0};
-                    float up = 1.0f;
-                    if constexpr (T == T_F16) {
-                        // The power that brings the row's largest finite element into [2^14, 2^15).
-                        if (pass == 0) {
-#pragma unroll
-                            for (int e = 0; e < 4; e++)
-                                if (fabsf(v[m][e]) <= 3.4e38f) top[m] = fmaxf(top[m], fabsf(v[m][e]));
-                            if (rp > 64) continue;
-                        }
-                        // Every lane of the row's sixteen is here.
-                        up = half_factor(group_max(top[m]));
+                        for (int e = 0; e < 4; e++) top = largest(top, v[e]);
+                        if (rp > 64) continue;
                     }
-                    if (rq < rp) store_h<T>(hi + p * pitch, lo + p * pitch, rq, v[m], up);
-                    if (a.H && blockIdx.y == 0 && in[m]) {
-                        float* const h = a.H + row_at(a.rows, tile.start + p) * a.ldh;
+                    // Every lane of the row's sixteen is here.
+                    up = half_factor(group_max(top));
+                }
+                if (rq < rp) store_h<T>(hi + p * pitch, lo + p * pitch, rq, v, up);
+                if (a.H && blockIdx.y == 0 && in) {
+                    float* const h = a.H + row_at(a.rows, tile.start + p) * a.ldh;
 #pragma unroll
-                        for (int e = 0; e < 4; e++)
-                            if (rq + e < a.R) h[rq + e] = v[m][e];
-                    }
+                    for (int e = 0; e < 4; e++)
+                        if (rq + e < a.R) h[rq + e] = v[e];
                 }
             }
         }
-        if (c == 0)
-#pragma unroll
-            for (int m = 0; m < TMB; m++) factor[16 * m + (threadIdx.x >> 4)] = s;
         if constexpr (T == T_F16) {
-#pragma unroll
-            for (int m = 0; m < TMB; m++) {
-                const float up = half_factor(group_max(top[m]));
-                if (c == 0) factor[16 * m + (threadIdx.x >> 4)] = s / up;
-            }
+            const float up = half_factor(group_max(top));
+            if (c == 0) factor[p] = s / up;
+        } else {
+            if (c == 0) factor[p] = s;
         }
         __syncthreads();
-        float f[TMB];
-#pragma unroll
-        for (int m = 0; m < TMB; m++) f[m] = factor[16 * m + i];
+        const float f = factor[i];
         for (int64_t n0 = nb + wave * 64; n0 < ne; n0 += 256) {
             Turn next;
             fetch(n0 + 256, next);
             const bool whole = n0 + 64 <= a.N;
+            v4f acc[4];
 #pragma unroll
-            for (int m = 0; m < TMB; m++) {
-                v4f acc[4];
+            for (int q = 0; q < 4; q++) acc[q] = v4f{0, 0, 0, 0};
+            if (has) {
+                const int at = i * pitch;
+                for (int u = 0; u < (KIND == EXPAND_LONG ? steps : 1); u += HELD) {
+                    if constexpr (KIND == EXPAND_LONG) load_w(n0, u, cur);
 #pragma unroll
-                for (int q = 0; q < 4; q++) acc[q] = v4f{0, 0, 0, 0};
-                if (has) {
-                    const int at = (16 * m + i) * pitch;
-                    for (int u = 0; u < (KIND == EXPAND_LONG ? steps : 1); u += HELD) {
-                        if constexpr (KIND == EXPAND_LONG) load_w(n0, u, cur);
+                    for (int h = 0; h < HELD; h++) {
+                        const int r = KIND == EXPAND_PACKED ? 8 * (g & 1) : (u + h) * STEP + g * V;
+                        const char* const from = KIND == EXPAND_PACKED && g >= 2 ? lo : hi;
+                        const u32x4 x = *reinterpret_cast<const u32x4*>(from + at + r * int(sizeof(E)));
 #pragma unroll
-                        for (int h = 0; h < HELD; h++) {
-                            const int r = KIND == EXPAND_PACKED ? 8 * (g & 1) : (u + h) * STEP + g * V;
-                            const char* const from = KIND == EXPAND_PACKED && g >= 2 ? lo : hi;
-                            const u32x4 x = *reinterpret_cast<const u32x4*>(from + at + r * int(sizeof(E)));
+                        for (int q = 0; q < 4; q++) acc[q] = mma16<T>(cur.w[h][q], x, acc[q]);
+                        if constexpr (T != T_F32 && KIND != EXPAND_PACKED) {
+                            const u32x4 y = *reinterpret_cast<const u32x4*>(lo + at + r * 2);
 #pragma unroll
-                            for (int q = 0; q < 4; q++) acc[q] = mma16<T>(cur.w[h][q], x, acc[q]);
-                            if constexpr (T != T_F32 && KIND != EXPAND_PACKED) {
-                                const u32x4 y = *reinterpret_cast<const u32x4*>(lo + at + r * 2);
-#pragma unroll
-                                for (int q = 0; q < 4; q++) acc[q] = mma16<T>(cur.w[h][q], y, acc[q]);
-                            }
+                            for (int q = 0; q < 4; q++) acc[q] = mma16<T>(cur.w[h][q], y, acc[q]);
                         }
                     }
                 }
-                if (!own[m]) continue;
+            }
+            if (own)
 #pragma unroll
                 for (int j = 0; j < NG; j++) {
                     float d[V], b[V];
 #pragma unroll
-                    for (int e = 0; e < V; e++) d[e] = f[m] * acc[j * V / 4 + e / 4][e % 4];
+                    for (int e = 0; e < V; e++) d[e] = f * acc[j * V / 4 + e / 4][e % 4];
                     const int64_t c = n0 + col(j);
                     if (whole) {
                         if (a.base) {
-                            unpack<T>(cur.b[m][j], b);
+                            unpack<T>(cur.b[j], b);
 #pragma unroll
                             for (int e = 0; e < V; e++) d[e] = has ? b[e] + d[e] : b[e];
                         }
-                        store16(out[m] + c, pack<T>(d));
+                        store16(out + c, pack<T>(d));
                     } else {
-                        store_edge<T>(base[m], out[m], c, a.N, has, a.base != nullptr, d);
+                        store_edge<T>(base, out, c, a.N, has, a.base != nullptr, d);
                     }
                 }
-            }
             cur = next;
         }
     }
@@ -548,7 +486,7 @@ lora_expand_tiles(ExpandArgs a) {
                 for (int u = 0; u < NS; u++)
 #pragma unroll
                     for (int e = 0; e < V; e++)
-                        if (fabsf(v[u][e]) <= 3.4e38f) top = fmaxf(top, fabsf(v[u][e]));
+                        top = largest(top, v[u][e]);
                 top = fmaxf(top, __shfl_xor(top, 16));
                 up = half_factor(fmaxf(top, __shfl_xor(top, 32)));
                 f = s / up;

@@ -122,5 +122,34 @@ __device__ __forceinline__ v4f mma16(u32x4 a, u32x4 b, v4f c) {
     }
 }
 
+// Float factors for the 16-bit instructions: the sum of two parts of the type, of
+// bfloat16 cut off and rounded, of float16 after a power of two that brings the
+// largest of those that share it into [2^14, 2^15).
+__device__ __forceinline__ float largest(float top, float v) {  // of the finite
+    return fabsf(v) < __builtin_inff() ? fmaxf(top, fabsf(v)) : top;
+}
+// That power, 2^(14 - exponent of top); 1 for zero.
+__device__ __forceinline__ float half_factor(float top) {
+    if (!(top > 0.0f)) return 1.0f;
+    int ex = int(__float_as_uint(top) >> 23) - 127;
+    ex = ex < -100 ? -100 : ex;
+    return __uint_as_float(uint32_t(14 - ex + 127) << 23);
+}
+template <int T>
+__device__ __forceinline__ void split_element(float v, float up, uint16_t& h, uint16_t& l) {
+    if constexpr (T == T_F16) {
+        const float x = v * up;
+        const _Float16 top = _Float16(x);
+        h = __builtin_bit_cast(uint16_t, top);
+        l = __builtin_bit_cast(uint16_t, _Float16(fabsf(x) <= 65504.0f ? x - float(top) : 0.0f));
+    } else {
+        const uint32_t cut = __float_as_uint(v) & 0xFFFF0000u;
+        const bool finite = (cut & 0x7F800000u) != 0x7F800000u;
+        // A NaN whose payload is in the cut bits stays one.
+        h = uint16_t(!finite && v != v ? 0x7FC0u : cut >> 16);
+        l = __builtin_bit_cast(uint16_t, __bf16(finite ? v - __uint_as_float(cut) : 0.0f));
+    }
+}
+
 }  // namespace
 }  // namespace sgemm

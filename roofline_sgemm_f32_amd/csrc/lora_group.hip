@@ -52,7 +52,8 @@ __device__ __forceinline__ int scan(int* v, int n) {
 // (LDS atomics on one address take their turns).  Rows without adapter come last.
 // Up to kHeld rows' groups and places stay in LDS between the two passes.  The
 // loops are not unrolled and the code is short: it runs once, on one CU, and is
-// fetched from memory first.
+// fetched from memory first (64 rows 6 us, 1025 rows 7, 8192 rows 12: bound by the
+// latency of one step after another).
 __device__ __forceinline__ void group_rows(const GroupArgs& a, int* lds) {
     const int groups = a.L + 1;           // the last: no adapter
     int* const first = lds;               // groups + 1: tiles before a group's
@@ -166,7 +167,8 @@ __global__ void __launch_bounds__(kGroupThreads) lora_group(GroupArgs a) {
     group_rows(a, lds);
 }
 
-// A 64 x 64 tile of a transposed matrix a workgroup.
+// A 64 x 64 tile of a transposed matrix a workgroup.  (The sort takes longer than the
+// copies of all adapters: 8192 rows with 8 adapters of rank 16 15 us together.)
 template <typename E>
 __device__ void turn_tile(const TurnArgs& a, int64_t t, E* tile) {
     constexpr int PITCH = 64 + 4 / sizeof(E);

@@ -18,7 +18,10 @@ namespace {
 constexpr int kShrinkWaves = 4;
 
 // A workgroup: a tile of 16 TMB rows, 16 RB of the R columns, a share of K split
-// again over its waves, whose sums are added through LDS.
+// again over its waves, whose sums are added through LDS.  R gives few
+// workgroups, so K is shared until there are about 512; the planes of sums cost
+// less than idle CUs.  Bound by memory: 8192 x 4096 bfloat16 of rank 64 26 us (67 MB
+// of X, 2.6 TB/s, the adapters from the caches); of rank 16 20 us (3.4 TB/s).
 template <int T, int RB, int TMB>
 __global__ void __launch_bounds__(64 * kShrinkWaves) __attribute__((amdgpu_waves_per_eu(TMB * RB > 8 ? 2 : 3)))
 lora_shrink(ShrinkArgs a) {
@@ -203,7 +206,8 @@ __device__ __forceinline__ u32x4 load_ranks(const typename Elem<T>::type* row, i
 // 16-bit type sums over 32: both parts of a rank of up to 16 (PACKED), else one
 // part of 32.  Of ranks up to 64 (float: 32) the next columns'
 // operands are fetched while these are multiplied (HELD); of more ranks there are
-// too many for that (LONG).
+// too many for that (LONG).  For tiles of few rows, bound by reading the adapters
+// (257 rows x 8192, 32 adapters of rank 32, bfloat16: 15 us).
 template <int T, int KIND, bool ODD>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(T == T_F32 ? 2 : 3))) lora_expand(ExpandArgs a) {
     using E = typename Elem<T>::type;
@@ -370,7 +374,9 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(T == T
 // for the whole of it.  64 columns of the adapter are staged in LDS for the four
 // waves, up to 64 ranks at a time, while the ones before are multiplied: read
 // from memory by each wave for itself (into registers), they passed through the L1
-// four times and took as long as base and Y (8192 x 8192 of rank 64: 97 us).
+// four times and took as long as base and Y (8192 x 8192 bfloat16 of rank 64: 97 us,
+// staged 78, which is 3.5 TB/s of base and Y; of rank 16 8192 x 4096 38 us).  Waves
+// wait for base most of the time; two turns of it are in flight (four gain nothing).
 // NS: matrix instructions' sums of one part that R takes.
 template <int T, int KIND, int NS, bool ODD>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(T == T_F32 ? (NS <= 2 ? 3 : NS <= 8 ? 2 : 1) : (NS <= 2 ? 4 : NS <= 4 ? 2 : 1))))

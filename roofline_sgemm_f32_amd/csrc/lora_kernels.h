@@ -375,8 +375,10 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(T == T
 // waves, up to 64 ranks at a time, while the ones before are multiplied: read
 // from memory by each wave for itself (into registers), they passed through the L1
 // four times and took as long as base and Y (8192 x 8192 bfloat16 of rank 64: 97 us,
-// staged 78, which is 3.5 TB/s of base and Y; of rank 16 8192 x 4096 38 us).  Waves
-// wait for base most of the time; two turns of it are in flight (four gain nothing).
+// staged 80).  A share's workgroups are on as few XCDs as can be, whose L2s then keep
+// that share of the adapters (75 us, 3.6 TB/s of base and Y; of rank 16 8192 x 4096
+// 38 -> 35).  Waves wait for base most of the time; two turns of it are in flight
+// (four, or the adapter's two turns ahead, are slower).
 // NS: matrix instructions' sums of one part that R takes.
 template <int T, int KIND, int NS, bool ODD>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(T == T_F32 ? (NS <= 2 ? 3 : NS <= 8 ? 2 : 1) : (NS <= 2 ? 4 : NS <= 4 ? 2 : 1))))
@@ -393,12 +395,13 @@ lora_expand_tiles(ExpandArgs a) {
     __shared__ __attribute__((aligned(16))) char stage[2][64 * PITCH];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i = lane & 15, g = lane >> 4;
-    const int64_t nb = blockIdx.y * a.nshare, ne = nb + a.nshare < a.N ? nb + a.nshare : a.N;
+    const uint2 block = block_of_run();
+    const int64_t nb = block.y * a.nshare, ne = nb + a.nshare < a.N ? nb + a.nshare : a.N;
     auto col = [&](int j) { return T == T_F32 ? 16 * j + 4 * g : 32 * j + 8 * g; };
     auto w_row = [&](int q) {
         return T == T_F32 ? 16 * q + i : 32 * (q >> 1) + 8 * (i >> 2) + 4 * (q & 1) + (i & 3);
     };
-    for (int64_t t = blockIdx.x; t < a.tiles; t += gridDim.x) {
+    for (int64_t t = block.x; t < a.tiles; t += gridDim.x) {
         const RowTile tile = row_tile(a.rows, t, 64);
         if (tile.count == 0) break;
         const bool has = tile.adapter >= 0;
@@ -480,7 +483,7 @@ lora_expand_tiles(ExpandArgs a) {
 #pragma unroll
                 for (int e = 0; e < V; e++)
                     if (!own || r + e >= a.R) v[u][e] = 0.0f;
-                if (a.H && blockIdx.y == 0 && own && (!PACKED || g < 2))
+                if (a.H && block.y == 0 && own && (!PACKED || g < 2))
 #pragma unroll
                     for (int e = 0; e < V; e++)
                         if (r + e < a.R) a.H[row * a.ldh + r + e] = v[u][e];

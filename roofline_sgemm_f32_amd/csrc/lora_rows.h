@@ -61,6 +61,14 @@ __device__ __forceinline__ int row_at(const RowPlan& p, int position) {
     return p.mode == RowPlan::SORTED ? p.order[position] : position;
 }
 
+// A workgroup's (x, y) of the grid, such that neighbours in x are on one XCD: they go
+// to the eight in turn, and what workgroups of one y share then stays in one L2.
+__device__ __forceinline__ uint2 block_of_run() {
+    const uint32_t n = gridDim.x * gridDim.y, id = blockIdx.x + blockIdx.y * gridDim.x;
+    const uint32_t q = n / 8, rem = n % 8, x = id % 8, t = x * q + (x < rem ? x : rem) + id / 8;
+    return {t % gridDim.x, t / gridDim.x};
+}
+
 // 16 bytes from any address, and to any.
 __device__ __forceinline__ u32x4 load16(const void* p) {
     u32x4 v;

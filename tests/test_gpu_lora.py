@@ -393,3 +393,18 @@ def test_refusals():
             rs.lora_backward(dY, X, A, B, H, ids, dW=bad)
     with pytest.raises(rs.SgemmError, match="ALIAS"):
         rs.lora_backward(dY, X, A, B, H, ids, dW=(A, B.clone()))
+
+
+@pytest.mark.parametrize("M", [1, 40])
+def test_the_largest_floats_are_finite(M):
+    # dH is 3.402e38, below the largest float (3.4028e38), in a rank whose A is zero:
+    # its power of two must bring it into float16's range, or zero times inf is NaN.
+    dY = torch.ones((M, 1), dtype=torch.float16, device="cuda")
+    B = torch.tensor([[[1.0, 0.0, 0.0, 0.0]]], dtype=torch.float16, device="cuda")
+    A = torch.zeros((1, 4, 70), dtype=torch.float16, device="cuda")
+    A[:, 1:] = 1.0
+    X = torch.ones((M, 70), dtype=torch.float16, device="cuda")
+    base = torch.randn((M, 70), device="cuda").half()
+    dX, dA, dB = rs.lora_backward(dY, X, A, B, torch.zeros((M, 4), device="cuda"), scale=3.402e38, base=base,
+                                  need_dw=False)
+    assert dA is None and dB is None and torch.equal(dX, base)

@@ -223,14 +223,15 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(T == T
     float* const factor = reinterpret_cast<float*>(smem + TM * pitch * (T == T_F32 ? 1 : 2));
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i = lane & 15, g = lane >> 4;
-    const int64_t nb = blockIdx.y * a.nshare, ne = nb + a.nshare < a.N ? nb + a.nshare : a.N;
+    const uint2 block = block_of_run();
+    const int64_t nb = block.y * a.nshare, ne = nb + a.nshare < a.N ? nb + a.nshare : a.N;
     // Columns of a lane's results: group j starts at column n0 + col(j), so that
     // four lanes' pieces adjoin; and the row of block q that becomes them.
     auto col = [&](int j) { return T == T_F32 ? 16 * j + 4 * g : 32 * j + 8 * g; };
     auto w_row = [&](int q) {
         return T == T_F32 ? 16 * q + i : 32 * (q >> 1) + 8 * (i >> 2) + 4 * (q & 1) + (i & 3);
     };
-    for (int64_t t = blockIdx.x; t < a.tiles; t += gridDim.x) {
+    for (int64_t t = block.x; t < a.tiles; t += gridDim.x) {
         const RowTile tile = row_tile(a.rows, t, TM);
         if (tile.count == 0) break;
         const bool has = tile.adapter >= 0;
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(T == T
                     up = half_factor(group_max(top));
                 }
                 if (rq < rp) store_h<T>(hi + p * pitch, lo + p * pitch, rq, v, up);
-                if (a.H && blockIdx.y == 0 && in) {
+                if (a.H && block.y == 0 && in) {
                     float* const h = a.H + row_at(a.rows, tile.start + p) * a.ldh;
 #pragma unroll
                     for (int e = 0; e < 4; e++)

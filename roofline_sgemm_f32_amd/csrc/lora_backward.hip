@@ -52,7 +52,7 @@ __device__ __forceinline__ int64_t slot_of(const WeightArgs& a, const RowTile& t
 // the ranks.  The sum of a matrix instruction runs over rows, so its operands
 // hold 8 rows of one column (16-bit types: a lane's 8 rows x 8 columns, 16 bytes a
 // row, are turned in registers, two rows by one byte permutation), or one row
-// (float).  V is in two 16-bit parts, as in the forward pass; for float16 after a
+// (float).  V is in three 16-bit parts, as in the forward pass; for float16 after a
 // power of two for each rank that brings the chunk's largest into [2^14, 2^15).
 // NARROW: fewer columns than a lane's on either side.
 //   Up to rank 16 it is bound by reading X and dY (8192 rows of 4096 + 4096 bfloat16:
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) l
     using E = typename Elem<T>::type;
     constexpr int V = kVec<T>, COLS = kGroupCols<T>, RN = 16 * RB;
     constexpr int VP = kWeightRows + 8;  // 16-bit: rows of a rank, padded
-    __shared__ __attribute__((aligned(16))) char vs[T == T_F32 ? kWeightRows * RN * 4 : 2 * RN * VP * 2];
+    __shared__ __attribute__((aligned(16))) char vs[T == T_F32 ? kWeightRows * RN * 4 : 3 * RN * VP * 2];
     __shared__ int row_of[kWeightRows];
     __shared__ uint32_t top[RN];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -138,10 +138,19 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) l
                     *reinterpret_cast<v4f*>(vs + (p * RN + r) * 4) = v;
                 } else {
 #pragma unroll
-                    for (int y = 0; y < 4; y++) {
+                    for (int y = 0; y < 4; y += 2) {
                         uint16_t* const at = reinterpret_cast<uint16_t*>(vs) + (r + y) * VP + p;
-                        const float up = T == T_F16 ? half_factor(__uint_as_float(top[r + y])) : 1.0f;
-                        split_element<T>(v[y], up, at[0], at[RN * VP]);
+                        uint32_t part[3];
+                        if constexpr (T == T_F16)  // each rank's power of two
+                            split_pair<T, 3>(v[y] * half_factor(__uint_as_float(top[r + y])),
+                                             v[y + 1] * half_factor(__uint_as_float(top[r + y + 1])), 1.0f, part);
+                        else
+                            split_pair<T, 3>(v[y], v[y + 1], 1.0f, part);
+#pragma unroll
+                        for (int i = 0; i < 3; i++) {
+                            at[i * RN * VP] = uint16_t(part[i]);
+                            at[i * RN * VP + VP] = uint16_t(part[i] >> 16);
+                        }
                     }
                 }
             }
@@ -194,13 +203,13 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) l
 #pragma unroll
                     for (int n = 0; n < RB; n++) {
                         const char* const at = vs + ((16 * n + i) * VP + 32 * q + 8 * g) * 2;
-                        const u32x4 hi = *reinterpret_cast<const u32x4*>(at);
-                        const u32x4 lo = *reinterpret_cast<const u32x4*>(at + RN * VP * 2);
+                        u32x4 part[3];
 #pragma unroll
-                        for (int e = 0; e < V; e++) {
-                            acc[e][n] = mma16<T>(hi, x[e], acc[e][n]);
-                            acc[e][n] = mma16<T>(lo, x[e], acc[e][n]);
-                        }
+                        for (int z = 0; z < 3; z++) part[z] = *reinterpret_cast<const u32x4*>(at + z * RN * VP * 2);
+#pragma unroll
+                        for (int z = 0; z < 3; z++)
+#pragma unroll
+                            for (int e = 0; e < V; e++) acc[e][n] = mma16<T>(part[z], x[e], acc[e][n]);
                     }
                 }
             }

@@ -128,12 +128,14 @@ enum ExpandKind { EXPAND_PACKED, EXPAND_HELD, EXPAND_LONG };
 
 // ---- Y = base + s H B^T -------------------------------------------------------
 
-// LDS of a workgroup: H in the operands' form (two 16-bit parts, or floats) with
-// rows padded by 16 bytes, and a factor for each row.
+// LDS of a workgroup: H in the operands' form (16-bit parts, or floats) with rows
+// padded by 16 bytes, and a factor for each row.
 __host__ __device__ constexpr int expand_ranks(int R) { return R <= 16 ? 32 : (R + 63) / 64 * 64; }
+// Parts of an element of H: of ranks up to 16 two share an instruction.
+template <int T> __host__ __device__ constexpr int h_parts(bool packed) { return T == T_F32 ? 1 : packed ? 4 : 3; }
 template <int T> inline size_t expand_lds(int R) {
     const int rp = expand_ranks(R);
-    return 16 * size_t((T == T_F32 ? (rp + 4) * 4 : 2 * (rp + 8) * 2) + 4);
+    return 16 * size_t((T == T_F32 ? (rp + 4) * 4 : h_parts<T>(R <= 16) * (rp + 8) * 2) + 4);
 }
 
 // The largest of sixteen lanes' values.
@@ -142,25 +144,17 @@ __device__ __forceinline__ float group_max(float v) {
     for (int d = 1; d < 16; d *= 2) v = fmaxf(v, __shfl_xor(v, d, 16));
     return v;
 }
-template <int T>
-__device__ __forceinline__ void split_h(const float (&v)[8], float up, u32x4& h, u32x4& l) {
-    uint16_t a[8], b[8];
-#pragma unroll
-    for (int e = 0; e < 8; e++) split_element<T>(v[e], up, a[e], b[e]);
-    __builtin_memcpy(&h, a, 16);
-    __builtin_memcpy(&l, b, 16);
-}
-// Elements r .. r + 3 of a row of H in the operands' form.
-template <int T>
-__device__ __forceinline__ void store_h(char* hi, char* lo, int r, v4f v, float up) {
+// Elements r .. r + 3 of a row of H in the operands' form, `plane` bytes between parts.
+template <int T, int PARTS>
+__device__ __forceinline__ void store_h(char* to, int plane, int r, v4f v, float up) {
     if constexpr (T == T_F32) {
-        *reinterpret_cast<v4f*>(hi + r * 4) = v;
+        *reinterpret_cast<v4f*>(to + r * 4) = v;
     } else {
-        uint16_t h[4], l[4];
+        uint32_t a[PARTS], b[PARTS];
+        split_pair<T, PARTS>(v[0], v[1], up, a);
+        split_pair<T, PARTS>(v[2], v[3], up, b);
 #pragma unroll
-        for (int e = 0; e < 4; e++) split_element<T>(v[e], up, h[e], l[e]);
-        __builtin_memcpy(hi + r * 2, h, 8);
-        __builtin_memcpy(lo + r * 2, l, 8);
+        for (int i = 0; i < PARTS; i++) *reinterpret_cast<uint2*>(to + i * plane + r * 2) = uint2{a[i], b[i]};
     }
 }
 
@@ -199,15 +193,13 @@ __device__ __forceinline__ u32x4 load_ranks(const typename Elem<T>::type* row, i
     return v;
 }
 
-// A workgroup: a tile of 16 rows and a share of N, 64 columns a wave at a time.  H is rounded to no fewer than 16 bits: for 16-bit types it is the sum
-// of two parts, of bfloat16 cut off and rounded (2^-16 of an element), or of
-// float16 after a power of two for the row that brings its largest element
-// below 2^15 (2^-22, and 2^-39 of that element).  One matrix instruction of a
-// 16-bit type sums over 32: both parts of a rank of up to 16 (PACKED), else one
-// part of 32.  Of ranks up to 64 (float: 32) the next columns'
-// operands are fetched while these are multiplied (HELD); of more ranks there are
-// too many for that (LONG).  For tiles of few rows, bound by reading the adapters
-// (257 rows x 8192, 32 adapters of rank 32, bfloat16: 15 us).
+// A workgroup: a tile of 16 rows and a share of N, 64 columns a wave at a time.  H
+// keeps its float precision on the 16-bit instructions as the sum of three parts.  One
+// such instruction sums over 32: two of four parts of a rank of up to 16 (PACKED), else
+// one part of 32.  Of ranks up to 64 (float: 32) the next columns' operands are fetched
+// while these are multiplied (HELD); of more ranks there are too many for that (LONG).
+// For tiles of few rows, bound by reading the adapters (257 rows x 8192, 32 adapters of
+// rank 32, bfloat16: 15 us).
 template <int T, int KIND, bool ODD>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(T == T_F32 ? 2 : 3))) lora_expand(ExpandArgs a) {
     using E = typename Elem<T>::type;
@@ -218,9 +210,9 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(T == T
     extern __shared__ __attribute__((aligned(16))) char smem[];
     const int rp = expand_ranks(a.R), steps = rp / STEP;
     const int pitch = T == T_F32 ? (rp + 4) * 4 : (rp + 8) * 2;  // bytes
-    char* const hi = smem;
-    char* const lo = smem + TM * pitch;  // 16-bit types
-    float* const factor = reinterpret_cast<float*>(smem + TM * pitch * (T == T_F32 ? 1 : 2));
+    constexpr int PARTS = h_parts<T>(KIND == EXPAND_PACKED);
+    const int plane = TM * pitch;
+    float* const factor = reinterpret_cast<float*>(smem + PARTS * plane);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i = lane & 15, g = lane >> 4;
     const uint2 block = block_of_run();
@@ -304,7 +296,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(T == T
                     // Every lane of the row's sixteen is here.
                     up = half_factor(group_max(top));
                 }
-                if (rq < rp) store_h<T>(hi + p * pitch, lo + p * pitch, rq, v, up);
+                if (rq < rp) store_h<T, PARTS>(smem + p * pitch, plane, rq, v, up);
                 if (a.H && block.y == 0 && in) {
                     float* const h = a.H + row_at(a.rows, tile.start + p) * a.ldh;
 #pragma unroll
@@ -335,14 +327,14 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(T == T
 #pragma unroll
                     for (int h = 0; h < HELD; h++) {
                         const int r = KIND == EXPAND_PACKED ? 8 * (g & 1) : (u + h) * STEP + g * V;
-                        const char* const from = KIND == EXPAND_PACKED && g >= 2 ? lo : hi;
-                        const u32x4 x = *reinterpret_cast<const u32x4*>(from + at + r * int(sizeof(E)));
+                        // PACKED: lanes of the sum's second half have the next part.
+                        constexpr int STRIDE = KIND == EXPAND_PACKED ? 2 : 1;
+                        const char* const from = smem + at + r * int(sizeof(E)) + (KIND == EXPAND_PACKED && g >= 2 ? plane : 0);
 #pragma unroll
-                        for (int q = 0; q < 4; q++) acc[q] = mma16<T>(cur.w[h][q], x, acc[q]);
-                        if constexpr (T != T_F32 && KIND != EXPAND_PACKED) {
-                            const u32x4 y = *reinterpret_cast<const u32x4*>(lo + at + r * 2);
+                        for (int i = 0; i < PARTS; i += STRIDE) {
+                            const u32x4 x = *reinterpret_cast<const u32x4*>(from + i * plane);
 #pragma unroll
-                            for (int q = 0; q < 4; q++) acc[q] = mma16<T>(cur.w[h][q], y, acc[q]);
+                            for (int q = 0; q < 4; q++) acc[q] = mma16<T>(cur.w[h][q], x, acc[q]);
                         }
                     }
                 }
@@ -371,7 +363,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(T == T
 }
 
 // The same for tiles of many rows: a workgroup takes 64 rows and a share of N,
-// each wave 16 of the rows, with their H in registers (in two parts, as above)
+// each wave 16 of the rows, with their H in registers (in parts, as above)
 // for the whole of it.  64 columns of the adapter are staged in LDS for the four
 // waves, up to 64 ranks at a time, while the ones before are multiplied: read
 // from memory by each wave for itself (into registers), they passed through the L1
@@ -453,7 +445,8 @@ lora_expand_tiles(ExpandArgs a) {
             for (int slot = 0; slot < AHEAD; slot++) fetch_base(slot, slot);
         // H: the lane's V ranks of each sum, all planes.
         const int hp = lora_pitch(a.R);
-        u32x4 hi[NS], lo[T == T_F32 || PACKED ? 1 : NS];
+        constexpr int PARTS = h_parts<T>(PACKED), HELD = PACKED ? 2 : PARTS;
+        u32x4 held[NS][HELD];
         float f = s;
         {
             const float* const P = a.P + int64_t(tile.start + (own ? p : 0)) * hp;
@@ -503,15 +496,17 @@ lora_expand_tiles(ExpandArgs a) {
             }
 #pragma unroll
             for (int u = 0; u < NS; u++) {
-                u32x4 h, l = {0, 0, 0, 0};
-                if constexpr (T == T_F32) h = pack<T>(v[u]);
-                else split_h<T>(v[u], up, h, l);
-                if constexpr (PACKED) {
-#pragma unroll
-                    for (int y = 0; y < 4; y++) hi[u][y] = g < 2 ? h[y] : l[y];
+                if constexpr (T == T_F32) {
+                    held[u][0] = pack<T>(v[u]);
                 } else {
-                    hi[u] = h;
-                    if constexpr (T != T_F32) lo[u] = l;
+#pragma unroll
+                    for (int y = 0; y < 4; y++) {
+                        uint32_t p[PARTS];
+                        split_pair<T, PARTS>(v[u][2 * y], v[u][2 * y + 1], up, p);
+#pragma unroll
+                        for (int i = 0; i < HELD; i++)
+                            held[u][i][y] = !PACKED ? p[i] : g < 2 ? p[2 * i] : p[2 * i + 1];
+                    }
                 }
             }
         }
@@ -535,8 +530,8 @@ lora_expand_tiles(ExpandArgs a) {
 #pragma unroll
                     for (int q = 0; q < 4; q++) {
                         const u32x4 x = *reinterpret_cast<const u32x4*>(st + w_row(q) * PITCH + c);
-                        acc[q] = mma16<T>(x, hi[ch * CHUNK + u], acc[q]);
-                        if constexpr (T != T_F32 && !PACKED) acc[q] = mma16<T>(x, lo[ch * CHUNK + u], acc[q]);
+#pragma unroll
+                        for (int i = 0; i < HELD; i++) acc[q] = mma16<T>(x, held[ch * CHUNK + u][i], acc[q]);
                     }
                 }
             }

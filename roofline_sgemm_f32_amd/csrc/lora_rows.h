@@ -130,9 +130,11 @@ __device__ __forceinline__ v4f mma16(u32x4 a, u32x4 b, v4f c) {
     }
 }
 
-// Float factors for the 16-bit instructions: the sum of two parts of the type, of
-// bfloat16 cut off and rounded, of float16 after a power of two that brings the
-// largest of those that share it into [2^14, 2^15).
+// Float factors for the 16-bit instructions: the sum of three parts of the type (four
+// where an instruction has room for them), which is all of a float's 24 bits.  Of
+// bfloat16 each is cut off the rest.  Of float16 they come after a power of two that
+// brings the largest of those that share it into [2^14, 2^15), and are rounded; what
+// float16 cannot hold is below 2^-39 of that largest.
 __device__ __forceinline__ float largest(float top, float v) {  // of the finite
     return fabsf(v) < __builtin_inff() ? fmaxf(top, fabsf(v)) : top;
 }
@@ -143,20 +145,36 @@ __device__ __forceinline__ float half_factor(float top) {
     ex = ex < -100 ? -100 : ex;
     return __uint_as_float(uint32_t(14 - ex + 127) << 23);
 }
-template <int T>
-__device__ __forceinline__ void split_element(float v, float up, uint16_t& h, uint16_t& l) {
-    if constexpr (T == T_F16) {
-        const float x = v * up;
-        const _Float16 top = _Float16(x);
-        h = __builtin_bit_cast(uint16_t, top);
-        l = __builtin_bit_cast(uint16_t, _Float16(fabsf(x) <= 65504.0f ? x - float(top) : 0.0f));
-    } else {
-        const uint32_t cut = __float_as_uint(v) & 0xFFFF0000u;
-        const bool finite = (cut & 0x7F800000u) != 0x7F800000u;
-        // A NaN whose payload is in the cut bits stays one.
-        h = uint16_t(!finite && v != v ? 0x7FC0u : cut >> 16);
-        l = __builtin_bit_cast(uint16_t, __bf16(finite ? v - __uint_as_float(cut) : 0.0f));
+// Two numbers' parts, the first's in the low half of each.
+template <int T, int PARTS>
+__device__ __forceinline__ void split_pair(float a, float b, float up, uint32_t (&part)[PARTS]) {
+    static_assert(PARTS == 3 || PARTS == 4, "the fourth is zero");
+    uint16_t p[2][PARTS] = {};
+    const float v[2] = {a, b};
+#pragma unroll
+    for (int e = 0; e < 2; e++) {
+        if constexpr (T == T_F16) {
+            const float x = v[e] * up;
+            const bool finite = fabsf(x) <= 65504.0f;
+            const _Float16 h = _Float16(x);
+            const float r = finite ? x - float(h) : 0.0f;
+            const _Float16 m = _Float16(r);
+            p[e][0] = __builtin_bit_cast(uint16_t, h);
+            p[e][1] = __builtin_bit_cast(uint16_t, m);
+            p[e][2] = __builtin_bit_cast(uint16_t, _Float16(r - float(m)));
+        } else {
+            const uint32_t cut = __float_as_uint(v[e]) & 0xFFFF0000u;
+            const bool finite = (cut & 0x7F800000u) != 0x7F800000u;
+            const float r = finite ? v[e] - __uint_as_float(cut) : 0.0f;
+            const uint32_t rest = __float_as_uint(r) & 0xFFFF0000u;
+            // A NaN whose payload is in the cut bits stays one.
+            p[e][0] = uint16_t(!finite && v[e] != v[e] ? 0x7FC0u : cut >> 16);
+            p[e][1] = uint16_t(rest >> 16);
+            p[e][2] = uint16_t(__float_as_uint(r - __uint_as_float(rest)) >> 16);
+        }
     }
+#pragma unroll
+    for (int i = 0; i < PARTS; i++) part[i] = p[0][i] | uint32_t(p[1][i]) << 16;
 }
 
 }  // namespace

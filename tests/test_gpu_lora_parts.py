@@ -1,0 +1,122 @@
+"""H and dH of low-rank adapters count in full on the 16-bit matrix instructions:
+to float's own precision."""
+import pytest
+import torch
+
+import roofline_sgemm_f32_amd as rs
+from tests.ff_util import TYPES, U, assert_within, rounded
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    rs.load()
+
+
+# (M, N, K, R, L): one launch for few rows; single rows; tiles of 16 rows (many
+# adapters) and of 64 (few), each with ranks of every form, aligned and odd.
+FORMS = [(3, 70, 40, 8, 2), (40, 700, 96, 40, 5),
+         (100, 130, 72, 8, 40), (100, 72, 200, 12, 40), (90, 200, 136, 32, 30), (100, 264, 72, 64, 40),
+         (90, 70, 300, 67, 30), (100, 130, 72, 200, 40),
+         (200, 130, 72, 8, 2), (200, 72, 200, 12, 2), (150, 200, 136, 32, 1), (200, 264, 72, 40, 2),
+         (300, 72, 300, 67, 3), (200, 136, 72, 128, 1), (200, 130, 72, 200, 2), (140, 70, 40, 255, 1)]
+NAMES = ["x".join(map(str, f)) for f in FORMS]
+
+
+def rows_of(gen, M, L):
+    """An adapter for each row; the first two rows have the first."""
+    ids = torch.randint(0, L, (M,), generator=gen, dtype=torch.int32)
+    ids[:2] = 0
+    return ids
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("form", FORMS, ids=NAMES)
+def test_a_base_that_nearly_cancels(form, t):
+    """One rank is not zero, so that H is one product of 22 bits at most and the
+    sums over ranks add zeros; base is minus the rounded correction, and what is
+    left shows the last bits of H, and of dH."""
+    M, N, K, R, L = form
+    dt = TYPES[t]
+    gen = torch.Generator().manual_seed(FORMS.index(form))
+    ids = rows_of(gen, M, L)
+    r0, k0, n0 = R // 2, K // 3, N // 3
+    X, A, B = torch.zeros((M, K)), torch.zeros((L, R, K)), torch.zeros((L, N, R))
+    X[:, k0] = torch.randn((M,), generator=gen)
+    A[:, r0, k0] = torch.randn((L,), generator=gen)
+    B[:, :, r0] = torch.randn((L, N), generator=gen)
+    X, A, B = X.to(dt), A.to(dt), B.to(dt)
+    scale = 0.5 + torch.rand((L,), generator=gen)
+    of, s = ids.long(), scale.double()[ids.long()][:, None]
+    # In float32 H is rounded; in the 16-bit types it is exact.
+    h = X[:, k0].double()[:, None] * A[of, r0, k0].double()[:, None]
+    d = s * h * B[of, :, r0].double()
+    base = (-d).to(dt)
+    ref = base.double() + d
+    # One product of H with an element of B, its (up to four) parts added, the scale
+    # and base: at most eight roundings of 2 U of |d|.  Of float16, H beside a power of
+    # two for its row, here of one number: nothing more.
+    err = 16 * U * d.abs()
+    Y, H = rs.lora(X.cuda(), A.cuda(), B.cuda(), ids.cuda(), scale=scale.cuda(), base=base.cuda(), save=True)
+    want = torch.zeros((M, R), dtype=torch.float64)
+    want[:, r0] = h[:, 0]
+    assert_within(H, want, 2 * U * want.abs(), "H")
+    assert_within(Y, ref, rounded(ref, err, dt), "Y")
+    # dH = s dY B of one column, dX = base + dH A.
+    dY = torch.zeros((M, N))
+    dY[:, n0] = torch.randn((M,), generator=gen)
+    A2 = torch.zeros((L, R, K))
+    A2[:, r0] = torch.randn((L, K), generator=gen)
+    dY, A2 = dY.to(dt), A2.to(dt)
+    dh = s * dY[:, n0].double()[:, None] * B[of, n0, r0].double()[:, None]
+    d = dh * A2[of, r0].double()
+    base = (-d).to(dt)
+    ref = base.double() + d
+    dX, _, _ = rs.lora_backward(dY.cuda(), X.cuda(), A2.cuda(), B.cuda(), H, ids.cuda(), scale=scale.cuda(),
+                                base=base.cuda(), need_dw=False)
+    assert_within(dX, ref, rounded(ref, 16 * U * d.abs(), dt), "dX")
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("R", [1, 8, 13, 16, 32, 45, 64, 130, 256])
+@pytest.mark.parametrize("M", [2, 70, 1200])
+def test_rows_that_nearly_cancel(M, R, t):
+    """Two rows whose products differ by 2^-14 of themselves; the others are zero."""
+    dt = TYPES[t]
+    gen = torch.Generator().manual_seed(M + R)
+    N, K, r0 = 72, 136, R // 2
+    i, j = (0, 1) if M == 2 else (3, M - 2)
+    scale = torch.tensor([1.2345678, 0.5772157])
+    ids = torch.ones((M,), dtype=torch.int32)
+    x = torch.randn((K,), generator=gen).to(dt)
+    X = torch.zeros((M, K), dtype=dt)
+    X[i], X[j] = x, -x
+    A = torch.zeros((2, R, K), dtype=dt)
+    B = torch.zeros((2, N, R), dtype=dt)
+    dY = torch.zeros((M, N), dtype=dt)
+    B[1, 0, r0], B[1, 1, r0] = 1.0, 2.0 ** -7
+    dY[i, 0] = dY[j, 0] = 1.0
+    dY[j, 1] = 2.0 ** -7
+    H = torch.zeros((M, R))
+    H[i, r0] = scale[1]                       # any number of 24 bits
+    H[j, r0] = -scale[1] * (1 + 2.0 ** -14)
+    _, dA, dB = rs.lora_backward(dY.cuda(), X.cuda(), A.cuda(), B.cuda(), H.cuda(), ids.cuda(), scale=scale.cuda(),
+                                 need_dx=False)
+    s = scale.double()[1]
+    want = torch.zeros((2, R, K), dtype=torch.float64)
+    want[1, r0] = s * -2.0 ** -14 * x.double()
+    mag = s * x.double().abs()
+    err = torch.zeros_like(want)
+    # dH of the two rows: three roundings of 2 U; the parts of each added, and each
+    # other: eight at most.
+    err[1, r0] = 2 * 11 * U * mag
+    assert_within(dA, want, rounded(want, err, dt), "dA")
+    want = torch.zeros((2, N, R), dtype=torch.float64)
+    err = torch.zeros_like(want)
+    want[1, 0, r0] = s * (H[i, r0].double() + H[j, r0].double())
+    want[1, 1, r0] = s * 2.0 ** -7 * H[j, r0].double()
+    err[1, :2, r0] = 2 * 9 * U * torch.tensor([2.0, 2.0 ** -7], dtype=torch.float64) * s * H[j, r0].double().abs()
+    assert_within(dB, want, rounded(want, err, dt), "dB")

@@ -141,11 +141,11 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) l
                     for (int y = 0; y < 4; y += 2) {
                         uint16_t* const at = reinterpret_cast<uint16_t*>(vs) + (r + y) * VP + p;
                         uint32_t part[3];
-                        if constexpr (T == T_F16)  // each rank's power of two
-                            split_pair<T, 3>(v[y] * half_factor(__uint_as_float(top[r + y])),
-                                             v[y + 1] * half_factor(__uint_as_float(top[r + y + 1])), 1.0f, part);
-                        else
-                            split_pair<T, 3>(v[y], v[y + 1], 1.0f, part);
+                        float up[2] = {1.0f, 1.0f};
+                        if constexpr (T == T_F16)
+#pragma unroll
+                            for (int z = 0; z < 2; z++) up[z] = half_factor(__uint_as_float(top[r + y + z]));
+                        split_pair<T, 3>(v[y], v[y + 1], up[0], up[1], part);
 #pragma unroll
                         for (int i = 0; i < 3; i++) {
                             at[i * RN * VP] = uint16_t(part[i]);

@@ -151,8 +151,8 @@ __device__ __forceinline__ void store_h(char* to, int plane, int r, v4f v, float
         *reinterpret_cast<v4f*>(to + r * 4) = v;
     } else {
         uint32_t a[PARTS], b[PARTS];
-        split_pair<T, PARTS>(v[0], v[1], up, a);
-        split_pair<T, PARTS>(v[2], v[3], up, b);
+        split_pair<T, PARTS>(v[0], v[1], up, up, a);
+        split_pair<T, PARTS>(v[2], v[3], up, up, b);
 #pragma unroll
         for (int i = 0; i < PARTS; i++) *reinterpret_cast<uint2*>(to + i * plane + r * 2) = uint2{a[i], b[i]};
     }
@@ -502,10 +502,12 @@ lora_expand_tiles(ExpandArgs a) {
 #pragma unroll
                     for (int y = 0; y < 4; y++) {
                         uint32_t p[PARTS];
-                        split_pair<T, PARTS>(v[u][2 * y], v[u][2 * y + 1], up, p);
+                        split_pair<T, PARTS>(v[u][2 * y], v[u][2 * y + 1], up, up, p);
 #pragma unroll
-                        for (int i = 0; i < HELD; i++)
-                            held[u][i][y] = !PACKED ? p[i] : g < 2 ? p[2 * i] : p[2 * i + 1];
+                        for (int i = 0; i < HELD; i++) {
+                            const uint32_t one = p[PACKED ? 2 * i : i], two = p[PACKED ? 2 * i + 1 : i];
+                            held[u][i][y] = g < 2 ? one : two;
+                        }
                     }
                 }
             }

@@ -132,9 +132,8 @@ __device__ __forceinline__ v4f mma16(u32x4 a, u32x4 b, v4f c) {
 
 // Float factors for the 16-bit instructions: the sum of three parts of the type (four
 // where an instruction has room for them), which is all of a float's 24 bits.  Of
-// bfloat16 each is cut off the rest.  Of float16 they come after a power of two that
-// brings the largest of those that share it into [2^14, 2^15), and are rounded; what
-// float16 cannot hold is below 2^-39 of that largest.
+// float16 they come after a power of two that brings the largest of those that share it
+// into [2^14, 2^15); what float16 cannot hold is below 2^-37 of that largest.
 __device__ __forceinline__ float largest(float top, float v) {  // of the finite
     return fabsf(v) < __builtin_inff() ? fmaxf(top, fabsf(v)) : top;
 }
@@ -145,36 +144,40 @@ __device__ __forceinline__ float half_factor(float top) {
     ex = ex < -100 ? -100 : ex;
     return __uint_as_float(uint32_t(14 - ex + 127) << 23);
 }
-// Two numbers' parts, the first's in the low half of each.
+// Two numbers' parts, the first's in the low half of each.  An infinity in the other
+// operand meets every part, so all have the number's sign, and of a number that is not
+// zero none is zero: each part is cut off the float just below the rest in magnitude,
+// which leaves a rest, and the type's smallest takes the place of a zero.  Of an
+// infinity the last part is one (the others are the largest finite), and of a NaN.
 template <int T, int PARTS>
-__device__ __forceinline__ void split_pair(float a, float b, float up, uint32_t (&part)[PARTS]) {
-    static_assert(PARTS == 3 || PARTS == 4, "the fourth is zero");
-    uint16_t p[2][PARTS] = {};
-    const float v[2] = {a, b};
+__device__ __forceinline__ void split_pair(float a, float b, float up_a, float up_b, uint32_t (&part)[PARTS]) {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    const float v[2] = {a, b}, up[2] = {up_a, up_b};
+    uint32_t one[2];   // 0 for a zero
+    float rest[2];
 #pragma unroll
     for (int e = 0; e < 2; e++) {
-        if constexpr (T == T_F16) {
-            const float x = v[e] * up;
-            const bool finite = fabsf(x) <= 65504.0f;
-            const _Float16 h = _Float16(x);
-            const float r = finite ? x - float(h) : 0.0f;
-            const _Float16 m = _Float16(r);
-            p[e][0] = __builtin_bit_cast(uint16_t, h);
-            p[e][1] = __builtin_bit_cast(uint16_t, m);
-            p[e][2] = __builtin_bit_cast(uint16_t, _Float16(r - float(m)));
-        } else {
-            const uint32_t cut = __float_as_uint(v[e]) & 0xFFFF0000u;
-            const bool finite = (cut & 0x7F800000u) != 0x7F800000u;
-            const float r = finite ? v[e] - __uint_as_float(cut) : 0.0f;
-            const uint32_t rest = __float_as_uint(r) & 0xFFFF0000u;
-            // A NaN whose payload is in the cut bits stays one.
-            p[e][0] = uint16_t(!finite && v[e] != v[e] ? 0x7FC0u : cut >> 16);
-            p[e][1] = uint16_t(rest >> 16);
-            p[e][2] = uint16_t(__float_as_uint(r - __uint_as_float(rest)) >> 16);
-        }
+        const uint32_t bits = __float_as_uint(v[e]) & 0x7FFFFFFFu;
+        one[e] = min(bits, 1u);
+        rest[e] = __uint_as_float(T == T_F16 ? max(__float_as_uint(__uint_as_float(bits) * up[e]), one[e]) : bits);
     }
+    const uint32_t least = one[0] | one[1] << 16;
+    const uint32_t sign = (__float_as_uint(a) >> 16 & 0x8000u) | (__float_as_uint(b) & 0x80000000u);
 #pragma unroll
-    for (int i = 0; i < PARTS; i++) part[i] = p[0][i] | uint32_t(p[1][i]) << 16;
+    for (int i = 0; i < PARTS; i++) {
+        const bool last = i + 1 == PARTS;
+        uint32_t c[2];
+#pragma unroll
+        for (int e = 0; e < 2; e++) c[e] = __float_as_uint(rest[e]) - (last ? 0 : one[e]);
+        uint32_t cut;
+        if constexpr (T == T_F16) cut = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(__uint_as_float(c[0]), __uint_as_float(c[1])));
+        else cut = c[0] >> 16 | (c[1] & 0xFFFF0000u);
+        if (!last) {
+            rest[0] -= T == T_F16 ? float(__builtin_bit_cast(_Float16, uint16_t(cut))) : __uint_as_float(cut << 16);
+            rest[1] -= T == T_F16 ? float(__builtin_bit_cast(_Float16, uint16_t(cut >> 16))) : __uint_as_float(cut & 0xFFFF0000u);
+        }
+        part[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, cut), __builtin_bit_cast(u16x2, least))) | sign;
+    }
 }
 
 }  // namespace

@@ -1,5 +1,7 @@
 """H and dH of low-rank adapters count in full on the 16-bit matrix instructions:
-to float's own precision."""
+to float's own precision, and beside infinities as the formula has it."""
+import math
+
 import pytest
 import torch
 
@@ -120,3 +122,99 @@ def test_rows_that_nearly_cancel(M, R, t):
     want[1, 1, r0] = s * 2.0 ** -7 * H[j, r0].double()
     err[1, :2, r0] = 2 * 9 * U * torch.tensor([2.0, 2.0 ** -7], dtype=torch.float64) * s * H[j, r0].double().abs()
     assert_within(dB, want, rounded(want, err, dt), "dB")
+
+
+def same_kind(got, ref, what):
+    """NaN and infinities where the formula has them, of its sign."""
+    got = got.detach().cpu().double()
+    for name, f in (("NaN", torch.isnan), ("inf", lambda v: v == math.inf), ("-inf", lambda v: v == -math.inf)):
+        bad = f(got) != f(ref)
+        assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} wrong as {name}; first at " \
+                              f"{bad.nonzero()[0].tolist()}: got {float(got[bad][0])}, want {float(ref[bad][0])}"
+
+
+def product(a, b):
+    """a @ b in float64, term by term."""
+    return torch.stack([(r[:, None] * b).sum(0) for r in a]) if len(a) else a @ b
+
+
+@pytest.mark.parametrize("t", TYPES)
+@pytest.mark.parametrize("form", FORMS, ids=NAMES)
+def test_infinities(form, t):
+    """An infinite element of B, A, X or dY: h inf is an infinity of h's sign also
+    where h is a small whole number, whose low bits are zero, and NaN only where the
+    formula has 0 inf or inf - inf."""
+    M, N, K, R, L = form
+    dt, inf = TYPES[t], math.inf
+    gen = torch.Generator().manual_seed(100 + FORMS.index(form))
+    ids = rows_of(gen, M, L)
+    of = ids.long()
+
+    def whole(*shape):
+        return torch.randint(-2, 3, shape, generator=gen).to(dt)
+
+    X, A, B, base = whole(M, K), whole(L, R, K), whole(L, N, R), whole(M, N)
+    for r in range(0, R, 2):  # half of the ranks' H are not whole
+        A[:, r] = (A[:, r].float() * (1 + torch.rand((L, K), generator=gen))).to(dt)
+    scale = torch.ones((L,))
+    scale[-1] = -0.5
+    # Every adapter: an infinity in a row of B of its own rank; in one row of X; in
+    # base, of both signs against B's.
+    for l in range(L):
+        B[l, 3, l % R] = inf
+        B[l, 5, (l + 1) % R] = -inf
+    X[2, K // 2] = inf
+    X[1] = 0                                   # H = 0: 0 inf
+    base[:, 3] = inf
+    base[::2, 9] = -inf
+    h = torch.stack([(A[of[m]].double() * X[m].double()).sum(1) for m in range(M)])
+    d = torch.stack([(B[of[m]].double() * h[m]).sum(1) for m in range(M)]) * scale.double()[of][:, None]
+    Y, H = rs.lora(X.cuda(), A.cuda(), B.cuda(), ids.cuda(), scale=scale.cuda(), base=base.cuda(), save=True)
+    same_kind(H, h, "H")
+    same_kind(Y, base.double() + d, "Y")
+    # Backward: finite H, infinities in dY, X and A (each once for a row or adapter).
+    dY, Hs = whole(M, N), torch.randint(-3, 4, (M, R), generator=gen).float()
+    B, X = whole(L, N, R), whole(M, K)
+    Hs[:, ::2] *= 1 + torch.rand((M, (R + 1) // 2), generator=gen)
+    dY[0, 2] = inf
+    dY[1, 4] = -inf
+    X[2, 5] = inf
+    X[-1, 6] = -inf
+    for l in range(L):
+        A[l, l % R, 7] = inf
+    s = scale.double()[of][:, None]
+    dH = torch.stack([(B[of[m]].double() * dY[m].double()[:, None]).sum(0) for m in range(M)]) * s
+    dXr = torch.stack([(A[of[m]].double() * dH[m][:, None]).sum(0) for m in range(M)])
+    dX, dA, dB = rs.lora_backward(dY.cuda(), X.cuda(), A.cuda(), B.cuda(), Hs.cuda(), ids.cuda(), scale=scale.cuda())
+    same_kind(dX, dXr, "dX")
+    for l in range(L):
+        rows = (of == l).nonzero()[:, 0]
+        if not len(rows):
+            assert not dA[l].any() and not dB[l].any()
+            continue
+        same_kind(dA[l], product(dH[rows].t(), X[rows].double()), f"dA {l}")
+        same_kind(dB[l], product((s[rows] * dY[rows].double()).t(), Hs[rows].double()), f"dB {l}")
+
+
+@pytest.mark.parametrize("M, L", [(100, 40), (200, 1)])
+def test_small_numbers_beside_infinities(M, L):
+    """h inf is an infinity for numbers far below the row's (and the rank's) largest
+    too, whose parts would be zero."""
+    N, K, R = 70, 40, 16
+    gen = torch.Generator().manual_seed(M)
+    ids = rows_of(gen, M, L)
+    X = torch.zeros((M, K), dtype=torch.float16)
+    A = torch.zeros((L, R, K), dtype=torch.float16)
+    B = torch.ones((L, N, R), dtype=torch.float16)
+    X[:, 0], X[:, 1] = 2.0 ** 10, 2.0 ** -20
+    A[:, 0, 0], A[:, 1:, 1] = 2.0 ** 10, 2.0 ** -14
+    B[:, 4, 5] = -math.inf
+    Y = rs.lora(X.cuda(), A.cuda(), B.cuda(), ids.cuda()).cpu()
+    assert bool((Y[:, 4] == -math.inf).all()) and bool((Y[:, 5] == math.inf).all())  # 2^20
+    H = torch.full((M, R), 2.0 ** -30)
+    H[0] = 2.0 ** 10
+    dY = torch.ones((M, N), dtype=torch.float16)
+    dY[1, 6] = math.inf
+    _, _, dB = rs.lora_backward(dY.cuda(), X.cuda(), A.cuda(), B.cuda(), H.cuda(), torch.zeros_like(ids).cuda(),
+                                need_dx=False)
+    assert bool((dB[0, 6] == math.inf).all()) and bool(torch.isfinite(dB[0, :6]).all())

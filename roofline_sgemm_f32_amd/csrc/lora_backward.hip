@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) l
                 const int r = 16 * n + 4 * g + y;
                 if (r0 + r >= a.R) continue;
                 float f = s;
-                if constexpr (T == T_F16) f = s / half_factor(__uint_as_float(top[r]));
+                if constexpr (T == T_F16) f = undone(s, half_factor(__uint_as_float(top[r])));
                 if (slot >= 0) {
                     float* const at = sd.partial + (slot * a.R + r0 + r) * sd.C + c;
 #pragma unroll

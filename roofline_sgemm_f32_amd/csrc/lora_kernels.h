@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(T == T
         }
         if constexpr (T == T_F16) {
             const float up = half_factor(group_max(top));
-            if (c == 0) factor[p] = s / up;
+            if (c == 0) factor[p] = undone(s, up);
         } else {
             if (c == 0) factor[p] = s;
         }
@@ -492,7 +492,7 @@ lora_expand_tiles(ExpandArgs a) {
                         top = largest(top, v[u][e]);
                 top = fmaxf(top, __shfl_xor(top, 16));
                 up = half_factor(fmaxf(top, __shfl_xor(top, 32)));
-                f = s / up;
+                f = undone(s, up);
             }
 #pragma unroll
             for (int u = 0; u < NS; u++) {

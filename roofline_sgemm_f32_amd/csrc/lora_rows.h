@@ -144,6 +144,12 @@ __device__ __forceinline__ float half_factor(float top) {
     ex = ex < -100 ? -100 : ex;
     return __uint_as_float(uint32_t(14 - ex + 127) << 23);
 }
+// The scale with that power undone.  A finite scale's stays finite: a sum of zero is
+// then zero, and any other (2^-48 at least) past float16's range as it should be.
+__device__ __forceinline__ float undone(float s, float up) {
+    const float f = s / up;
+    return fabsf(s) < __builtin_inff() ? fminf(fmaxf(f, -__FLT_MAX__), __FLT_MAX__) : f;
+}
 // Two numbers' parts, the first's in the low half of each.  An infinity in the other
 // operand meets every part, so all have the number's sign, and of a number that is not
 // zero none is zero: each part is cut off the float just below the rest in magnitude,

@@ -218,3 +218,28 @@ def test_small_numbers_beside_infinities(M, L):
     _, _, dB = rs.lora_backward(dY.cuda(), X.cuda(), A.cuda(), B.cuda(), H.cuda(), torch.zeros_like(ids).cuda(),
                                 need_dx=False)
     assert bool((dB[0, 6] == math.inf).all()) and bool(torch.isfinite(dB[0, :6]).all())
+
+
+@pytest.mark.parametrize("M, L", [(3, 1), (100, 40), (200, 1)])
+def test_zero_adapters_with_the_largest_scale(M, L):
+    """A correction of zero times any finite scale is zero: the factor that undoes
+    float16's power of two must not be infinite."""
+    N, K, R = 600, 64, 16
+    gen = torch.Generator().manual_seed(M)
+    ids = rows_of(gen, M, L)
+    X = torch.full((M, K), 2.0 ** 10).half()
+    A = torch.full((L, R, K), 2.0 ** 10).half()
+    B = torch.zeros((L, N, R)).half()
+    base = torch.randn((M, N), generator=gen).half()
+    scale = torch.full((L,), 3e38)
+    args = (X.cuda(), A.cuda(), B.cuda(), ids.cuda())
+    assert torch.equal(rs.lora(*args, scale=scale.cuda(), base=base.cuda()).cpu(), base)
+    B[:, 1] = 1
+    Y = rs.lora(args[0], args[1], B.cuda(), args[3], scale=scale.cuda(), base=base.cuda()).cpu()
+    assert bool((Y[:, 1] == math.inf).all()) and torch.equal(Y[:, 2:], base[:, 2:])
+    # dB from H above 2^15 and dY of zeros.
+    H = torch.full((M, R), 2.0 ** 30)
+    dY = torch.zeros((M, N)).half()
+    _, dA, dB = rs.lora_backward(dY.cuda(), X.cuda(), A.cuda(), B.cuda(), H.cuda(), ids.cuda(), scale=scale.cuda(),
+                                 need_dx=False)
+    assert not dA.any() and not dB.any()

@@ -241,24 +241,21 @@ bool ortho_bounds(int steps, const double* coef, double* bounds) {
         const double a = coef[3 * i], b = coef[3 * i + 1], c = coef[3 * i + 2];
         if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
         bounds[i] = r;
+        // The factor a + b s^2 + c s^4 is stored too.  (Also no square below overflows.)
+        if (!(std::fabs(a) + std::fabs(b) * r * r + std::fabs(c) * std::pow(r, 4) <= 1e9)) return false;
         auto p = [&](double q) { return std::fabs(std::sqrt(q) * (a + q * (b + q * c))); };
         double top = p(r * r);
         const double disc = 9 * b * b - 20 * a * c;
-        double roots[2] = {-1, -1};
-        if (c != 0 && disc >= 0) {
-            roots[0] = (-3 * b + std::sqrt(disc)) / (10 * c);
-            roots[1] = (-3 * b - std::sqrt(disc)) / (10 * c);
-        } else if (c == 0 && b != 0) {
-            roots[0] = -a / (3 * b);
+        if (disc >= 0) {
+            // No difference of nearly equal numbers: a root far smaller than the other
+            // keeps its digits.  Where c or t is zero one is infinite or NaN, and not taken.
+            const double t = -(3 * b + std::copysign(std::sqrt(disc), b)) / 2;
+            for (double q : {t / (5 * c), a / t})
+                if (q > 0 && q < r * r) top = std::max(top, p(q));
         }
-        for (double q : roots)
-            if (q > 0 && q < r * r) top = std::max(top, p(q));
         // Roundings of a step and of its result, counted generously.
         r = top * 1.01;
         if (!(r <= 64.0) || r < 0x1p-40) return false;
-        // The factor a + b s^2 + c s^4 is stored too.
-        if (!(std::fabs(a) + std::fabs(b) * bounds[i] * bounds[i] + std::fabs(c) * std::pow(bounds[i], 4) <= 1e9))
-            return false;
     }
     bounds[steps] = r;
     return true;

@@ -116,7 +116,8 @@ __global__ void __launch_bounds__(256) small_steps(const double* parts, int shar
         trace = v;
     }
     __syncthreads();
-    const double norm = sqrt(trace) + eps, f = norm > 0 ? 1.0 / norm : norm;  // 0 for zeros, NaN stays
+    // 0 for zeros, whatever eps (f^2 may pass the largest double), NaN stays.
+    const double f = trace > 0 ? 1.0 / (sqrt(trace) + eps) : trace;
     for (int e = threadIdx.x; e < SIDE * SIDE; e += 256) S[e / SIDE * LD + e % SIDE] *= f * f;
     // C = A B, waves by blocks; `put` takes each element.
     auto product = [&](const double* A, const double* B, auto put) {

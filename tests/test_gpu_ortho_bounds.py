@@ -1,5 +1,5 @@
 """Orthogonalised updates: coefficients whose largest value on the way is hard to
-see."""
+see, and matrices of zeros with the smallest eps."""
 import pytest
 import torch
 
@@ -27,3 +27,15 @@ def test_a_small_fifth_power(c):
     got = rs.orthogonalize(G.cuda(), coefficients=steps).cpu().double()
     ref = ortho64(G, steps)
     assert float((got - ref).norm()) <= ortho_norm_bound(G, steps) + 2.0 ** -24 * float(ref.norm())
+
+
+@pytest.mark.parametrize("eps", [1e-160, 1e-200, 1e-308, 5e-324, 1e-60])
+@pytest.mark.parametrize("shape", [(16, 40), (40, 30), (64, 200), (1, 1), (70, 80)], ids=lambda s: "x".join(map(str, s)))
+def test_zeros_with_the_smallest_eps(shape, eps):
+    G = torch.zeros((2, *shape), device="cuda")
+    G[1, 0, 0] = 2.0
+    O = rs.orthogonalize(G, eps=eps)
+    assert not O[0].any()
+    ref = ortho64(G[1].cpu(), [rs.MUON] * 5, eps)
+    bound = ortho_norm_bound(G[1].cpu(), [rs.MUON] * 5, eps) + 2.0 ** -24 * float(ref.norm())
+    assert float((O[1].cpu().double() - ref).norm()) <= bound

@@ -133,6 +133,15 @@ int check_alias(const View (&in)[NI], const View (&out)[NO], int n_place = 0, in
     return SGEMM_OK;
 }
 
+// Whether the last input, a workspace, shares memory with another: kernels write it
+// while those are still to be read.
+template <int NI>
+bool workspace_shared(const View (&in)[NI]) {
+    for (int i = 0; i + 1 < NI; i++)
+        if (share(in[i], in[NI - 1])) return true;
+    return false;
+}
+
 constexpr int64_t kDimLimit = int64_t(1) << 40;
 
 bool dims_ok(int64_t a, int64_t b, int64_t c) {
@@ -461,6 +470,7 @@ int sgemm_lora(int type, int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, 
                        {workspace, 1, workspace_bytes, workspace_bytes > 0 ? workspace_bytes : 1, 1}};
     const View out[] = {{Y, M, N, ldy, es}, {H, M, R, ldh, 4}};
     if ((v = check_alias(in, out, 1, 1)) != SGEMM_OK) return v;
+    if (workspace_shared(in)) return SGEMM_ERR_ALIAS;
     if (workspace_bytes < int64_t(sgemm::lora_workspace_bytes(false, type, M, N, K, int(R), int(L))))
         return SGEMM_ERR_SCRATCH;
     if (workspace_bytes > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15))) return SGEMM_ERR_ARG;
@@ -496,6 +506,7 @@ int sgemm_lora_backward(int type, int64_t M, int64_t N, int64_t K, int64_t R, in
     const View out[] = {{dX, M, K, lddx, es}, stack_view(dA, L, stride_da, R, K, ldda, es),
                         stack_view(dB, L, stride_db, N, R, lddb, es)};
     if ((v = check_alias(in, out, 1, 1)) != SGEMM_OK) return v;
+    if (workspace_shared(in)) return SGEMM_ERR_ALIAS;
     if (workspace_bytes < int64_t(sgemm::lora_workspace_bytes(true, type, M, N, K, int(R), int(L))))
         return SGEMM_ERR_SCRATCH;
     if (workspace_bytes > 0 && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15))) return SGEMM_ERR_ARG;

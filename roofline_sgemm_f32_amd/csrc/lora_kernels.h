@@ -199,7 +199,9 @@ __device__ __forceinline__ u32x4 load_ranks(const typename Elem<T>::type* row, i
 // one part of 32.  Of ranks up to 64 (float: 32) the next columns' operands are fetched
 // while these are multiplied (HELD); of more ranks there are too many for that (LONG).
 // For tiles of few rows, bound by reading the adapters (257 rows x 8192, 32 adapters of
-// rank 32, bfloat16: 15 us).
+// rank 32, bfloat16: 15 us).  At three waves a SIMD the 16-bit HELD forms keep 4 to 6
+// registers in memory (ranks that are no multiple of 8: 22), all but two of them
+// outside the loop over columns.
 template <int T, int KIND, bool ODD>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(T == T_F32 ? 2 : 3))) lora_expand(ExpandArgs a) {
     using E = typename Elem<T>::type;
@@ -369,12 +371,14 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(T == T
 // from memory by each wave for itself (into registers), they passed through the L1
 // four times and took as long as base and Y (8192 x 8192 bfloat16 of rank 64: 97 us,
 // staged 80).  A share's workgroups are on as few XCDs as can be, whose L2s then keep
-// that share of the adapters (75 us, 3.6 TB/s of base and Y; of rank 16 8192 x 4096
+// that share of the adapters (77 us, 3.5 TB/s of base and Y; of rank 16 8192 x 4096
 // 38 -> 35).  Waves wait for base most of the time; two turns of it are in flight
 // (four, or the adapter's two turns ahead, are slower).
-// NS: matrix instructions' sums of one part that R takes.
+// NS: matrix instructions' sums of one part that R takes.  Ranks up to 64 of 16-bit
+// types have three waves a SIMD: for four, 20 registers go to memory (4096 x 4096 of
+// rank 64 27 us, 24 with three; 8192 x 8192 the same).
 template <int T, int KIND, int NS, bool ODD>
-__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(T == T_F32 ? (NS <= 2 ? 3 : NS <= 8 ? 2 : 1) : (NS <= 2 ? 4 : NS <= 4 ? 2 : 1))))
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(T == T_F32 ? (NS <= 2 ? 3 : NS <= 8 ? 2 : 1) : (NS <= 1 ? 4 : NS <= 2 ? 3 : NS <= 4 ? 2 : 1))))
 lora_expand_tiles(ExpandArgs a) {
     using E = typename Elem<T>::type;
     constexpr bool PACKED = KIND == EXPAND_PACKED;

@@ -243,3 +243,29 @@ def test_zero_adapters_with_the_largest_scale(M, L):
     _, dA, dB = rs.lora_backward(dY.cuda(), X.cuda(), A.cuda(), B.cuda(), H.cuda(), ids.cuda(), scale=scale.cuda(),
                                  need_dx=False)
     assert not dA.any() and not dB.any()
+
+
+@pytest.mark.parametrize("t", ["f32", "bf16"])
+@pytest.mark.parametrize("M, L, R", [(3, 1, 16), (100, 40, 16), (100, 40, 40), (200, 1, 16), (200, 1, 40)])
+@pytest.mark.parametrize("e", [-100, -120, -126])
+def test_the_smallest_normal_numbers_beside_infinities(e, M, L, R, t):
+    """H = 2^e: what its parts hold is below bfloat16's normal numbers."""
+    N, K, dt = 70, 40, TYPES[t]
+    gen = torch.Generator().manual_seed(M)
+    ids = rows_of(gen, M, L)
+    X, A, B = torch.zeros((M, K)), torch.zeros((L, R, K)), torch.ones((L, N, R))
+    X[:, 0], A[:, :, 0] = 2.0 ** (e // 2), 2.0 ** (e - e // 2)
+    B[:, 4, 5], B[:, 6, 1] = -math.inf, math.inf
+    Y, H = rs.lora(X.to(dt).cuda(), A.to(dt).cuda(), B.to(dt).cuda(), ids.cuda(), save=True)
+    assert bool((H == 2.0 ** e).all())
+    Y = Y.cpu()
+    assert bool((Y[:, 4] == -math.inf).all()) and bool((Y[:, 6] == math.inf).all())
+    # The parts of 2^e in whole numbers of the type's smallest, 2^-133: three roundings.
+    assert_within(Y[:, :4], torch.full((M, 4), R * 2.0 ** e, dtype=torch.float64),
+                  rounded(torch.tensor(R * 2.0 ** e, dtype=torch.float64), R * (3 * 2.0 ** -133 + 2 * (R + 24) * U * 2.0 ** e),
+                          dt).expand(M, 4))
+    dY = torch.ones((M, N))
+    dY[1, 6] = math.inf
+    _, _, dB = rs.lora_backward(dY.to(dt).cuda(), X.to(dt).cuda(), A.to(dt).cuda(), B.to(dt).cuda(), H,
+                                torch.zeros_like(ids).cuda(), need_dx=False)
+    assert bool((dB[0, 6] == math.inf).all()) and bool(torch.isfinite(dB[0, :6]).all())

@@ -370,10 +370,16 @@ int sgemm_q4_glu(int act, int xtype, int stype, int64_t M, int64_t F, int64_t K,
  *   X A^T is formed and kept in float, and so is the sum with base, which is
  * rounded to `type` once.  Nothing is atomic: the result of a call is the same
  * from run to run.  An adapter's zero rank columns change no result, so smaller
- * ranks are padded with zeros.
+ * ranks are padded with zeros.  The second product takes all of H's 24 bits also
+ * on the 16-bit matrix instructions, as a sum of parts of `type` (of float16 in
+ * tiles of rows: what is below 2^-36 of the row's largest is lost).  Infinities
+ * and NaN are as the formula has them, in the rows and adapters that hold them.
  *   Both entry points take scratch memory from the caller: `workspace`, of at
  * least the bytes that sgemm_lora_workspace names for these sizes (0: NULL is
- * fine), 16-byte aligned, which the call's kernels use until they end.  They
+ * fine), 16-byte aligned, which the call's kernels use until they end and which
+ * shares memory with no operand.  A stack of more than one matrix counts as the
+ * whole range from its first element to its last: an output may not lie in the
+ * gaps of another operand's stack, nor an operand in the gaps of its own.  They
  * allocate nothing and never synchronise; every call can be captured. */
 #define SGEMM_LORA_MAX_RANK 256
 #define SGEMM_LORA_MAX_ADAPTERS 4096
@@ -399,7 +405,9 @@ int sgemm_lora(int type, int64_t M, int64_t N, int64_t K, int64_t R, int64_t L, 
  * dX == NULL skips dX; dA == NULL and dB == NULL skip theirs.  dA and dB are
  * written for every adapter (zero where no row has it), laid out like A and B
  * with strides of their own, which must keep the adapters apart.  Sums are in
- * float, in an order that depends on the sizes and ids alone. */
+ * float, in an order that depends on the sizes and ids alone; dH and H enter the
+ * products as H does above (of float16, dA and dB lose what is below 2^-36 of a
+ * rank's largest among up to 512 rows). */
 int sgemm_lora_backward(int type, int64_t M, int64_t N, int64_t K, int64_t R, int64_t L,
                         const void *dY, int64_t lddy, const void *X, int64_t ldx, const void *A,
                         int64_t lda, int64_t stride_a, const void *B, int64_t ldb, int64_t stride_b,
@@ -421,16 +429,23 @@ int sgemm_lora_backward(int type, int64_t M, int64_t N, int64_t K, int64_t R, in
  * whose directions all count alike.  coefficients: 3 * steps doubles in host
  * memory, read before the call returns; steps 1..SGEMM_ORTHO_MAX_STEPS.  G and O
  * are of type `type`; O may be G itself (same strides), else they must not
- * overlap; O's strides must keep the matrices apart.
+ * overlap (a stack counts as the whole range that it spans); O's strides must
+ * keep the matrices apart.  M and N are at most SGEMM_ORTHO_MAX_SIDE, batch at
+ * most SGEMM_ORTHO_MAX_BATCH.
  *   The norm is summed in double.  Matrices with a side of up to 64 are computed
- * in double.  For others X and S are kept between the steps as two float16 parts
- * each, 22 bits, times a power of two, and products are summed in float.  The power comes from a bound of X that follows from the coefficients
- * alone (|X| <= 1 at the start); coefficients that are not finite, let it pass 64
- * or bring it below 2^-40 are SGEMM_ERR_ARG.  A matrix of zeros gives zeros; an infinity or NaN in G
- * makes its matrix's results NaN.
+ * in double.  For others X, S and the factor a I + b S + c S^2 are kept as two
+ * float16 parts each, 22 bits, times a power of two; products leave out the low
+ * parts' own product (2^-22 of a term) and are summed in float.  The power comes
+ * from a bound of X that follows from the coefficients alone (|X| <= 1 at the
+ * start); coefficients that are not finite, let it pass 64 or bring it below
+ * 2^-40, or whose factor's terms pass 10^9, are SGEMM_ERR_ARG.  A matrix of zeros
+ * gives zeros, whatever eps; an infinity or NaN in G makes its matrix's results
+ * NaN.
  *   `workspace`: at least sgemm_orthogonalize_workspace bytes, 256-byte aligned.
  * No allocation, no synchronisation, every call can be captured. */
 #define SGEMM_ORTHO_MAX_STEPS 64
+#define SGEMM_ORTHO_MAX_SIDE 65536
+#define SGEMM_ORTHO_MAX_BATCH 65535
 
 int64_t sgemm_orthogonalize_workspace(int64_t batch, int64_t M, int64_t N);
 

@@ -639,6 +639,7 @@ def lora(X, A, B, ids=None, scale=1.0, base=None, out=None, save=False):
     outside 0..L-1, -1 say, means none: Y[m] = base[m].  None: every row has the
     only adapter.  ``scale`` is a number, or float32 numbers for the adapters.
     ``out`` may be base itself.  Sums are kept in float32 and rounded once.
+    Infinities and NaN are as the formula has them.
     Returns Y, with ``save`` (Y, H): H[m] = X[m] A[l]^T (M x R, float32, zero for
     a row without adapter), which lora_backward takes; ``save`` may also be the
     tensor H to write."""
@@ -717,6 +718,7 @@ def lora_backward(dY, X, A, B, H, ids=None, scale=1.0, base=None, need_dx=True, 
     return dX, dA, dB
 
 
+# The published coefficients of the Muon optimiser's quintic steps (Jordan et al., 2024).
 MUON = (3.4445, -4.7750, 2.0315)
 
 
@@ -728,7 +730,9 @@ def orthogonalize(G, steps=5, coefficients=MUON, eps=1e-7, out=None):
     (3-D), float32, float16 or bfloat16, and so is the result (``out`` when
     given; it may be G itself).  ``coefficients`` is one triple (a, b, c) for
     all ``steps``, or a sequence of triples, one for each step (``steps`` is
-    then not used).  They are refused where they let X grow past 64."""
+    then not used).  They are refused where they let X grow past 64.  A side is at
+    most 65536.  Matrices with a side of more than 64 are kept with 22 bits between
+    the products, which are summed in float32."""
     _FLOATS or _use_torch()
     if not isinstance(G, torch.Tensor) or G.dtype not in _FLOATS:
         raise TypeError(f"G must be a tensor of {' or '.join(str(d) for d in _FLOATS)}")

@@ -232,7 +232,7 @@ bool stack_ok(int64_t n, int64_t stride, int64_t rows, int64_t cols, int64_t ld,
 }
 
 constexpr int64_t kIndexLimit = (int64_t(1) << 31) - 1;
-constexpr int64_t kOrthoLimit = 65536, kOrthoBatch = 65535;
+constexpr int64_t kOrthoLimit = SGEMM_ORTHO_MAX_SIDE, kOrthoBatch = SGEMM_ORTHO_MAX_BATCH;
 
 int validate_lora_sizes(int type, int64_t M, int64_t N, int64_t K, int64_t R, int64_t L) {
     if (type < 0 || type > SGEMM_TYPE_BF16) return SGEMM_ERR_ARG;

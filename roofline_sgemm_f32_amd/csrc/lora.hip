@@ -109,9 +109,10 @@ PassPlan pass_plan(int type, bool ids, bool single, int64_t M, int64_t N, int64_
     p.kshare = K > 0 ? ceil_div(ceil_div(K, planes), kunit) * kunit : 1;
     p.planes = int(K > 0 ? ceil_div(K, p.kshare) : 1);
     const int64_t nunit = p.tmb == 1 ? 256 : 64;
-    // As many workgroups as are resident at a time (lora_expand_tiles by its registers;
-    // 8192 x 8192 bfloat16 of rank 64 78 us, with half as many 98; float 2048 x 4096
-    // of rank 64 24 us, with twice as many 30).
+    // About as many workgroups as are resident at a time (lora_expand_tiles by its
+    // registers: 1024, 768 with the 16-bit types' ranks 33 to 64, 512; 8192 x 8192
+    // bfloat16 of rank 64 77 us, with half as many 98; float 2048 x 4096 of rank 64
+    // 24 us, with twice as many 30).
     const int64_t resident = p.tmb == 1 || R <= 32 || (type != T_F32 && R <= 64) ? 1024 : 512;
     int64_t shares = ceil_div(resident, busy), top = ceil_div(N, nunit);
     shares = shares > top ? top : shares;
@@ -141,10 +142,11 @@ hipError_t launch_expand(int type, const ExpandArgs& a, const PassPlan& p, hipSt
 }
 
 // Whether one launch (lora_few) is better than two: at most 16 workgroups, which each
-// read an adapter's A of at most 128 KiB.  us on the GPU, and with what the host takes
-// to call it from Python (11 against 15 at least): A of 16 KiB 3.8 against 6.8, 64 KiB
-// 5.3 against 6.8, 128 KiB 7.3 against 7.0, 256 KiB 10.9 against 7.9, 512 KiB 19.9
-// against 9.6.
+// read an adapter's A of at most 128 KiB.  Calls in a replayed graph, us, one launch
+// against two: A of 16 KiB 3.8 and 6.0, 64 KiB 5.2 and 6.3, 128 KiB 7.0 to 7.5 and 6.7
+// to 6.9 (8192 x 4096 of rank 8 9.4 and 6.5), 256 KiB 10.9 and 7.3, 512 KiB 19.9 and
+// 8.9.  At 128 KiB the one launch is for calls from a host that each pay for their
+// launches (from Python 11 to 12 against 15); in a graph it loses up to 3 us there.
 bool few_rows(int type, int64_t M, int64_t N, int64_t K, int64_t R) {
     return M * ceil_div(N > 0 ? N : 1, kFewCols) <= 16 && R * K * (type == T_F32 ? 4 : 2) <= 128 * 1024;
 }

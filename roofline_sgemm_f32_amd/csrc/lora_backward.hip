@@ -1,9 +1,11 @@
 // Gradients of low-rank adapters:
 //   dH[m] = s_l dY[m] B_l,  dX[m] = base[m] + dH[m] A_l      (l = ids[m])
 //   dA_l = sum dH[m]^T X[m],  dB_l = s_l sum dY[m]^T H[m]     (over l's rows m)
-// The first two are the forward pass's products with the adapters transposed
-// (a copy of them, small beside the rows).  The others are sums over rows: each
-// chunk of an adapter's rows gives a partial sum, and these are added in order.
+// The first two are the forward pass's products with the adapters transposed: a copy
+// of all of them, whichever have rows.  It is small beside many rows; with few rows of
+// many adapters it is most of the work, as the zeros of the unused dA and dB are.  The
+// others are sums over rows: each chunk of an adapter's rows gives a partial sum, and
+// these are added in order.
 #include "lora.h"
 
 namespace sgemm {
@@ -56,10 +58,12 @@ __device__ __forceinline__ int64_t slot_of(const WeightArgs& a, const RowTile& t
 // power of two for each rank that brings the chunk's largest into [2^14, 2^15).
 // NARROW: fewer columns than a lane's on either side.
 //   Up to rank 16 it is bound by reading X and dY (8192 rows of 4096 + 4096 bfloat16:
-// 134 MB in 30 us, 4.5 TB/s), above by registers: with 64 ranks' sums in them two
-// workgroups fit a CU, too few to hide the loads (4096 rows of 4096 + 4096: 67 MB in
-// 51 us; float, 2048 rows of 4096 + 2048: 50 MB in 35 us).  Loads one batch ahead
-// and other layouts of V in LDS changed nothing there.
+// 134 MB in 31 us, 4.3 TB/s).  Above, the chunks, chosen from M alone, leave the card
+// half empty: 4096 rows of 4096 + 4096 are 256 workgroups, one a CU, where registers
+// allow two (67 MB in 47 us; float, 2048 rows of 4096 + 2048: 50 MB in 35 us).  Loads one
+// batch ahead and other layouts of V in LDS changed nothing there.  With 64 ranks' sums
+// the 16-bit forms keep 48 to 77 registers in memory, of what a chunk begins and ends
+// with: one of them is read in the loop over rows.
 template <int T, int RB, bool NARROW>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) lora_weights(WeightArgs a) {
     using E = typename Elem<T>::type;

@@ -53,7 +53,8 @@ __device__ __forceinline__ int scan(int* v, int n) {
 // Up to kHeld rows' groups and places stay in LDS between the two passes.  The
 // loops are not unrolled and the code is short: it runs once, on one CU, and is
 // fetched from memory first (64 rows 6 us, 1025 rows 7, 8192 rows 12: bound by the
-// latency of one step after another).
+// latency of one step after another; 32768 rows 52, 65536 rows 90 with the copies of
+// lora_prepare: the ids past kHeld are fetched in each pass, 64 a wave at a time).
 __device__ __forceinline__ void group_rows(const GroupArgs& a, int* lds) {
     const int groups = a.L + 1;           // the last: no adapter
     int* const first = lds;               // groups + 1: tiles before a group's
@@ -217,7 +218,9 @@ __global__ void __launch_bounds__(kGroupThreads) lora_prepare(GroupArgs g, TurnA
 }
 
 // Waves that sort, by the tables of all of them and the tiles' prefix sums in what
-// held, place and scan leave of 64 KiB; and these tables' bytes.
+// held, place and scan leave of 64 KiB; and these tables' bytes.  From 3949 adapters
+// on one wave's table passes that, by up to 1.2 KiB (65612 bytes with held, place and
+// scan at 4096): a CU has 160 KiB, and one such workgroup runs.
 size_t group_waves(GroupArgs& a) {
     const int groups = a.L + 1, ints = 7900;
     a.waves = (ints - groups - 1) / groups;

@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(T == T
 // from memory by each wave for itself (into registers), they passed through the L1
 // four times and took as long as base and Y (8192 x 8192 bfloat16 of rank 64: 97 us,
 // staged 80).  A share's workgroups are on as few XCDs as can be, whose L2s then keep
-// that share of the adapters (77 us, 3.5 TB/s of base and Y; of rank 16 8192 x 4096
+// that share of the adapters (77 to 82 us, 3.3 to 3.5 TB/s of base and Y; of rank 16 8192 x 4096
 // 38 -> 35).  Waves wait for base most of the time; two turns of it are in flight
 // (four, or the adapter's two turns ahead, are slower).
 // NS: matrix instructions' sums of one part that R takes.  Ranks up to 64 of 16-bit

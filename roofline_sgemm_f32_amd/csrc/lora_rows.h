@@ -133,7 +133,7 @@ __device__ __forceinline__ v4f mma16(u32x4 a, u32x4 b, v4f c) {
 // Float factors for the 16-bit instructions: the sum of three parts of the type (four
 // where an instruction has room for them), which is all of a float's 24 bits.  Of
 // float16 they come after a power of two that brings the largest of those that share it
-// into [2^14, 2^15); what float16 cannot hold is below 2^-37 of that largest.
+// into [2^14, 2^15); what float16 cannot hold is below 2^-36 of that largest.
 __device__ __forceinline__ float largest(float top, float v) {  // of the finite
     return fabsf(v) < __builtin_inff() ? fmaxf(top, fabsf(v)) : top;
 }

@@ -300,9 +300,9 @@ __device__ __forceinline__ void step_barrier() {
 // pieces are turned by (row / 2) % 8 places, so that sixteen lanes that read the
 // same piece of sixteen rows are on sixteen different bank groups.
 //   Bound by the matrix instructions, whose clock falls under their load: P X of
-// 4096 x 4096 takes 317 us, 1.3 PFLOP/s of float16 instructions (a library's plain
-// float16 product: 1.17), the matrix units 68 % busy at 1.78 GHz; S and P there 199
-// and 203 us.  Halves of a step pipelined across the barrier were slower.
+// 4096 x 4096 takes 316 to 331 us, 1.25 to 1.3 PFLOP/s of float16 instructions (a
+// library's plain float16 product: 1.17), the matrix units 68 % busy at 1.78 GHz; S
+// and P there 193 to 207 us.  Halves of a step pipelined across the barrier were slower.
 template <class CF, int EPI, bool SPLIT>
 __global__ void __launch_bounds__(64 * CF::WAVES) __attribute__((amdgpu_waves_per_eu(CF::OCC)))
 ortho_product(ProductArgs a) {

@@ -5,7 +5,8 @@
 //   O = (P_last ... P_0) G / (|G| + eps),    |G|^2 = the trace of G G^T.
 // Three launches, G read twice: 16 matrices of 16 x 4096 float take 5, 9 and 5 us,
 // bound by the launches and by small_steps' chain of products in one workgroup (4.2
-// MB of G: 0.9 us; sixteen launches of steps on tiles would take 80).  S loses what
+// MB of G: 0.9 us; sixteen launches of steps on tiles would take 80).  16 of 32 x 4096
+// take 9, 21 and 11 us, of 64 x 4096 24, 90 and 35: there the chain is most of it.  S loses what
 // is below its own rounding, and each step multiplies that by up to a^2, so this is
 // done in double throughout: the double matrix instruction (16 x 16, sums of 4),
 // whose work is small here (16 x 4096: 2 MFLOP a matrix).  Its operands: lane l holds
